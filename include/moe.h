@@ -79,6 +79,7 @@ typedef enum {
   MOE_DTYPE_F32 = 0,
   MOE_DTYPE_BF16 = 1,
   MOE_DTYPE_FP8_E4M3 = 2, /* OCP FP8 E4M3 codes (moe_quantize_fp8, moe_grouped_gemm_fp8) */
+  MOE_DTYPE_MXFP4 = 3,    /* E2M1 codes with E8M0 scales (moe_quantize_mxfp4) */
   MOE_DTYPE_ENUM_MIN_ = -0x7fffffff - 1,
   MOE_DTYPE_ENUM_MAX_ = 0x7fffffff
 } moe_dtype_t;
@@ -307,6 +308,108 @@ moe_status_t moe_grouped_gemm_fp8(moe_gemm_op_t op, const uint8_t* a, float a_sc
                                   hipStream_t stream);
 
 /*
+ * MXFP4 expert weights: 4-bit codes with a scale for every 32 weights, read
+ * by products with bf16 activations (decoding is bound by the bytes of the
+ * weights; these take 17/32 byte each).
+ *   Source: [A2A] review of torch_moe.py: the quantized MoE ops run the same
+ *   routed template with 4-bit expert linears; the format is the OCP
+ *   microscaling specification's MXFP4.
+ *   - codes are E2M1, s ee m: value (-1)^s times 0, 0.5, 1, 1.5, 2, 3, 4, 6;
+ *     two a byte, the weight with the even index in the low four bits;
+ *   - 32 consecutive weights of a row (along the contraction) share one E8M0
+ *     scale byte b: 2^(b - 127), 255 = NaN. Rows are whole groups: a matrix
+ *     [N, Kd] has codes [N, Kd/2] and scales [N, Kd/32], Kd % 32 == 0.
+ *
+ * moe_quantize_mxfp4 -- w[i] of w_dt (MOE_DTYPE_BF16 or MOE_DTYPE_F32), n
+ * values, n % 32 == 0, to codes [n/2] and scale [n/32]. A group's scale is
+ * b = max(floor(log2 amax) - 2 + 127, 0), amax its largest magnitude; a code
+ * is the E2M1 value nearest to w * 2^(127 - b), ties to the even code,
+ * magnitudes above 6 to 6. A group with a NaN or an infinity gets scale 255.
+ * moe_dequantize_mxfp4 -- the weights that codes and scales stand for, exact
+ * in both output types up to their range.
+ * w, codes, scale: 16-byte aligned; n < 2^40.
+ */
+moe_status_t moe_quantize_mxfp4(const void* w, moe_dtype_t w_dt, int64_t n, uint8_t* codes,
+                                uint8_t* scale, hipStream_t stream);
+moe_status_t moe_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scale, int64_t n, void* w,
+                                  moe_dtype_t w_dt, hipStream_t stream);
+
+/*
+ * moe_grouped_gemm_mxfp4 -- moe_grouped_gemm with MXFP4 weights.
+ * a: bf16 [rows, H] (gate/up) or [rows, I] (down); w: codes [S, 2I, H/2] or
+ * [S, H, I/2]; w_scale: [S, 2I, H/32] or [S, H, I/32]. c: bf16, or f32 for
+ * the down product (c_dt). H % 32 == 0 and I % 32 == 0. Products are exact
+ * (a code times its scale is a bf16 value), sums f32, one rounding to c_dt;
+ * the order of the sums depends on max_rows, S and the shape, not on the
+ * scheduling. A weight whose scale byte is 255 makes its outputs NaN. The
+ * other rules are those of moe_grouped_gemm; w_scale is 16-byte aligned.
+ */
+moe_status_t moe_grouped_gemm_mxfp4(moe_gemm_op_t op, const void* a, const int32_t* offsets,
+                                    int S, int max_rows, const uint8_t* w,
+                                    const uint8_t* w_scale, int H, int I, void* c,
+                                    moe_dtype_t c_dt, hipStream_t stream);
+
+/*
+ * moe_rms_norm -- root-mean-square norm of the layer's input, with the
+ * residual's addition and an output in codes for the FP8 experts.
+ *   h = x + residual in f32 (residual NULL: h = x); residual_out = round(h);
+ *   v = h / sqrt(mean(h^2) + eps) * gamma;  y = round(v);
+ *   q = quantize(v, q_scale) as moe_quantize_fp8 does, from the unrounded v.
+ * x, residual, residual_out, y [T, H] and gamma [H] of dt (f32 or bf16); q
+ * codes [T, H]. residual_out, y and q may be NULL, but not all three of them.
+ * residual_out may be x or residual itself, and y may be x; no other overlap.
+ * q's consumer is moe_forward with x_codes and a1_scale = q_scale, or
+ * moe_grouped_gemm_fp8. H % 8 == 0, H <= 32768; eps finite and >= 0; q_scale
+ * finite and > 0 where q is given; 16-byte aligned pointers. h must be finite
+ * and the sum of its squares below 2^128; a row with others has unspecified
+ * outputs (a NaN stays NaN in y).
+ */
+moe_status_t moe_rms_norm(const void* x, const void* residual, const void* gamma, moe_dtype_t dt,
+                          int T, int H, float eps, void* residual_out, void* y, uint8_t* q,
+                          float q_scale, hipStream_t stream);
+
+/*
+ * moe_balance_loss -- the router's balance loss with its per-expert counts.
+ *   Source: [EPMASK] module docstring (the global top-k ids every rank
+ *   computes are what the counts count); [SLOTS] Description (per-expert load
+ *   is what decides which experts get a second slot).
+ *   p_t = softmax(logits_t); n = number of valid tokens;
+ *   counts[e] = number of pairs (t, k) of valid tokens with ids[t, k] == e;
+ *   prob[e] = sum of p_te over the valid tokens / n;
+ *   loss = coef * E * sum_e counts[e] / (n K) * prob[e].
+ * logits [T, E] f32, ids [T, K] int32 (of any routing rule; ids outside
+ * [0, E) count nowhere; an id that a token holds twice counts twice),
+ * token_mask [T] uint8 or NULL (0: the token is padding, its logits and ids
+ * have no influence whatever they hold). counts [E + 1] int32, counts[E] = n;
+ * prob [E] f32; loss one f32. With no valid token counts, prob and loss are 0.
+ * Logits of -inf have probability 0 (a row of only -inf: all 0); NaN and +inf
+ * in a valid row give NaN. Sums are f32 in a fixed order, f64 over blocks.
+ * Limits as moe_route. ws: 16-byte aligned, at least
+ * moe_balance_loss_workspace_size(T, E, K) bytes, contents ignored.
+ *
+ * moe_route_backward -- gradient of the routing weights and of the balance
+ * loss with respect to the logits:
+ *   dlogits = d(weights)^T dw + dloss * d(loss)
+ * weights: those of moe_route (or moe_route_grouped) for these ids: softmax
+ * probabilities, or with renormalize their share of the K selected ones; dw
+ * [T, K] f32 (NULL: no such term). loss: that of moe_balance_loss with these
+ * counts (its output; NULL: no such term) and coef; counts are constants of
+ * the gradient; dloss one f32 on the device (NULL: 1).
+ * ids outside [0, E) select nothing; an id held twice adds twice. Rows of
+ * masked tokens are zero whatever logits, ids and dw hold there. dlogits
+ * [T, E] f32, written whole; it must not overlap the inputs.
+ * MOE_ERR_INVALID_ARG where both dw and counts are NULL and T > 0.
+ */
+size_t moe_balance_loss_workspace_size(int T, int E, int K);
+moe_status_t moe_balance_loss(const float* logits, const int32_t* ids, const uint8_t* token_mask,
+                              int T, int E, int K, float coef, int32_t* counts, float* prob,
+                              float* loss, void* ws, size_t ws_bytes, hipStream_t stream);
+moe_status_t moe_route_backward(const float* logits, const int32_t* ids, const float* dw,
+                                const uint8_t* token_mask, const int32_t* counts,
+                                const float* dloss, int T, int E, int K, int renormalize,
+                                float coef, float* dlogits, hipStream_t stream);
+
+/*
  * moe_combine -- weighted sum back into token order.
  *   Source: [AUTOTP] the routed output is the weighted sum of the selected
  *   experts' outputs, completed before the single reduction of the layer;
@@ -372,6 +475,8 @@ typedef struct {
                            n > 0: at most n blocks, leaving the other compute units to work
                            queued on other streams (for instance a collective running beside
                            the layer). The output does not depend on it. Negative: error. */
+  int x_codes;          /* dtype MOE_DTYPE_FP8_E4M3: x holds E4M3 codes of scale a1_scale (the q
+                           of moe_rms_norm) instead of bf16; 0 for every other dtype */
 } moe_config_t;
 
 /* Stage boundaries at which moe_forward records the caller's events. */
@@ -399,6 +504,8 @@ typedef struct {
   const void* shared_out;   /* [T, H] dtype or NULL: shared-expert output added in the combine */
   const float* w_gate_up_scale; /* dtype MOE_DTYPE_FP8_E4M3: [S] scales of w_gate_up */
   const float* w_down_scale;    /* dtype MOE_DTYPE_FP8_E4M3: [S] scales of w_down */
+  const uint8_t* w_gate_up_e8m0; /* dtype MOE_DTYPE_MXFP4: [S, 2I, H/32] scales of w_gate_up */
+  const uint8_t* w_down_e8m0;    /* dtype MOE_DTYPE_MXFP4: [S, H, I/32] scales of w_down */
 } moe_forward_args_t;
 
 /*
@@ -424,7 +531,13 @@ typedef struct {
  * the grouped GEMMs are moe_grouped_gemm_fp8 with the SwiGLU output
  * quantized with cfg->a2_scale, and the expert outputs are bf16. H and I
  * must be multiples of 128 and at least 256; routing_on_input is not
- * supported with FP8 (MOE_ERR_UNSUPPORTED).
+ * supported with FP8 (MOE_ERR_UNSUPPORTED). With cfg->x_codes x already holds
+ * the codes and is read as they are; shared_out stays bf16.
+ * cfg->dtype == MOE_DTYPE_MXFP4: x (and shared_out) are bf16; w_gate_up and
+ * w_down are codes [S, 2I, H/2] and [S, H, I/2] with the scales
+ * args->w_gate_up_e8m0 and args->w_down_e8m0; the products are
+ * moe_grouped_gemm_mxfp4 with the SwiGLU output in bf16 and the expert
+ * outputs in f32. H % 32 == 0 and I % 32 == 0; cfg->gemm_blocks has no effect.
  */
 size_t moe_forward_workspace_size(const moe_config_t* cfg);
 moe_status_t moe_forward(const moe_config_t* cfg, const moe_forward_args_t* args, void* ws,

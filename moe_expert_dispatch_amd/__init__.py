@@ -25,6 +25,8 @@ __all__ = [
     "grouped_gemm", "combine",
     "forward", "forward_workspace_size", "ForwardConfig",
     "a2a_dispatch", "a2a_dispatch_workspace_size", "a2a_combine",
+    "rms_norm", "balance_loss", "balance_loss_workspace_size", "route_backward",
+    "MXFP4", "quantize_mxfp4", "dequantize_mxfp4", "grouped_gemm_mxfp4",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -35,6 +37,7 @@ _LIB_FILE = os.environ.get("MOE_HIP_LIBRARY") or os.path.join(_HERE, "libmoe_hip
 MOE_DTYPE_F32 = 0
 MOE_DTYPE_BF16 = 1
 MOE_DTYPE_FP8_E4M3 = 2
+MOE_DTYPE_MXFP4 = 3
 GATE_UP_SWIGLU = 0
 DOWN = 1
 NUM_EVENTS = 6
@@ -43,7 +46,9 @@ MAX_TOPK = 32
 MAX_SLOTS = 1024
 
 _DT = {torch.float32: MOE_DTYPE_F32, torch.bfloat16: MOE_DTYPE_BF16,
-       torch.float8_e4m3fn: MOE_DTYPE_FP8_E4M3}
+       torch.float8_e4m3fn: MOE_DTYPE_FP8_E4M3, torch.float4_e2m1fn_x2: MOE_DTYPE_MXFP4}
+MXFP4 = torch.float4_e2m1fn_x2  # ForwardConfig dtype of the 4-bit expert path
+MX_GROUP = 32  # weights that share one scale byte
 FP8 = torch.float8_e4m3fn  # ForwardConfig dtype of the FP8 expert path
 _CODES = (torch.uint8, torch.float8_e4m3fn)  # tensors holding E4M3 codes
 _TORCH_DT = {MOE_DTYPE_F32: torch.float32, MOE_DTYPE_BF16: torch.bfloat16}
@@ -59,14 +64,15 @@ class _Config(ctypes.Structure):
                 ("dtype", _i), ("out_dtype", _i), ("accumulate", _i),
                 ("num_expert_group", _i), ("topk_group", _i), ("routing_on_input", _i),
                 ("a1_scale", ctypes.c_float), ("a2_scale", ctypes.c_float),
-                ("gemm_blocks", _i)]
+                ("gemm_blocks", _i), ("x_codes", _i)]
 
 
 class _ForwardArgs(ctypes.Structure):
     _fields_ = [("x", _p), ("logits", _p), ("topk_ids", _p), ("topk_w", _p),
                 ("w_gate_up", _p), ("w_down", _p), ("rep_off", _p), ("rep_slots", _p),
                 ("out", _p), ("events", _p * NUM_EVENTS), ("shared_out", _p),
-                ("w_gate_up_scale", _p), ("w_down_scale", _p)]
+                ("w_gate_up_scale", _p), ("w_down_scale", _p),
+                ("w_gate_up_e8m0", _p), ("w_down_e8m0", _p)]
 
 
 _SIGS = {
@@ -91,6 +97,13 @@ _SIGS = {
     "moe_quantize_fp8": (_i, [_p, _i, ctypes.c_int64, ctypes.c_float, _p, _p]),
     "moe_grouped_gemm_fp8": (_i, [_i, _p, ctypes.c_float, _p, _i, _i, _p, _p, _i, _i, _p,
                                   ctypes.c_float, _p]),
+    "moe_quantize_mxfp4": (_i, [_p, _i, ctypes.c_int64, _p, _p, _p]),
+    "moe_dequantize_mxfp4": (_i, [_p, _p, ctypes.c_int64, _p, _i, _p]),
+    "moe_grouped_gemm_mxfp4": (_i, [_i, _p, _p, _i, _i, _p, _p, _i, _i, _p, _i, _p]),
+    "moe_rms_norm": (_i, [_p, _p, _p, _i, _i, _i, ctypes.c_float, _p, _p, _p, ctypes.c_float, _p]),
+    "moe_balance_loss_workspace_size": (_sz, [_i, _i, _i]),
+    "moe_balance_loss": (_i, [_p, _p, _p, _i, _i, _i, ctypes.c_float, _p, _p, _p, _p, _sz, _p]),
+    "moe_route_backward": (_i, [_p, _p, _p, _p, _p, _p, _i, _i, _i, _i, ctypes.c_float, _p, _p]),
 }
 EXPORTED_SYMBOLS = tuple(_SIGS)
 
@@ -153,6 +166,14 @@ def _dev(t: torch.Tensor, name: str, dtype=None, shape=None) -> torch.Tensor:
 
 def _empty(shape, dtype, like: torch.Tensor) -> torch.Tensor:
     return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _on(t: torch.Tensor, *others: Optional[torch.Tensor]):
+    """A context in which t's device is the current one; the others have to be on it too."""
+    for o in others:
+        if o is not None and o.device != t.device:
+            raise ValueError(f"tensors on {t.device} and {o.device}: one device is needed")
+    return torch.cuda.device(t.device)
 
 
 # ---------------------------------------------------------------- stages
@@ -352,6 +373,188 @@ def grouped_gemm_fp8(op: int, a: torch.Tensor, a_scale: float, offsets: torch.Te
     return c
 
 
+def _mx_shape(w: torch.Tensor, name: str) -> Tuple[int, ...]:
+    if w.dim() < 1 or w.shape[-1] % MX_GROUP != 0:
+        raise ValueError(f"{name}: the last size must be a multiple of {MX_GROUP}, "
+                         f"got {tuple(w.shape)}")
+    return tuple(w.shape[:-1])
+
+
+def quantize_mxfp4(w: torch.Tensor, codes: Optional[torch.Tensor] = None,
+                   scale: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """moe_quantize_mxfp4: w [..., K] (bf16 or f32, K % 32 == 0) -> (codes [..., K/2] uint8,
+    scale [..., K/32] uint8)."""
+    _dev(w, "w", (torch.float32, torch.bfloat16))
+    lead, K = _mx_shape(w, "w"), w.shape[-1]
+    codes = (_empty((*lead, K // 2), torch.uint8, w) if codes is None
+             else _dev(codes, "codes", torch.uint8, (*lead, K // 2)))
+    scale = (_empty((*lead, K // MX_GROUP), torch.uint8, w) if scale is None
+             else _dev(scale, "scale", torch.uint8, (*lead, K // MX_GROUP)))
+    with _on(w, codes, scale):
+        _check(lib().moe_quantize_mxfp4(_ptr(w), _DT[w.dtype], w.numel(), _ptr(codes),
+                                        _ptr(scale), _stream()), "moe_quantize_mxfp4")
+    return codes, scale
+
+
+def dequantize_mxfp4(codes: torch.Tensor, scale: torch.Tensor,
+                     dtype: torch.dtype = torch.bfloat16,
+                     out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """moe_dequantize_mxfp4: the weights [..., K] (bf16 or f32) that codes [..., K/2] and
+    scale [..., K/32] stand for."""
+    _dev(codes, "codes", torch.uint8)
+    if codes.dim() < 1 or (2 * codes.shape[-1]) % MX_GROUP != 0:
+        raise ValueError(f"codes must be whole groups of {MX_GROUP // 2} bytes a row")
+    lead, K = tuple(codes.shape[:-1]), 2 * codes.shape[-1]
+    _dev(scale, "scale", torch.uint8, (*lead, K // MX_GROUP))
+    if out is None:
+        if dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError(f"dtype {dtype}, expected torch.float32 or torch.bfloat16")
+        out = _empty((*lead, K), dtype, codes)
+    else:
+        _dev(out, "out", (torch.float32, torch.bfloat16), (*lead, K))
+    with _on(codes, scale, out):
+        _check(lib().moe_dequantize_mxfp4(_ptr(codes), _ptr(scale), out.numel(), _ptr(out),
+                                          _DT[out.dtype], _stream()), "moe_dequantize_mxfp4")
+    return out
+
+
+def grouped_gemm_mxfp4(op: int, a: torch.Tensor, offsets: torch.Tensor, w: torch.Tensor,
+                       w_scale: torch.Tensor, c: Optional[torch.Tensor] = None,
+                       c_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """moe_grouped_gemm_mxfp4. GATE_UP_SWIGLU: a bf16 [rows, H], w codes [S, 2I, H/2], w_scale
+    [S, 2I, H/32] -> bf16 [rows, I]. DOWN: a bf16 [rows, I], w [S, H, I/2], w_scale
+    [S, H, I/32] -> [rows, H] of c_dtype (bf16 or f32)."""
+    _dev(a, "a", torch.bfloat16)
+    _dev(w, "w", torch.uint8)
+    _dev(offsets, "offsets", torch.int32)
+    if a.dim() != 2 or w.dim() != 3:
+        raise ValueError("a must be 2-D and w 3-D")
+    S, N, half = w.shape
+    rows, Kd = a.shape
+    if offsets.numel() != S + 1:
+        raise ValueError("offsets must have S + 1 entries")
+    if 2 * half != Kd:
+        raise ValueError(f"w rows hold {2 * half} codes, a rows {Kd} values")
+    if op == GATE_UP_SWIGLU:
+        if N % 2:
+            raise ValueError("w must be [S, 2I, H/2]")
+        H, I, cols, kinds = Kd, N // 2, N // 2, (torch.bfloat16,)
+    elif op == DOWN:
+        H, I, cols, kinds = N, Kd, N, (torch.bfloat16, torch.float32)
+    else:
+        raise ValueError("op must be GATE_UP_SWIGLU or DOWN")
+    _dev(w_scale, "w_scale", torch.uint8, (S, N, Kd // MX_GROUP))
+    if c is None:
+        if c_dtype not in kinds:
+            raise TypeError(f"c_dtype {c_dtype}, expected one of {kinds}")
+        c = _empty((rows, cols), c_dtype, a)
+    else:
+        _dev(c, "c", kinds, (rows, cols))
+    with _on(a, offsets, w, w_scale, c):
+        _check(lib().moe_grouped_gemm_mxfp4(op, _ptr(a), _ptr(offsets), S, rows, _ptr(w),
+                                            _ptr(w_scale), H, I, _ptr(c), _DT[c.dtype],
+                                            _stream()), "moe_grouped_gemm_mxfp4")
+    return c
+
+
+# ---------------------------------------------------------------- before the layer
+def rms_norm(x: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-6,
+             residual: Optional[torch.Tensor] = None, q_scale: Optional[float] = None,
+             y: Optional[torch.Tensor] = None, residual_out: Optional[torch.Tensor] = None,
+             q: Optional[torch.Tensor] = None
+             ) -> Tuple[torch.Tensor, Optional[torch.Tensor], Optional[torch.Tensor]]:
+    """moe_rms_norm -> (y [T, H], residual_out [T, H] or None, q codes [T, H] uint8 or None).
+
+    x [T, H], gamma [H] and residual [T, H] of one dtype (bf16 or f32). residual_out is x +
+    residual (only with a residual; pass x or residual itself to update it in place), q the E4M3
+    codes of the norm at q_scale (only with a q_scale)."""
+    _dev(x, "x", (torch.float32, torch.bfloat16))
+    if x.dim() != 2:
+        raise ValueError("x must be [T, H]")
+    T, H = x.shape
+    _dev(gamma, "gamma", x.dtype, (H,))
+    if residual is not None:
+        _dev(residual, "residual", x.dtype, (T, H))
+        residual_out = (torch.empty_like(x) if residual_out is None
+                        else _dev(residual_out, "residual_out", x.dtype, (T, H)))
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    if q_scale is not None:
+        q = (_empty((T, H), torch.uint8, x) if q is None else _dev(q, "q", _CODES, (T, H)))
+    elif q is not None:
+        raise ValueError("q needs a q_scale")
+    y = torch.empty_like(x) if y is None else _dev(y, "y", x.dtype, (T, H))
+    with _on(x, gamma, residual, residual_out, y, q):
+        _check(lib().moe_rms_norm(_ptr(x), _ptr(residual), _ptr(gamma), _DT[x.dtype], T, H,
+                                  float(eps), _ptr(residual_out), _ptr(y), _ptr(q),
+                                  0.0 if q_scale is None else float(q_scale), _stream()),
+               "moe_rms_norm")
+    return y, residual_out, q
+
+
+# ---------------------------------------------------------------- the router's training step
+def _router_inputs(logits, ids, token_mask) -> Tuple[int, int, int]:
+    _dev(logits, "logits", torch.float32)
+    _dev(ids, "ids", torch.int32)
+    if logits.dim() != 2 or ids.dim() != 2 or ids.shape[0] != logits.shape[0]:
+        raise ValueError("logits must be [T, E] and ids [T, K]")
+    T, E = logits.shape
+    if token_mask is not None:
+        _dev(token_mask, "token_mask", (torch.uint8, torch.bool), (T,))
+    return T, E, ids.shape[1]
+
+
+def balance_loss_workspace_size(T: int, E: int, K: int) -> int:
+    return int(lib().moe_balance_loss_workspace_size(T, E, K))
+
+
+def balance_loss(logits: torch.Tensor, ids: torch.Tensor, coef: float,
+                 token_mask: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None
+                 ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """moe_balance_loss: logits [T, E] f32, ids [T, K] int32, token_mask [T] (uint8 or bool, 0 =
+    padding) -> (loss f32 scalar, counts [E+1] int32 with the number of valid tokens last,
+    prob [E] f32)."""
+    T, E, K = _router_inputs(logits, ids, token_mask)
+    counts = _empty((E + 1,), torch.int32, logits)
+    prob = _empty((E,), torch.float32, logits)
+    loss = _empty((), torch.float32, logits)
+    if ws is None:
+        ws = _empty((max(balance_loss_workspace_size(T, E, K), 1),), torch.uint8, logits)
+    with _on(logits, ids, token_mask, ws):
+        _check(lib().moe_balance_loss(_ptr(logits), _ptr(ids), _ptr(token_mask), T, E, K,
+                                      float(coef), _ptr(counts), _ptr(prob), _ptr(loss),
+                                      _ptr(ws), ws.numel() * ws.element_size(), _stream()),
+               "moe_balance_loss")
+    return loss, counts, prob
+
+
+def route_backward(logits: torch.Tensor, ids: torch.Tensor, dw: Optional[torch.Tensor],
+                   renormalize: bool, counts: Optional[torch.Tensor] = None, coef: float = 0.0,
+                   dloss: Optional[torch.Tensor] = None,
+                   token_mask: Optional[torch.Tensor] = None,
+                   dlogits: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """moe_route_backward: dlogits [T, E] f32 of the routing weights' gradient dw [T, K] f32
+    (None: no such term) plus that of balance_loss, whose counts and coef are given (counts
+    None: no such term), times dloss (one f32 on the device, None: 1)."""
+    T, E, K = _router_inputs(logits, ids, token_mask)
+    if dw is not None:
+        _dev(dw, "dw", torch.float32, (T, K))
+    if counts is not None:
+        _dev(counts, "counts", torch.int32, (E + 1,))
+    if dloss is not None:
+        _dev(dloss, "dloss", torch.float32)
+        if dloss.numel() != 1:
+            raise ValueError("dloss must hold one value")
+    dlogits = (torch.empty_like(logits) if dlogits is None
+               else _dev(dlogits, "dlogits", torch.float32, (T, E)))
+    with _on(logits, ids, dw, counts, dloss, token_mask, dlogits):
+        _check(lib().moe_route_backward(_ptr(logits), _ptr(ids), _ptr(dw), _ptr(token_mask),
+                                        _ptr(counts), _ptr(dloss), T, E, K,
+                                        int(bool(renormalize)), float(coef), _ptr(dlogits),
+                                        _stream()), "moe_route_backward")
+    return dlogits
+
+
 def combine(y: torch.Tensor, pair_row: torch.Tensor, w_masked: Optional[torch.Tensor], K: int,
             out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
             accumulate: bool = False, shared: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -399,24 +602,25 @@ class ForwardConfig:
                  ep_size: int = 1, ep_rank: int = 0, accumulate: bool = False,
                  T_max: Optional[int] = None, num_expert_group: int = 0, topk_group: int = 0,
                  routing_on_input: bool = False, a1_scale: float = 1.0, a2_scale: float = 1.0,
-                 gemm_blocks: int = 0):
+                 gemm_blocks: int = 0, x_codes: bool = False):
         self.T, self.H, self.I, self.E_global, self.K = T, H, I, E_global, K
         self.renormalize, self.S, self.dtype = bool(renormalize), S, dtype
-        # FP8 (dtype FP8): x, shared_out and the default out are bf16
-        self.out_dtype = out_dtype or (torch.bfloat16 if dtype == FP8 else dtype)
+        # FP8 and MXFP4: x, shared_out and the default out are bf16
+        self.out_dtype = out_dtype or (torch.bfloat16 if dtype in (FP8, MXFP4) else dtype)
         self.a1_scale, self.a2_scale = float(a1_scale), float(a2_scale)
         self.ep_size, self.ep_rank, self.accumulate = ep_size, ep_rank, bool(accumulate)
         self.T_max = T if T_max is None else T_max
         self.num_expert_group, self.topk_group = num_expert_group, topk_group
         self.routing_on_input = bool(routing_on_input)
         self.gemm_blocks = int(gemm_blocks)  # 0: one persistent GEMM block per compute unit
+        self.x_codes = bool(x_codes)  # FP8: x holds E4M3 codes at a1_scale (rms_norm's q)
 
     def c_struct(self) -> _Config:
         return _Config(self.T_max, self.T, self.H, self.I, self.E_global, self.K,
                        int(self.renormalize), self.ep_size, self.ep_rank, self.S,
                        _DT[self.dtype], _DT[self.out_dtype], int(self.accumulate),
                        self.num_expert_group, self.topk_group, int(self.routing_on_input),
-                       self.a1_scale, self.a2_scale, self.gemm_blocks)
+                       self.a1_scale, self.a2_scale, self.gemm_blocks, int(self.x_codes))
 
 
 def forward_workspace_size(cfg: ForwardConfig) -> int:
@@ -440,14 +644,20 @@ def forward(cfg: ForwardConfig, x: torch.Tensor, w_gate_up: torch.Tensor, w_down
     `events`: up to NUM_EVENTS raw hipEvent_t handles (0 = skip) recorded at the
     stage boundaries. cfg.dtype FP8: x is bf16, the weights are E4M3 codes
     (uint8 or float8_e4m3fn) with f32 per-slot scales w_gate_up_scale,
-    w_down_scale [S]."""
+    w_down_scale [S]; with cfg.x_codes x holds codes too (rms_norm's q).
+    cfg.dtype MXFP4: x is bf16, the weights are codes [S, 2I, H/2], [S, H, I/2]
+    and scales [S, 2I, H/32], [S, H, I/32], all uint8 (quantize_mxfp4)."""
     T, H, I, S = cfg.T, cfg.H, cfg.I, cfg.S
-    fp8 = cfg.dtype == FP8
-    xdt = torch.bfloat16 if fp8 else cfg.dtype
-    wdt = _CODES if fp8 else cfg.dtype
-    _dev(x, "x", xdt, (T, H))
-    _dev(w_gate_up, "w_gate_up", wdt, (S, 2 * I, H))
-    _dev(w_down, "w_down", wdt, (S, H, I))
+    fp8, mx = cfg.dtype == FP8, cfg.dtype == MXFP4
+    xdt = torch.bfloat16 if fp8 or mx else cfg.dtype
+    wdt = _CODES if fp8 else torch.uint8 if mx else cfg.dtype
+    pack = 2 if mx else 1  # weights in an element
+    _dev(x, "x", _CODES if fp8 and cfg.x_codes else xdt, (T, H))
+    _dev(w_gate_up, "w_gate_up", wdt, (S, 2 * I, H // pack))
+    _dev(w_down, "w_down", wdt, (S, H, I // pack))
+    if mx:
+        _dev(w_gate_up_scale, "w_gate_up_scale", torch.uint8, (S, 2 * I, H // MX_GROUP))
+        _dev(w_down_scale, "w_down_scale", torch.uint8, (S, H, I // MX_GROUP))
     if fp8:
         _dev(w_gate_up_scale, "w_gate_up_scale", torch.float32, (S,))
         _dev(w_down_scale, "w_down_scale", torch.float32, (S,))
@@ -476,7 +686,10 @@ def forward(cfg: ForwardConfig, x: torch.Tensor, w_gate_up: torch.Tensor, w_down
         _dev(shared_out, "shared_out", xdt, (T, H))
     args = _ForwardArgs(_ptr(x), _ptr(logits), _ptr(topk_ids), _ptr(topk_w), _ptr(w_gate_up),
                         _ptr(w_down), _ptr(rep_off), _ptr(rep_slots), _ptr(out), ev,
-                        _ptr(shared_out), _ptr(w_gate_up_scale), _ptr(w_down_scale))
+                        _ptr(shared_out), None if mx else _ptr(w_gate_up_scale),
+                        None if mx else _ptr(w_down_scale),
+                        _ptr(w_gate_up_scale) if mx else None,
+                        _ptr(w_down_scale) if mx else None)
     c = cfg.c_struct()
     _check(lib().moe_forward(ctypes.byref(c), ctypes.byref(args), _ptr(ws),
                              ws.numel() * ws.element_size(), _stream()), "moe_forward")

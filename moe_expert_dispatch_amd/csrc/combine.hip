@@ -16,9 +16,12 @@
 #include <algorithm>
 
 #include "common.h"
+#include "vec8.h"
 
 namespace moe {
 namespace {
+
+using moe::load8;  // beside the forms below that load through a resource
 
 typedef int int32x4_t __attribute__((ext_vector_type(4)));
 constexpr int kNonTemporal = 2;
@@ -58,37 +61,6 @@ __device__ __forceinline__ void load8(__amdgpu_buffer_rsrc_t r, uint32_t off, co
     v[i] = __int_as_float(a[i]);
     v[4 + i] = __int_as_float(b[i]);
   }
-}
-
-__device__ __forceinline__ void load8(const uint16_t* p, float* v) {
-  const uint4 q = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = bf16_to_f32(w[i] & 0xffffu);
-    v[2 * i + 1] = bf16_to_f32(w[i] >> 16);
-  }
-}
-
-__device__ __forceinline__ void load8(const float* p, float* v) {
-  const float4 a = *reinterpret_cast<const float4*>(p);
-  const float4 b = *reinterpret_cast<const float4*>(p + 4);
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-
-__device__ __forceinline__ void store8(uint16_t* p, const float* v) {
-  uint4 q;
-  q.x = pack_bf16x2(v[0], v[1]);
-  q.y = pack_bf16x2(v[2], v[3]);
-  q.z = pack_bf16x2(v[4], v[5]);
-  q.w = pack_bf16x2(v[6], v[7]);
-  *reinterpret_cast<uint4*>(p) = q;
-}
-
-__device__ __forceinline__ void store8(float* p, const float* v) {
-  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-  *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
 }
 
 // One block per token. Each thread owns kVec vectors of 8 elements. The K

@@ -354,6 +354,39 @@ moe_status_t launch_gemm_fp8_gate_up_gathered(const uint8_t* xq, int T, int K,
 moe_status_t launch_quantize_fp8(const void* x, bool x_bf16, int64_t n, float scale, uint8_t* q,
                                  hipStream_t stream);
 
+// MXFP4 expert weights (E2M1 codes, an E8M0 scale for 32 of them). n is a
+// multiple of 32.
+moe_status_t launch_quantize_mxfp4(const void* w, bool bf16, int64_t n, uint8_t* codes,
+                                   uint8_t* scale, hipStream_t stream);
+moe_status_t launch_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scale, int64_t n,
+                                     void* w, bool bf16, hipStream_t stream);
+// Grouped products with MXFP4 weights and bf16 rows a. sorted_pairs non-null
+// (gate/up only): row r is a[sorted_pairs[r] / topk]. c is bf16, or f32 for
+// the down product with c_f32.
+moe_status_t launch_gemm_mxfp4(moe_gemm_op_t op, const void* a, const int32_t* sorted_pairs,
+                               int topk, const int32_t* offsets, int S, int max_rows,
+                               const uint8_t* w, const uint8_t* w_scale, int H, int I, void* c,
+                               bool c_f32, hipStream_t stream);
+
+constexpr int kMaxNormWidth = 32768;
+// h = x + residual (null: x), the norm of h times gamma as y (dtype of x)
+// and as E4M3 codes; null outputs are not written.
+moe_status_t launch_rms_norm(const void* x, const void* residual, const void* gamma, bool bf16,
+                             int T, int H, float eps, void* residual_out, void* y, uint8_t* q,
+                             float scale, hipStream_t stream);
+
+// Balance loss with counts [E + 1] and mean probabilities [E]; the gradient
+// of routing weights and loss. Null token_mask: every token is valid.
+size_t balance_workspace_bytes(int T, int E, int K);
+moe_status_t launch_balance_loss(const float* logits, const int32_t* ids,
+                                 const uint8_t* token_mask, int T, int E, int K, float coef,
+                                 int32_t* counts, float* prob, float* loss, void* ws,
+                                 hipStream_t stream);
+moe_status_t launch_route_backward(const float* logits, const int32_t* ids, const float* dw,
+                                   const uint8_t* token_mask, const int32_t* counts,
+                                   const float* dloss, int T, int E, int K, int renorm,
+                                   float coef, float* dlogits, hipStream_t stream);
+
 // All-to-all dispatch workspace (carved in this order, 256-byte aligned).
 struct A2aLayout {
   size_t bits, hist, total;  // per-token rank masks, per-chunk rank counts

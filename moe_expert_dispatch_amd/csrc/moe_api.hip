@@ -27,9 +27,12 @@ constexpr size_t kAlign = 256;
 size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 
 bool dtype_ok(moe_dtype_t dt) { return dt == MOE_DTYPE_F32 || dt == MOE_DTYPE_BF16; }
+// Bytes of an activation (MXFP4: bf16 activations).
 int dtype_bytes(moe_dtype_t dt) {
   return dt == MOE_DTYPE_F32 ? 4 : dt == MOE_DTYPE_FP8_E4M3 ? 1 : 2;
 }
+// Bytes of a weight for the weight-panel limit (MXFP4: rounded up).
+int weight_bytes(moe_dtype_t dt) { return dt == MOE_DTYPE_MXFP4 ? 1 : dtype_bytes(dt); }
 bool scale_ok(float s) { return s > 0.0f && s <= 3.4e38f; }  // finite, positive (false for NaN)
 
 // T * K and T * K * max(H, I) must stay addressable with 32-bit row indices.
@@ -129,7 +132,9 @@ ForwardLayout forward_layout(const moe_config_t* c) {
   const size_t P = (size_t)c->T_max * c->K;
   const bool fp8 = c->dtype == MOE_DTYPE_FP8_E4M3;
   const size_t eb = dtype_bytes(c->dtype);
-  const size_t yb = fp8 ? 2 : eb;  // FP8: the expert outputs are bf16
+  // FP8: the expert outputs are bf16; MXFP4: f32 (a rounding less than bf16,
+  // and the products that leave them are bound by their weights)
+  const size_t yb = fp8 ? 2 : c->dtype == MOE_DTYPE_MXFP4 ? 4 : eb;
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t o = off;
@@ -147,7 +152,7 @@ ForwardLayout forward_layout(const moe_config_t* c) {
   L.perm_ws = take(permute_plan(c->T_max, c->K, c->S).ws_bytes);
   L.x_perm = take(P * c->H * yb);  // later reused for the down-projection output
   L.act = take(P * c->I * eb);
-  L.xq = take(fp8 ? (size_t)c->T_max * c->H : 0);  // FP8: the quantized input
+  L.xq = take(fp8 && !c->x_codes ? (size_t)c->T_max * c->H : 0);  // FP8: the quantized input
   L.total = off;
   return L;
 }
@@ -172,6 +177,25 @@ moe_status_t check_a2a_dispatch(const void* x, moe_dtype_t dt, int T, int H, int
   return MOE_OK;
 }
 
+// n values in whole groups of 32.
+moe_status_t check_mxfp4(const void* w, moe_dtype_t w_dt, int64_t n, const uint8_t* codes,
+                         const uint8_t* scale) {
+  if (n < 0) return MOE_ERR_INVALID_ARG;
+  if (!dtype_ok(w_dt) || n % 32 != 0 || n >= (1LL << 40)) return MOE_ERR_UNSUPPORTED;
+  if (n > 0 && (!w || !codes || !scale || !aligned16(w) || !aligned16(codes) ||
+                !aligned16(scale)))
+    return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+// Sizes of the balance loss and the router's backward pass (those of check_route).
+moe_status_t check_router_grad(int T, int E, int K) {
+  if (T < 0 || E < 1 || K < 1 || K > E) return MOE_ERR_INVALID_ARG;
+  if (E > MOE_MAX_EXPERTS || K > MOE_MAX_TOPK) return MOE_ERR_UNSUPPORTED;
+  if (!pairs_fit(T, K) || (long long)T * E >= (1LL << 40)) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
 // Group-limited routing: 1 <= topk_groups <= num_groups <= 64, E divisible
 // by num_groups, and the kept groups hold at least K experts.
 moe_status_t check_groups(int E, int K, int num_groups, int topk_groups) {
@@ -191,7 +215,10 @@ moe_status_t check_config(const moe_config_t* c) {
     return MOE_ERR_INVALID_ARG;
   if (c->S < c->E_global / c->ep_size) return MOE_ERR_INVALID_ARG;
   const bool fp8 = c->dtype == MOE_DTYPE_FP8_E4M3;
-  if ((!dtype_ok(c->dtype) && !fp8) || !dtype_ok(c->out_dtype)) return MOE_ERR_UNSUPPORTED;
+  const bool mx = c->dtype == MOE_DTYPE_MXFP4;
+  if ((!dtype_ok(c->dtype) && !fp8 && !mx) || !dtype_ok(c->out_dtype)) return MOE_ERR_UNSUPPORTED;
+  if (c->x_codes && !fp8) return MOE_ERR_INVALID_ARG;
+  if (mx && (c->H % 32 != 0 || c->I % 32 != 0)) return MOE_ERR_UNSUPPORTED;
   if (fp8 && (!scale_ok(c->a1_scale) || !scale_ok(c->a2_scale))) return MOE_ERR_INVALID_ARG;
   if (fp8 && (c->routing_on_input || !gemm_fp8_ok(c->H) || !gemm_fp8_ok(c->I) ||
               !gemm_fp8_gather_ok(c->T_max, c->H)))
@@ -199,7 +226,7 @@ moe_status_t check_config(const moe_config_t* c) {
   if (c->E_global > MOE_MAX_EXPERTS || c->K > MOE_MAX_TOPK || c->S > MOE_MAX_SLOTS)
     return MOE_ERR_UNSUPPORTED;
   if (c->H % 8 != 0 || c->I % 8 != 0 || !pairs_fit(c->T_max, c->K)) return MOE_ERR_UNSUPPORTED;
-  if (!weight_panel_ok(c->H, c->I, dtype_bytes(c->dtype))) return MOE_ERR_UNSUPPORTED;
+  if (!weight_panel_ok(c->H, c->I, weight_bytes(c->dtype))) return MOE_ERR_UNSUPPORTED;
   if (c->gemm_blocks < 0) return MOE_ERR_INVALID_ARG;
   const long long P = (long long)c->T_max * c->K;
   if (P * (c->H > c->I ? c->H : c->I) >= (1LL << 40)) return MOE_ERR_UNSUPPORTED;
@@ -357,6 +384,10 @@ moe_status_t moe_forward(const moe_config_t* cfg, const moe_forward_args_t* args
     if (args->shared_out && !aligned16(args->shared_out)) return MOE_ERR_INVALID_ARG;
     if (cfg->dtype == MOE_DTYPE_FP8_E4M3 && (!args->w_gate_up_scale || !args->w_down_scale))
       return MOE_ERR_INVALID_ARG;
+    if (cfg->dtype == MOE_DTYPE_MXFP4 &&
+        (!args->w_gate_up_e8m0 || !args->w_down_e8m0 || !aligned16(args->w_gate_up_e8m0) ||
+         !aligned16(args->w_down_e8m0)))
+      return MOE_ERR_INVALID_ARG;
   }
   const ForwardLayout L = forward_layout(cfg);
   if (!ws || ws_bytes < L.total) return MOE_ERR_WORKSPACE;
@@ -374,9 +405,12 @@ moe_status_t moe_forward(const moe_config_t* cfg, const moe_forward_args_t* args
   void* perm_ws = base + L.perm_ws;
   void* x_perm = base + L.x_perm;
   void* act = base + L.act;
-  uint8_t* xq = reinterpret_cast<uint8_t*>(base + L.xq);
-  void* y = x_perm;  // grouped GEMM 1 has consumed x_perm when GEMM 2 writes
   const bool fp8 = cfg->dtype == MOE_DTYPE_FP8_E4M3;
+  const bool mx = cfg->dtype == MOE_DTYPE_MXFP4;
+  const bool quant = fp8 && !cfg->x_codes;  // x is quantized here
+  uint8_t* xq_ws = reinterpret_cast<uint8_t*>(base + L.xq);
+  const uint8_t* xq = quant ? xq_ws : static_cast<const uint8_t*>(args->x);
+  void* y = x_perm;  // grouped GEMM 1 has consumed x_perm when GEMM 2 writes
   const int gb = cfg->gemm_blocks;  // persistent GEMM grid cap (0: one block per CU)
 
   auto mark = [&](int ev) -> moe_status_t {
@@ -409,19 +443,24 @@ moe_status_t moe_forward(const moe_config_t* cfg, const moe_forward_args_t* args
   const bool on_input = cfg->routing_on_input != 0;
   // FP8: x is quantized once per token and GEMM 1 gathers the code rows.
   const bool fused_gather =
-      fp8 || (!on_input && cfg->dtype == MOE_DTYPE_BF16 && gemm_bf16_gather_ok(T, H));
+      fp8 || (!on_input && (mx || (cfg->dtype == MOE_DTYPE_BF16 && gemm_bf16_gather_ok(T, H))));
   // FP8: x is quantized by extra blocks of the permutation's scatter launch
   const FusedQuant fq{static_cast<const uint16_t*>(args->x), (int64_t)T * H,
-                      1.0f / cfg->a1_scale, xq};
+                      1.0f / cfg->a1_scale, xq_ws};
   MOE_TRY(launch_permute(args->x, fp8 ? 2 : dtype_bytes(cfg->dtype), T, H, K, slot, mask, S,
                          offsets, sorted_pairs, pair_row, fused_gather ? nullptr : x_perm,
                          perm_ws, stream, on_input ? w_masked : nullptr,
-                         fp8 ? &fq : nullptr));
+                         quant ? &fq : nullptr));
   MOE_TRY(mark(MOE_EV_PERMUTED));
   if (fp8)
     MOE_TRY(launch_gemm_fp8_gate_up_gathered(
         xq, T, K, sorted_pairs, offsets, S, T * K, static_cast<const uint8_t*>(args->w_gate_up),
         args->w_gate_up_scale, cfg->a1_scale, H, I, act, cfg->a2_scale, stream, gb));
+  else if (mx)
+    MOE_TRY(launch_gemm_mxfp4(MOE_GEMM_GATE_UP_SWIGLU, fused_gather ? args->x : x_perm,
+                              fused_gather ? sorted_pairs : nullptr, K, offsets, S, T * K,
+                              static_cast<const uint8_t*>(args->w_gate_up), args->w_gate_up_e8m0,
+                              H, I, act, false, stream));
   else if (fused_gather)
     MOE_TRY(launch_gemm_bf16_gate_up_gathered(args->x, T, K, sorted_pairs, offsets, S, T * K,
                                               args->w_gate_up, H, I, act, stream, gb));
@@ -433,13 +472,18 @@ moe_status_t moe_forward(const moe_config_t* cfg, const moe_forward_args_t* args
     MOE_TRY(launch_gemm_fp8(MOE_GEMM_DOWN, static_cast<const uint8_t*>(act), cfg->a2_scale,
                             offsets, S, T * K, static_cast<const uint8_t*>(args->w_down),
                             args->w_down_scale, H, I, y, 1.0f, stream, gb));
+  else if (mx)
+    MOE_TRY(launch_gemm_mxfp4(MOE_GEMM_DOWN, act, nullptr, 1, offsets, S, T * K,
+                              static_cast<const uint8_t*>(args->w_down), args->w_down_e8m0, H, I,
+                              y, true, stream));
   else
     MOE_TRY(launch_gemm(MOE_GEMM_DOWN, cfg->dtype, act, offsets, S, T * K, args->w_down, H, I,
                         y, stream, gb));
   MOE_TRY(mark(MOE_EV_DOWN));
-  const moe_dtype_t ydt = fp8 ? MOE_DTYPE_BF16 : cfg->dtype;
+  const moe_dtype_t ydt = fp8 ? MOE_DTYPE_BF16 : mx ? MOE_DTYPE_F32 : cfg->dtype;
   MOE_TRY(launch_combine(y, ydt, pair_row, on_input ? nullptr : w_masked, T, K, H, args->out,
-                         cfg->out_dtype, cfg->accumulate, stream, args->shared_out, ydt));
+                         cfg->out_dtype, cfg->accumulate, stream, args->shared_out,
+                         mx ? MOE_DTYPE_BF16 : ydt));
   MOE_TRY(mark(MOE_EV_COMBINED));
 #undef MOE_TRY
   return MOE_OK;
@@ -469,6 +513,78 @@ moe_status_t moe_grouped_gemm_fp8(moe_gemm_op_t op, const uint8_t* a, float a_sc
   if (!gemm_fp8_ok(op == MOE_GEMM_GATE_UP_SWIGLU ? H : I)) return MOE_ERR_UNSUPPORTED;
   return launch_gemm_fp8(op, a, a_scale, offsets, S, max_rows, w, w_scale, H, I, c, c_scale,
                          stream);
+}
+
+moe_status_t moe_quantize_mxfp4(const void* w, moe_dtype_t w_dt, int64_t n, uint8_t* codes,
+                                uint8_t* scale, hipStream_t stream) {
+  const moe_status_t st = check_mxfp4(w, w_dt, n, codes, scale);
+  if (st != MOE_OK || n == 0) return st;
+  return launch_quantize_mxfp4(w, w_dt == MOE_DTYPE_BF16, n, codes, scale, stream);
+}
+
+moe_status_t moe_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scale, int64_t n, void* w,
+                                  moe_dtype_t w_dt, hipStream_t stream) {
+  const moe_status_t st = check_mxfp4(w, w_dt, n, codes, scale);
+  if (st != MOE_OK || n == 0) return st;
+  return launch_dequantize_mxfp4(codes, scale, n, w, w_dt == MOE_DTYPE_BF16, stream);
+}
+
+moe_status_t moe_grouped_gemm_mxfp4(moe_gemm_op_t op, const void* a, const int32_t* offsets,
+                                    int S, int max_rows, const uint8_t* w,
+                                    const uint8_t* w_scale, int H, int I, void* c,
+                                    moe_dtype_t c_dt, hipStream_t stream) {
+  const moe_status_t st =
+      check_gemm(op, MOE_DTYPE_BF16, a, offsets, S, max_rows, w, H, I, c, 1);
+  if (st != MOE_OK) return st;
+  if (H % 32 != 0 || I % 32 != 0 || !dtype_ok(c_dt)) return MOE_ERR_UNSUPPORTED;
+  if (op == MOE_GEMM_GATE_UP_SWIGLU && c_dt != MOE_DTYPE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (max_rows > 0 && (!w_scale || !aligned16(w_scale))) return MOE_ERR_INVALID_ARG;
+  return launch_gemm_mxfp4(op, a, nullptr, 1, offsets, S, max_rows, w, w_scale, H, I, c,
+                           c_dt == MOE_DTYPE_F32, stream);
+}
+
+moe_status_t moe_rms_norm(const void* x, const void* residual, const void* gamma, moe_dtype_t dt,
+                          int T, int H, float eps, void* residual_out, void* y, uint8_t* q,
+                          float q_scale, hipStream_t stream) {
+  if (T < 0 || H < 1 || !(eps >= 0.0f && eps <= 3.4e38f)) return MOE_ERR_INVALID_ARG;
+  if (!dtype_ok(dt) || H % 8 != 0 || H > kMaxNormWidth) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!x || !gamma || (!residual_out && !y && !q)) return MOE_ERR_INVALID_ARG;
+  if (q && !scale_ok(q_scale)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(residual) || !aligned16(gamma) || !aligned16(residual_out) ||
+      !aligned16(y) || !aligned16(q))
+    return MOE_ERR_INVALID_ARG;
+  return launch_rms_norm(x, residual, gamma, dt == MOE_DTYPE_BF16, T, H, eps, residual_out, y, q,
+                         q_scale, stream);
+}
+
+size_t moe_balance_loss_workspace_size(int T, int E, int K) {
+  if (check_router_grad(T, E, K) != MOE_OK) return 0;
+  return balance_workspace_bytes(T, E, K);
+}
+
+moe_status_t moe_balance_loss(const float* logits, const int32_t* ids, const uint8_t* token_mask,
+                              int T, int E, int K, float coef, int32_t* counts, float* prob,
+                              float* loss, void* ws, size_t ws_bytes, hipStream_t stream) {
+  const moe_status_t st = check_router_grad(T, E, K);
+  if (st != MOE_OK) return st;
+  if (!counts || !prob || !loss || (T > 0 && (!logits || !ids))) return MOE_ERR_INVALID_ARG;
+  if (!ws || ws_bytes < balance_workspace_bytes(T, E, K)) return MOE_ERR_WORKSPACE;
+  if (!aligned16(ws)) return MOE_ERR_INVALID_ARG;
+  return launch_balance_loss(logits, ids, token_mask, T, E, K, coef, counts, prob, loss, ws,
+                             stream);
+}
+
+moe_status_t moe_route_backward(const float* logits, const int32_t* ids, const float* dw,
+                                const uint8_t* token_mask, const int32_t* counts,
+                                const float* dloss, int T, int E, int K, int renormalize,
+                                float coef, float* dlogits, hipStream_t stream) {
+  const moe_status_t st = check_router_grad(T, E, K);
+  if (st != MOE_OK) return st;
+  if (T > 0 && !dw && !counts) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (!logits || !dlogits || (dw && !ids))) return MOE_ERR_INVALID_ARG;
+  return launch_route_backward(logits, ids, dw, token_mask, counts, dloss, T, E, K,
+                               renormalize ? 1 : 0, coef, dlogits, stream);
 }
 
 size_t moe_a2a_dispatch_workspace_size(int T, int ep_size, int cap) {

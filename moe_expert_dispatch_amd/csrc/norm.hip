@@ -1,0 +1,106 @@
+// Root-mean-square norm with the residual's addition, and an output in E4M3
+// codes for the FP8 experts.
+//
+//   h = x + residual (f32), residual_out = round(h)
+//   v = h / sqrt(mean(h^2) + eps) * gamma
+//   y = round(v), q = quantize(v, scale)   (the rule of moe_quantize_fp8)
+//
+// One block per row. Every thread keeps its VPT vectors of 8 values in f32
+// registers from the load to the stores, so the row is read once and both
+// outputs come from the unrounded v. The sum of squares is f32: per thread,
+// then per wave, then over the waves in order, so it does not depend on
+// scheduling.
+#include "common.h"
+#include "vec8.h"
+
+namespace moe {
+namespace {
+
+template <typename XT, int VPT>
+__global__ __launch_bounds__(1024) void rms_norm_kernel(
+    const XT* x, const XT* residual, const XT* __restrict__ gamma, int H, float eps,
+    XT* residual_out, XT* y, uint8_t* __restrict__ q, float inv) {
+  __shared__ float part[16];
+  const int nvec = H / 8;
+  const size_t row = (size_t)blockIdx.x * H;
+  float h[VPT][8];
+  float ss = 0.f;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int v = threadIdx.x + j * blockDim.x;
+    if (v < nvec) {
+      load8(x + row + v * 8, h[j]);
+      if (residual != nullptr) {
+        float r[8];
+        load8(residual + row + v * 8, r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[j][i] += r[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss = fmaf(h[j][i], h[j][i], ss);
+    }
+  }
+  ss = wave_sum(ss);
+  if (lane_id() == 0) part[threadIdx.x / kWave] = ss;
+  __syncthreads();
+  float total = 0.f;
+  for (int w = 0; w < (int)(blockDim.x / kWave); ++w) total += part[w];
+  const float r = 1.0f / sqrtf(total / (float)H + eps);
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int v = threadIdx.x + j * blockDim.x;
+    if (v < nvec) {
+      if (residual_out != nullptr) store8(residual_out + row + v * 8, h[j]);
+      float g[8];
+      load8(gamma + v * 8, g);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) g[i] = h[j][i] * r * g[i];
+      if (y != nullptr) store8(y + row + v * 8, g);
+      if (q != nullptr) {
+        uint2 c;
+        c.x = fp8_q4(g[0], g[1], g[2], g[3], inv);
+        c.y = fp8_q4(g[4], g[5], g[6], g[7], inv);
+        *reinterpret_cast<uint2*>(q + row + v * 8) = c;
+      }
+    }
+  }
+}
+
+template <typename XT, int VPT>
+void launch_v(const void* x, const void* residual, const void* gamma, int T, int H, float eps,
+              void* residual_out, void* y, uint8_t* q, float inv, hipStream_t stream) {
+  const int threads = ceil_div(ceil_div(H / 8, VPT), kWave) * kWave;
+  rms_norm_kernel<XT, VPT><<<T, threads, 0, stream>>>(
+      static_cast<const XT*>(x), static_cast<const XT*>(residual),
+      static_cast<const XT*>(gamma), H, eps, static_cast<XT*>(residual_out),
+      static_cast<XT*>(y), q, inv);
+}
+
+template <typename XT>
+void launch_typed(const void* x, const void* residual, const void* gamma, int T, int H,
+                  float eps, void* residual_out, void* y, uint8_t* q, float inv,
+                  hipStream_t stream) {
+  const int nvec = H / 8;
+  if (nvec <= 1024)
+    launch_v<XT, 1>(x, residual, gamma, T, H, eps, residual_out, y, q, inv, stream);
+  else if (nvec <= 2048)
+    launch_v<XT, 2>(x, residual, gamma, T, H, eps, residual_out, y, q, inv, stream);
+  else
+    launch_v<XT, 4>(x, residual, gamma, T, H, eps, residual_out, y, q, inv, stream);
+}
+
+}  // namespace
+
+moe_status_t launch_rms_norm(const void* x, const void* residual, const void* gamma, bool bf16,
+                             int T, int H, float eps, void* residual_out, void* y, uint8_t* q,
+                             float scale, hipStream_t stream) {
+  if (T == 0) return MOE_OK;
+  const float inv = q != nullptr ? 1.0f / scale : 0.0f;
+  if (bf16)
+    launch_typed<uint16_t>(x, residual, gamma, T, H, eps, residual_out, y, q, inv, stream);
+  else
+    launch_typed<float>(x, residual, gamma, T, H, eps, residual_out, y, q, inv, stream);
+  return launch_status();
+}
+
+}  // namespace moe

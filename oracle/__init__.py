@@ -34,3 +34,15 @@ from .fp8_oracle import (  # noqa: F401
     fp8_linear,
     quantize_fp8,
 )
+from .mxfp4_oracle import (  # noqa: F401
+    mxfp4_decode,
+    mxfp4_encode,
+    mxfp4_grouped_down,
+    mxfp4_grouped_gate_up,
+)
+from .layer_oracle import (  # noqa: F401
+    balance_loss,
+    rms_norm,
+    route_backward,
+    routing_weights,
+)
