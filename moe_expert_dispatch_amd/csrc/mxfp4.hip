@@ -169,10 +169,240 @@ __global__ __launch_bounds__(256) void mxfp4_product_kernel(
   }
 }
 
+// ---------------------------------------------------------------- products, many rows
+// One block per (128 token rows of a slot, 256 weight rows): the same 128
+// gate and up rows, or 256 rows of down. Four waves, each with 64 weight rows
+// (gate and up of 32 columns, or 64 columns) against all 128 tokens, so a
+// weight is converted once in a block and never passes through LDS; the
+// tokens' rows, which all waves need, do: stages of 64 k's, two of them,
+// fetched into registers while the other feeds the matrix cores
+// (v_mfma_f32_32x32x16_bf16, weights first). Lane l holds weight row
+// l mod 32 and the k's 32 (l / 32) .. + 31 of a stage: 16 bytes of codes
+// under one scale. LDS rows are 128 bytes, their 16-byte chunks XOR-swizzled
+// by (row mod 8).
+constexpr int kTileRows = 128;
+constexpr int kTileWeights = 256;
+constexpr int kStage = 64;
+
+typedef float floatx16 __attribute__((ext_vector_type(16)));
+
+// Finds row tile `tile` of the slots' tiles of kTileRows rows, in slot order:
+// the slot, its rows [r0, r1) in the tile; false behind the last. Every wave
+// computes it for itself (a scan over 64 slots at a time).
+__device__ __forceinline__ bool find_tile(const int32_t* __restrict__ offsets, int S,
+                                          int max_rows, int tile, int* slot, int* r0, int* r1) {
+  const int lane = lane_id();
+  for (int s0 = 0; s0 < S; s0 += kWave) {
+    const int s = s0 + lane;
+    int a = 0, b = 0;
+    if (s < S) {
+      a = min(offsets[s], max_rows);
+      b = min(offsets[s + 1], max_rows);
+    }
+    const int n = ceil_div(b - a, kTileRows);
+    int incl = n;
+#pragma unroll
+    for (int o = 1; o < kWave; o <<= 1) {
+      const int v = __shfl_up(incl, o, kWave);
+      if (lane >= o) incl += v;
+    }
+    const uint64_t hit = __ballot(incl > tile);
+    if (hit != 0) {
+      const int l = __ffsll((unsigned long long)hit) - 1;
+      const int first = tile - (__builtin_amdgcn_readlane(incl, l) -
+                                __builtin_amdgcn_readlane(n, l));
+      *slot = s0 + l;
+      *r0 = __builtin_amdgcn_readlane(a, l) + first * kTileRows;
+      *r1 = min(*r0 + kTileRows, __builtin_amdgcn_readlane(b, l));
+      return true;
+    }
+    tile -= __builtin_amdgcn_readlane(incl, kWave - 1);
+  }
+  return false;
+}
+
+// NT: 32-token blocks of the tile that hold rows.
+template <int OP, typename CT, int NT>
+__device__ __forceinline__ void tile_product(uint4 (*stage)[kTileRows * 8],
+                                             const uint16_t* const (&src)[4], int r0, int rows,
+                                             const uint8_t* __restrict__ w,
+                                             const uint8_t* __restrict__ w_scale, int n0, int N,
+                                             int Kd, CT* __restrict__ c) {
+  constexpr bool GU = OP == MOE_GEMM_GATE_UP_SWIGLU;
+  const int tid = threadIdx.x;
+  const int lane = lane_id();
+  const int wave = tid / kWave;
+  const int m = lane & 31, h = lane >> 5;
+  // first columns of the wave's two blocks of 32 weight rows (whole blocks:
+  // N is a multiple of 32); a block past the end computes on another's rows
+  const int col0 = GU ? n0 + 32 * wave : n0 + 64 * wave;
+  const int col1 = GU ? col0 : col0 + 32;
+  const int row0 = min(col0, N - 32) + m;
+  const int row1 = GU ? N + row0 : min(col1, N - 32) + m;
+  // 32-bit offsets into the slot's panel (below 2^31 bytes: weight_panel_ok)
+  const uint32_t wp[2] = {(uint32_t)row0 * (uint32_t)(Kd / 2) + 16 * h,
+                          (uint32_t)row1 * (uint32_t)(Kd / 2) + 16 * h};
+  const uint32_t sp[2] = {(uint32_t)row0 * (uint32_t)(Kd / 32) + h,
+                          (uint32_t)row1 * (uint32_t)(Kd / 32) + h};
+
+  floatx16 acc[2][NT];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[i][t] = floatx16{};
+
+  // thread tid fetches chunk tid % 8 of rows tid / 8 + 32 i
+  const int chunk = tid & 7;
+  uint4 fa[NT];
+  auto fetch = [&](int k0) {
+    const bool in = k0 + 8 * chunk < Kd;
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+      fa[i] = in ? *reinterpret_cast<const uint4*>(src[i] + k0) : make_uint4(0, 0, 0, 0);
+  };
+  auto put = [&](int b) {
+    const int r = tid >> 3;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) stage[b][(r + 32 * i) * 8 + (chunk ^ (r & 7))] = fa[i];
+  };
+  uint4 q[2][2], qn[2][2];
+  uint32_t sc[2][2], scn[2][2];
+  auto load_codes = [&](int k0, uint4 (&qq)[2][2], uint32_t (&ss)[2][2]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const bool in = k0 + kStage * u + 32 * h < Kd;
+        qq[i][u] = make_uint4(0, 0, 0, 0);
+        ss[i][u] = 127;
+        if (in) {
+          qq[i][u] = *reinterpret_cast<const uint4*>(w + (wp[i] + (uint32_t)(k0 + kStage * u) / 2));
+          ss[i][u] = w_scale[sp[i] + (uint32_t)(k0 + kStage * u) / 32];
+        }
+      }
+  };
+  auto compute = [&](int b, int u) {
+    const float s0 = e8m0(sc[0][u]), s1 = e8m0(sc[1][u]);
+    const uint32_t q0[4] = {q[0][u].x, q[0][u].y, q[0][u].z, q[0][u].w};
+    const uint32_t q1[4] = {q[1][u].x, q[1][u].y, q[1][u].z, q[1][u].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const bf16x8_t a0 = __builtin_bit_cast(bf16x8_t, cvt8(q0[j], s0));
+      const bf16x8_t a1 = __builtin_bit_cast(bf16x8_t, cvt8(q1[j], s1));
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const bf16x8_t x = __builtin_bit_cast(
+            bf16x8_t, stage[b][(32 * t + m) * 8 + ((4 * h + j) ^ (m & 7))]);
+        acc[0][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a0, x, acc[0][t], 0, 0, 0);
+        acc[1][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a1, x, acc[1][t], 0, 0, 0);
+      }
+    }
+  };
+
+  fetch(0);
+  load_codes(0, q, sc);
+  put(0);
+  __syncthreads();
+  for (int k0 = 0; k0 < Kd; k0 += 2 * kStage) {
+    fetch(k0 + kStage);
+    load_codes(k0 + 2 * kStage, qn, scn);
+    compute(0, 0);
+    put(1);
+    __syncthreads();
+    fetch(k0 + 2 * kStage);
+    compute(1, 1);
+    put(0);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        q[i][u] = qn[i][u];
+        sc[i][u] = scn[i][u];
+      }
+  }
+
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int tok = 32 * t + m;
+    if (tok >= rows) continue;
+    CT* crow = c + (size_t)(r0 + tok) * N;
+#pragma unroll
+    for (int i = 0; i < (GU ? 1 : 2); ++i) {
+      const int cb = i == 0 ? col0 : col1;
+      if (cb >= N) continue;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        float o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          o[e] = acc[i][t][4 * v + e];
+          if constexpr (GU) o[e] = o[e] / (1.0f + expf(-o[e])) * acc[1][t][4 * v + e];
+        }
+        CT* p = crow + cb + 8 * v + 4 * h;
+        if constexpr (sizeof(CT) == 2)
+          *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+        else
+          *reinterpret_cast<float4*>(p) = make_float4(o[0], o[1], o[2], o[3]);
+      }
+    }
+  }
+}
+
+// Blocks b, b + 8, ... run on one XCD (workgroups are dealt round-robin):
+// it takes whole groups of two row tiles and all their columns, so the two
+// tiles of a slot share its weights in that XCD's L2.
+template <int OP, bool GATHER, typename CT>
+__global__ __launch_bounds__(256, 2) void mxfp4_tile_kernel(
+    const uint16_t* __restrict__ a, const int32_t* __restrict__ offsets,
+    const int32_t* __restrict__ sorted_pairs, int topk, int S, int max_rows,
+    const uint8_t* __restrict__ w, const uint8_t* __restrict__ w_scale, int N, int Kd,
+    CT* __restrict__ c) {
+  constexpr int M = OP == MOE_GEMM_GATE_UP_SWIGLU ? 2 : 1;
+  __shared__ uint4 stage[2][kTileRows * 8];
+  const int ncol = ceil_div(N, kTileWeights / M);
+  const int group = 2 * ncol;
+  const int in = (int)(blockIdx.x >> 3);
+  const int tile = ((in / group) * 8 + (int)(blockIdx.x & 7)) * 2 + (in % group) % 2;
+  const int n0 = (in % group) / 2 * (kTileWeights / M);
+  int s = 0, r0 = 0, r1 = 0;
+  if (!find_tile(offsets, S, max_rows, tile, &s, &r0, &r1)) return;
+  const int rows = r1 - r0;
+  const uint16_t* src[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    int row = r0 + min((int)(threadIdx.x >> 3) + 32 * i, rows - 1);
+    if constexpr (GATHER) row = sorted_pairs[row] / topk;
+    src[i] = a + (size_t)row * Kd + 8 * (threadIdx.x & 7);
+  }
+  const size_t wrow = (size_t)s * M * N;
+  const uint8_t* ws = w + wrow * (Kd / 2);
+  const uint8_t* ss = w_scale + wrow * (Kd / 32);
+  if (rows <= 32)
+    tile_product<OP, CT, 1>(stage, src, r0, rows, ws, ss, n0, N, Kd, c);
+  else if (rows <= 64)
+    tile_product<OP, CT, 2>(stage, src, r0, rows, ws, ss, n0, N, Kd, c);
+  else if (rows <= 96)
+    tile_product<OP, CT, 3>(stage, src, r0, rows, ws, ss, n0, N, Kd, c);
+  else
+    tile_product<OP, CT, 4>(stage, src, r0, rows, ws, ss, n0, N, Kd, c);
+}
+
 template <int OP, bool GATHER, typename CT>
 void launch_product(const void* a, const int32_t* offsets, const int32_t* sorted_pairs, int topk,
                     int S, int max_rows, const uint8_t* w, const uint8_t* w_scale, int N, int Kd,
                     void* c, hipStream_t stream) {
+  if (max_rows >= 32 * S) {
+    constexpr int M = OP == MOE_GEMM_GATE_UP_SWIGLU ? 2 : 1;
+    // at most this many row tiles, whatever the slots' counts
+    const int64_t tiles = (int64_t)max_rows / kTileRows + S;
+    const int64_t group = 2 * ceil_div(N, kTileWeights / M);
+    const int64_t groups = (tiles + 15) / 16 * 8;  // groups of two row tiles, eight XCDs
+    mxfp4_tile_kernel<OP, GATHER, CT><<<(unsigned)(groups * group), 256, 0, stream>>>(
+        static_cast<const uint16_t*>(a), offsets, sorted_pairs, topk, S, max_rows, w, w_scale, N,
+        Kd, static_cast<CT*>(c));
+    return;
+  }
   mxfp4_product_kernel<OP, GATHER, CT><<<dim3(ceil_div(N, 16), S), 256, 0, stream>>>(
       static_cast<const uint16_t*>(a), offsets, sorted_pairs, topk, max_rows, w, w_scale, N, Kd,
       static_cast<CT*>(c));

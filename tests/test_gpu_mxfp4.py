@@ -95,7 +95,9 @@ def test_quantize_empty_and_refusals():
 
 # ------------------------------------------------------------------ products
 SIZES = [[1], [0, 1, 0], [3, 0, 16, 1], [17, 0, 5, 33], [70, 1, 0, 0, 2], [300, 129], [0, 0],
-         [40, 64, 65, 8, 9, 4, 5, 2]]
+         [40, 64, 65, 8, 9, 4, 5, 2],
+         # enough rows a slot for the tiles of 128, with every number of 32-row blocks in one
+         [0, 500, 0, 31, 97, 128, 0, 0, 4, 0], [33], [64, 1], [96, 160, 129, 0], [0] * 70 + [4000, 1, 0]]
 
 
 def _offsets(sizes):
