@@ -83,89 +83,216 @@ __global__ __launch_bounds__(256) void dequantize_mxfp4_kernel(const uint32_t* _
   }
 }
 
-// ---------------------------------------------------------------- products
-// One block per (16 output columns, slot): its four waves split the
-// contraction into chunks of 128 (wave w takes chunks w, w + 4, ...), hold
-// 16 x 16 sums for 16 weight rows and 16 token rows, and add up in LDS in
-// wave order. v_mfma_f32_16x16x32_bf16 with the weights as the first operand:
-// lane l supplies weight row l mod 16 and token row l mod 16, the k's
-// 32 (l / 16) .. + 31 of the chunk in four steps of 8, so a lane's codes are
+// ---------------------------------------------------------------- products, few rows
+// Bound by the stream of the codes. One block per (16 WN output columns,
+// slot): eight waves, WN column tiles times WK waves that split the
+// contraction. v_mfma_f32_16x16x32_bf16 with the weights as the first
+// operand: lane l supplies weight row l mod 16 and token row l mod 16, the
+// k's 32 (l / 16) .. + 31 of a 128 in four steps of 8, so a lane's codes are
 // 16 consecutive bytes under one scale. Register r of lane l then holds
-// column 4 (l / 16) + r of token row l mod 16.
-constexpr int kProdWaves = 4;
+// column 4 (l / 16) + r of token row l mod 16. A wave walks its k's 128 RUN
+// at a time with the next codes in flight, and meets no barrier on the way:
+// the token rows, RB at a time, wait in LDS (all their k's, or a window of
+// them where they are too long), fetched once for the block's columns. The
+// WK partial sums are added in LDS in wave order.
+// The codes and scales of one lane for a step: of its weight row the 16 bytes
+// at k0 + 128 i + 32 g, and in byte g of s[i] their scale.
+template <int M, int RUN>
+struct StepWeights {
+  uint4 q[M][RUN];
+  uint32_t s[M][RUN];
+};
 
-template <int OP, bool GATHER, typename CT>
-__global__ __launch_bounds__(256) void mxfp4_product_kernel(
+// ALIGNED: Kd is a multiple of 128, so a row's scales start at a whole word
+// and a 128 has one word of them.
+template <int M, int RUN, bool ALIGNED>
+__device__ __forceinline__ void load_step(StepWeights<M, RUN>& v, const uint8_t* __restrict__ w,
+                                          const uint8_t* __restrict__ w_scale,
+                                          const uint32_t (&row)[M], int Kd, int k0, int kend,
+                                          int g) {
+#pragma unroll
+  for (int i = 0; i < M; ++i) {
+    const uint32_t cb = row[i] * (uint32_t)(Kd / 2) + (uint32_t)k0 / 2 + 16 * g;
+    const uint32_t sb = row[i] * (uint32_t)(Kd / 32) + (uint32_t)k0 / 32;
+#pragma unroll
+    for (int j = 0; j < RUN; ++j)
+      v.q[i][j] = k0 + 128 * j + 32 * g < kend
+                      ? *reinterpret_cast<const uint4*>(w + (cb + 64 * j))
+                      : make_uint4(0, 0, 0, 0);
+    if (ALIGNED && k0 + 128 * RUN <= kend) {
+      uint32_t t[RUN];
+      __builtin_memcpy(t, __builtin_assume_aligned(w_scale + sb, 4), sizeof(t));
+#pragma unroll
+      for (int j = 0; j < RUN; ++j) v.s[i][j] = t[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < RUN; ++j) {
+        v.s[i][j] = 0;
+        if constexpr (ALIGNED) {
+          if (k0 + 128 * j < kend)
+            v.s[i][j] = *reinterpret_cast<const uint32_t*>(w_scale + (sb + 4 * j));
+        } else {
+          if (k0 + 128 * j + 32 * g < kend)
+            v.s[i][j] = (uint32_t)w_scale[sb + 4 * j + g] << (8 * g);
+        }
+      }
+    }
+  }
+}
+
+// The slot of blockIdx.y: itself, or with `find` the blockIdx.y-th slot that
+// has rows (fewer rows than slots: the grid then has one line a row). Every
+// wave computes it for itself. False where there is none.
+__device__ __forceinline__ bool block_slot(const int32_t* __restrict__ offsets, int S,
+                                           int max_rows, bool find, int* slot, int* r0, int* r1) {
+  if (!find) {
+    *slot = blockIdx.y;
+    *r0 = min(offsets[blockIdx.y], max_rows);
+    *r1 = min(offsets[blockIdx.y + 1], max_rows);
+    return *r0 < *r1;
+  }
+  const int lane = lane_id();
+  int want = blockIdx.y;
+  for (int s0 = 0; s0 < S; s0 += kWave) {
+    const int s = s0 + lane;
+    int a = 0, b = 0;
+    if (s < S) {
+      a = min(offsets[s], max_rows);
+      b = min(offsets[s + 1], max_rows);
+    }
+    uint64_t some = __ballot(b > a);
+    const int n = __popcll(some);
+    if (want < n) {
+      for (; want > 0; --want) some &= some - 1;
+      const int l = __ffsll((unsigned long long)some) - 1;
+      *slot = s0 + l;
+      *r0 = __builtin_amdgcn_readlane(a, l);
+      *r1 = __builtin_amdgcn_readlane(b, l);
+      return true;
+    }
+    want -= n;
+  }
+  return false;
+}
+
+constexpr int kStreamWaves = 8;
+constexpr int kStreamLds = 64 * 1024;  // of the token rows in a block: two blocks a CU
+
+// k's of a window: all, or equal parts that fit, in whole steps of WK waves.
+__host__ __device__ inline int stream_window(int Kd, int RB, int WK) {
+  const int fit = kStreamLds / (2 * RB);
+  const int parts = ceil_div(Kd, fit);
+  return ceil_div(ceil_div(Kd, parts), WK * 128) * WK * 128;
+}
+// 16-byte vectors of a row in LDS: one more, so that rows start in other banks
+__host__ __device__ inline int stream_row_vecs(int window) { return window / 8 + 1; }
+
+template <int OP, bool GATHER, typename CT, int WK, int RB, int RUN, bool PIPE, bool ALIGNED>
+__global__ __launch_bounds__(64 * kStreamWaves) void mxfp4_stream_kernel(
     const uint16_t* __restrict__ a, const int32_t* __restrict__ offsets,
-    const int32_t* __restrict__ sorted_pairs, int topk, int max_rows,
+    const int32_t* __restrict__ sorted_pairs, int topk, int S, int max_rows, int find,
     const uint8_t* __restrict__ w, const uint8_t* __restrict__ w_scale, int N, int Kd,
     CT* __restrict__ c) {
   constexpr int M = OP == MOE_GEMM_GATE_UP_SWIGLU ? 2 : 1;  // matrices (gate and up, or down)
-  __shared__ floatx4 red[kProdWaves][M][kWave];
-  const int s = blockIdx.y;
-  const int r0 = offsets[s];
-  const int r1 = min(offsets[s + 1], max_rows);
-  if (r0 >= r1) return;
-  const int n0 = blockIdx.x * 16;
+  constexpr int WN = kStreamWaves / WK;
+  extern __shared__ uint4 lds[];
+  int s, r0, r1;
+  if (!block_slot(offsets, S, max_rows, find != 0, &s, &r0, &r1)) return;
+  const int tid = threadIdx.x;
   const int lane = lane_id();
-  const int wave = threadIdx.x / kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int wk = wave % WK, wn = wave / WK;
   const int m = lane & 15, g = lane >> 4;
-  const int n = min(n0 + m, N - 1);
+  const int n0 = (blockIdx.x * WN + wn) * 16;
+  const bool tile = n0 < N;  // N is a multiple of 16
+  uint32_t wrow[M];
+#pragma unroll
+  for (int i = 0; i < M; ++i) wrow[i] = (uint32_t)(i * N + (tile ? n0 : 0) + m);
   const size_t rows_s = (size_t)s * M * N;
-  for (int rt = r0; rt < r1; rt += 16) {
-    int row = min(rt + m, r1 - 1);
-    if constexpr (GATHER) row = sorted_pairs[row] / topk;
-    const uint16_t* arow = a + (size_t)row * Kd;
+  const uint8_t* ws = w + rows_s * (size_t)(Kd / 2);
+  const uint8_t* ss = w_scale + rows_s * (size_t)(Kd / 32);
+  const int window = stream_window(Kd, RB, WK);
+  const int per = window / WK;  // k's of a wave in a window, whole 128s
+  const int rvecs = stream_row_vecs(window);
+  const int pieces = ceil_div(window, 8 * kWave);
+
+  for (int rt = r0; rt < r1; rt += RB) {
+    const int nr = min(r1 - rt, RB);
     floatx4 acc[M];
 #pragma unroll
     for (int i = 0; i < M; ++i) acc[i] = floatx4{0.f, 0.f, 0.f, 0.f};
-    for (int k0 = wave * 128; k0 < Kd; k0 += kProdWaves * 128) {
-      const int k = k0 + 32 * g;
-      const bool in = k < Kd;  // Kd is a multiple of 32
-      uint4 b[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        b[j] = in ? *reinterpret_cast<const uint4*>(arow + k + 8 * j) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int i = 0; i < M; ++i) {
-        const size_t wr = rows_s + (size_t)i * N + n;
-        uint4 q = make_uint4(0, 0, 0, 0);
-        float sc = 1.0f;
-        if (in) {
-          q = *reinterpret_cast<const uint4*>(w + (wr * Kd + k) / 2);
-          sc = e8m0(w_scale[(wr * Kd + k) / 32]);
+    StepWeights<M, RUN> cur, next;
+    load_step<M, RUN, ALIGNED>(cur, ws, ss, wrow, Kd, wk * per, min((wk + 1) * per, Kd), g);
+    for (int base = 0; base < Kd; base += window) {
+      if (base != 0) __syncthreads();  // the last window is read
+      // a wave fetches 512 k's of a row at a time
+      for (int u = wave; u < nr * pieces; u += kStreamWaves) {
+        const int r = u / pieces;
+        const int v = (u - r * pieces) * kWave + lane;
+        int row = rt + r;
+        if constexpr (GATHER) row = sorted_pairs[row] / topk;
+        if (v < window / 8)
+          lds[r * rvecs + v] =
+              base + 8 * v < Kd
+                  ? *reinterpret_cast<const uint4*>(a + (size_t)row * Kd + base + 8 * v)
+                  : make_uint4(0, 0, 0, 0);
+      }
+      __syncthreads();
+      for (int at = 0; at < per; at += 128 * RUN) {
+        if constexpr (PIPE) {
+          // the next step's codes: in this window, or the first of the next
+          const bool last = at + 128 * RUN >= per;
+          const int nbase = base + (last ? window : 0) + wk * per;
+          load_step<M, RUN, ALIGNED>(next, ws, ss, wrow, Kd, nbase + (last ? 0 : at + 128 * RUN),
+                                     min(nbase + per, Kd), g);
         }
-        const uint32_t qq[4] = {q.x, q.y, q.z, q.w};
+        const uint4* x = lds + (m < nr ? m : 0) * rvecs + (wk * per + at) / 8 + 4 * g;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-              __builtin_bit_cast(bf16x8_t, cvt8(qq[j], sc)), __builtin_bit_cast(bf16x8_t, b[j]),
-              acc[i], 0, 0, 0);
+        for (int j = 0; j < RUN; ++j) {
+          if (at + 128 * j >= per) break;  // the same for the whole block
+          uint4 b[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) b[e] = m < nr ? x[16 * j + e] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int i = 0; i < M; ++i) {
+            const float sc = e8m0((cur.s[i][j] >> (8 * g)) & 255u);
+            const uint32_t qq[4] = {cur.q[i][j].x, cur.q[i][j].y, cur.q[i][j].z, cur.q[i][j].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                  __builtin_bit_cast(bf16x8_t, cvt8(qq[e], sc)),
+                  __builtin_bit_cast(bf16x8_t, b[e]), acc[i], 0, 0, 0);
+          }
+        }
+        if constexpr (PIPE) cur = next;
       }
     }
+    if constexpr (WK > 1) {
+      __syncthreads();  // the rows are read: the partial sums take their place
+      floatx4* red = reinterpret_cast<floatx4*>(lds) + wn * WK * M * kWave;
 #pragma unroll
-    for (int i = 0; i < M; ++i) red[wave][i][lane] = acc[i];
-    __syncthreads();
-    if (wave == 0) {
+      for (int i = 0; i < M; ++i) red[(wk * M + i) * kWave + lane] = acc[i];
+      __syncthreads();
+      if (wk == 0) {
 #pragma unroll
-      for (int i = 0; i < M; ++i)
-        for (int v = 1; v < kProdWaves; ++v) acc[i] += red[v][i][lane];
-      if (rt + m < r1) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int col = n0 + 4 * g + r;
-          if (col >= N) continue;
-          float v = acc[0][r];
-          if constexpr (M == 2) v = v / (1.0f + expf(-v)) * acc[1][r];
-          CT* o = c + (size_t)(rt + m) * N + col;
-          if constexpr (sizeof(CT) == 2)
-            *o = (CT)(pack_bf16x2(v, 0.f) & 0xffffu);
-          else
-            *o = v;
-        }
+        for (int i = 0; i < M; ++i)
+          for (int u = 1; u < WK; ++u) acc[i] += red[(u * M + i) * kWave + lane];
       }
     }
-    __syncthreads();
+    if (wk == 0 && tile && m < nr) {
+      float o[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        o[r] = acc[0][r];
+        if constexpr (M == 2) o[r] = o[r] / (1.0f + expf(-o[r])) * acc[1][r];
+      }
+      CT* p = c + (size_t)(rt + m) * N + n0 + 4 * g;
+      if constexpr (sizeof(CT) == 2)
+        *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+      else
+        *reinterpret_cast<float4*>(p) = make_float4(o[0], o[1], o[2], o[3]);
+    }
+    if (rt + RB < r1) __syncthreads();  // rows and partial sums are read
   }
 }
 
@@ -186,9 +313,10 @@ constexpr int kStage = 64;
 
 typedef float floatx16 __attribute__((ext_vector_type(16)));
 
-// Finds row tile `tile` of the slots' tiles of kTileRows rows, in slot order:
-// the slot, its rows [r0, r1) in the tile; false behind the last. Every wave
+// Finds row tile `tile` of the slots' tiles of TR rows, in slot order: the
+// slot, its rows [r0, r1) in the tile; false behind the last. Every wave
 // computes it for itself (a scan over 64 slots at a time).
+template <int TR>
 __device__ __forceinline__ bool find_tile(const int32_t* __restrict__ offsets, int S,
                                           int max_rows, int tile, int* slot, int* r0, int* r1) {
   const int lane = lane_id();
@@ -199,7 +327,7 @@ __device__ __forceinline__ bool find_tile(const int32_t* __restrict__ offsets, i
       a = min(offsets[s], max_rows);
       b = min(offsets[s + 1], max_rows);
     }
-    const int n = ceil_div(b - a, kTileRows);
+    const int n = ceil_div(b - a, TR);
     int incl = n;
 #pragma unroll
     for (int o = 1; o < kWave; o <<= 1) {
@@ -212,8 +340,8 @@ __device__ __forceinline__ bool find_tile(const int32_t* __restrict__ offsets, i
       const int first = tile - (__builtin_amdgcn_readlane(incl, l) -
                                 __builtin_amdgcn_readlane(n, l));
       *slot = s0 + l;
-      *r0 = __builtin_amdgcn_readlane(a, l) + first * kTileRows;
-      *r1 = min(*r0 + kTileRows, __builtin_amdgcn_readlane(b, l));
+      *r0 = __builtin_amdgcn_readlane(a, l) + first * TR;
+      *r1 = min(*r0 + TR, __builtin_amdgcn_readlane(b, l));
       return true;
     }
     tile -= __builtin_amdgcn_readlane(incl, kWave - 1);
@@ -366,7 +494,7 @@ __global__ __launch_bounds__(256, 2) void mxfp4_tile_kernel(
   const int tile = ((in / group) * 8 + (int)(blockIdx.x & 7)) * 2 + (in % group) % 2;
   const int n0 = (in % group) / 2 * (kTileWeights / M);
   int s = 0, r0 = 0, r1 = 0;
-  if (!find_tile(offsets, S, max_rows, tile, &s, &r0, &r1)) return;
+  if (!find_tile<kTileRows>(offsets, S, max_rows, tile, &s, &r0, &r1)) return;
   const int rows = r1 - r0;
   const uint16_t* src[4];
 #pragma unroll
@@ -388,24 +516,294 @@ __global__ __launch_bounds__(256, 2) void mxfp4_tile_kernel(
     tile_product<OP, CT, 4>(stage, src, r0, rows, ws, ss, n0, N, Kd, c);
 }
 
+// ---------------------------------------------------------------- products, some rows
+// Between the two: tiles of 32 NT token rows against 256 weight rows, still
+// bound by the stream of the codes. Eight waves: four of 64 weight rows, as
+// above, twice, the two halves taking every other run of 64 U k's, so a block
+// has twice the loads in flight and half the steps; the second half's sums
+// are added in LDS at the end. A step's codes are whole 128-byte lines
+// (U = 4), fetched a step ahead with the tokens' rows.
+template <int OP, bool GATHER, typename CT, int NT, int U, bool ALIGNED>
+__global__ __launch_bounds__(512, U == 2 ? 2 : 1) void mxfp4_split_kernel(
+    const uint16_t* __restrict__ a, const int32_t* __restrict__ offsets,
+    const int32_t* __restrict__ sorted_pairs, int topk, int S, int max_rows,
+    const uint8_t* __restrict__ w, const uint8_t* __restrict__ w_scale, int N, int Kd,
+    CT* __restrict__ c) {
+  constexpr bool GU = OP == MOE_GEMM_GATE_UP_SWIGLU;
+  constexpr int M = GU ? 2 : 1;
+  constexpr int TR = 32 * NT;
+  constexpr int kRun64 = 64 * U;              // k's of a half's step
+  constexpr int kVecs = TR * 8 * U;           // 16-byte vectors of a half's stage
+  constexpr int kFetch = kVecs / 256;         // of them a thread's
+  __shared__ uint4 stage[2][2][kVecs];        // [half][buffer][unit, row, swizzled chunk]
+  static_assert(sizeof(stage) >= 2u * NT * 16 * 4 * 256, "the second half's sums fit");
+  const int ncol = ceil_div(N, kTileWeights / M);
+  const int group = 2 * ncol;
+  const int bi = (int)(blockIdx.x >> 3);
+  const int tile = ((bi / group) * 8 + (int)(blockIdx.x & 7)) * 2 + (bi % group) % 2;
+  const int n0 = (bi % group) / 2 * (kTileWeights / M);
+  int s = 0, r0 = 0, r1 = 0;
+  if (!find_tile<TR>(offsets, S, max_rows, tile, &s, &r0, &r1)) return;
+  const int rows = r1 - r0;
+  const int lane = lane_id();
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
+  const int half = wave >> 2, wn = wave & 3;
+  const int tid = threadIdx.x & 255;  // in the half
+  const int m = lane & 31, h = lane >> 5;
+  const int col0 = GU ? n0 + 32 * wn : n0 + 64 * wn;
+  const int col1 = GU ? col0 : col0 + 32;
+  const uint32_t row[2] = {(uint32_t)(min(col0, N - 32) + m),
+                           (uint32_t)(GU ? N + min(col0, N - 32) + m : min(col1, N - 32) + m)};
+  const size_t wrow = (size_t)s * M * N;
+  const uint8_t* ws = w + wrow * (Kd / 2);
+  const uint8_t* ss = w_scale + wrow * (Kd / 32);
+
+  struct Codes {
+    uint4 q[2][U];
+    uint32_t s[2][(U + 1) / 2];  // byte 2 u + h: the scale of unit u
+  };
+  auto load_codes = [&](Codes& v, int kb) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t cb = row[i] * (uint32_t)(Kd / 2) + (uint32_t)kb / 2 + 16 * h;
+      const uint32_t sb = row[i] * (uint32_t)(Kd / 32) + (uint32_t)kb / 32;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        v.q[i][u] = kb + 64 * u + 32 * h < Kd
+                        ? *reinterpret_cast<const uint4*>(ws + (cb + 32 * u))
+                        : make_uint4(0, 0, 0, 0);
+      if (ALIGNED && kb + kRun64 <= Kd) {
+#pragma unroll
+        for (int x = 0; x < U / 2; ++x)
+          v.s[i][x] = *reinterpret_cast<const uint32_t*>(ss + (sb + 4 * x));
+      } else {
+#pragma unroll
+        for (int x = 0; x < U / 2; ++x) v.s[i][x] = 0;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (kb + 64 * u + 32 * h < Kd)
+            v.s[i][u / 2] |= (uint32_t)ss[sb + 2 * u + h] << (16 * (u & 1) + 8 * h);
+      }
+    }
+  };
+  // vector v = tid + 256 i of a stage: unit v / (8 TR), row (v / 8) mod TR, chunk v mod 8
+  const uint16_t* src[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    int r = r0 + min((tid >> 3) + 32 * i, rows - 1);
+    if constexpr (GATHER) r = sorted_pairs[r] / topk;
+    src[i] = a + (size_t)r * Kd + 8 * (tid & 7);
+  }
+  uint4 fa[kFetch];
+  auto fetch = [&](int kb) {
+#pragma unroll
+    for (int i = 0; i < kFetch; ++i) {
+      const int k = kb + 64 * (i / NT);
+      fa[i] = k + 8 * (tid & 7) < Kd ? *reinterpret_cast<const uint4*>(src[i % NT] + k)
+                                     : make_uint4(0, 0, 0, 0);
+    }
+  };
+  auto put = [&](int b) {
+#pragma unroll
+    for (int i = 0; i < kFetch; ++i) {
+      const int r = (tid >> 3) + 32 * (i % NT);
+      stage[half][b][(i / NT) * TR * 8 + r * 8 + ((tid & 7) ^ (r & 7))] = fa[i];
+    }
+  };
+
+  floatx16 acc[2][NT];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[i][t] = floatx16{};
+  const int steps = ceil_div(Kd, 2 * kRun64);
+  const int kb0 = half * kRun64;
+  Codes cur, next;
+  load_codes(cur, kb0);
+  fetch(kb0);
+  put(0);
+  __syncthreads();
+  for (int st = 0; st < steps; ++st) {
+    const int kn = kb0 + (st + 1) * 2 * kRun64;
+    if (st + 1 < steps) {
+      load_codes(next, kn);
+      fetch(kn);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    const int b = st & 1;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float s0 = e8m0((cur.s[0][u / 2] >> (16 * (u & 1) + 8 * h)) & 255u);
+      const float s1 = e8m0((cur.s[1][u / 2] >> (16 * (u & 1) + 8 * h)) & 255u);
+      const uint32_t q0[4] = {cur.q[0][u].x, cur.q[0][u].y, cur.q[0][u].z, cur.q[0][u].w};
+      const uint32_t q1[4] = {cur.q[1][u].x, cur.q[1][u].y, cur.q[1][u].z, cur.q[1][u].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bf16x8_t a0 = __builtin_bit_cast(bf16x8_t, cvt8(q0[j], s0));
+        const bf16x8_t a1 = __builtin_bit_cast(bf16x8_t, cvt8(q1[j], s1));
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const bf16x8_t x = __builtin_bit_cast(
+              bf16x8_t,
+              stage[half][b][u * TR * 8 + (32 * t + m) * 8 + ((4 * h + j) ^ (m & 7))]);
+          acc[0][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a0, x, acc[0][t], 0, 0, 0);
+          acc[1][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a1, x, acc[1][t], 0, 0, 0);
+        }
+      }
+    }
+    if (st + 1 < steps) {
+      put(b ^ 1);
+      cur = next;
+    }
+    __syncthreads();
+  }
+
+  floatx4* red = reinterpret_cast<floatx4*>(&stage[0][0][0]);
+  if (half == 1) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          red[((i * NT + t) * 4 + v) * 256 + tid] =
+              floatx4{acc[i][t][4 * v], acc[i][t][4 * v + 1], acc[i][t][4 * v + 2],
+                      acc[i][t][4 * v + 3]};
+  }
+  __syncthreads();
+  if (half == 1) return;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int tok = 32 * t + m;
+    if (tok >= rows) continue;
+    CT* crow = c + (size_t)(r0 + tok) * N;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const floatx4 e0 = red[(t * 4 + v) * 256 + tid];
+      const floatx4 e1 = red[((NT + t) * 4 + v) * 256 + tid];
+      float o[2][4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        o[0][e] = acc[0][t][4 * v + e] + e0[e];
+        o[1][e] = acc[1][t][4 * v + e] + e1[e];
+        if constexpr (GU) o[0][e] = o[0][e] / (1.0f + expf(-o[0][e])) * o[1][e];
+      }
+#pragma unroll
+      for (int i = 0; i < (GU ? 1 : 2); ++i) {
+        const int cb = i == 0 ? col0 : col1;
+        if (cb >= N) continue;
+        CT* p = crow + cb + 8 * v + 4 * h;
+        if constexpr (sizeof(CT) == 2)
+          *reinterpret_cast<uint2*>(p) =
+              make_uint2(pack_bf16x2(o[i][0], o[i][1]), pack_bf16x2(o[i][2], o[i][3]));
+        else
+          *reinterpret_cast<float4*>(p) = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
+      }
+    }
+  }
+}
+
+// Which kernel, by the rows a slot has on the average of all (max_rows / S:
+// the host knows no more).
+constexpr int kStreamRows = 10;
+constexpr int kSplitRows1 = 24;
+constexpr int kSplitRows2 = 56;
+
 template <int OP, bool GATHER, typename CT>
 void launch_product(const void* a, const int32_t* offsets, const int32_t* sorted_pairs, int topk,
                     int S, int max_rows, const uint8_t* w, const uint8_t* w_scale, int N, int Kd,
                     void* c, hipStream_t stream) {
-  if (max_rows >= 32 * S) {
-    constexpr int M = OP == MOE_GEMM_GATE_UP_SWIGLU ? 2 : 1;
-    // at most this many row tiles, whatever the slots' counts
-    const int64_t tiles = (int64_t)max_rows / kTileRows + S;
-    const int64_t group = 2 * ceil_div(N, kTileWeights / M);
-    const int64_t groups = (tiles + 15) / 16 * 8;  // groups of two row tiles, eight XCDs
-    mxfp4_tile_kernel<OP, GATHER, CT><<<(unsigned)(groups * group), 256, 0, stream>>>(
-        static_cast<const uint16_t*>(a), offsets, sorted_pairs, topk, S, max_rows, w, w_scale, N,
-        Kd, static_cast<CT*>(c));
+  using std::integral_constant;
+  constexpr int M = OP == MOE_GEMM_GATE_UP_SWIGLU ? 2 : 1;
+  // Blocks for all tiles of `tr` rows, of which there are at most this many
+  // whatever the slots' counts: groups of two row tiles, eight XCDs.
+  auto tile_blocks = [&](int tr) {
+    const int64_t tiles = (int64_t)max_rows / tr + S;
+    return (unsigned)((tiles + 15) / 16 * 8 * 2 * ceil_div(N, kTileWeights / M));
+  };
+  const uint16_t* a16 = static_cast<const uint16_t*>(a);
+  CT* ct = static_cast<CT*>(c);
+  const bool aligned = Kd % 128 == 0;
+  if (max_rows > (M == 2 ? kSplitRows2 : kSplitRows1) * S) {
+    mxfp4_tile_kernel<OP, GATHER, CT><<<tile_blocks(kTileRows), 256, 0, stream>>>(
+        a16, offsets, sorted_pairs, topk, S, max_rows, w, w_scale, N, Kd, ct);
     return;
   }
-  mxfp4_product_kernel<OP, GATHER, CT><<<dim3(ceil_div(N, 16), S), 256, 0, stream>>>(
-      static_cast<const uint16_t*>(a), offsets, sorted_pairs, topk, max_rows, w, w_scale, N, Kd,
-      static_cast<CT*>(c));
+  if (max_rows > kStreamRows * S) {
+    auto go = [&](auto nt, auto al) {
+      constexpr int NT = decltype(nt)::value;
+      mxfp4_split_kernel<OP, GATHER, CT, NT, NT == 1 ? 2 : 4, decltype(al)::value>
+          <<<tile_blocks(32 * NT), 512, 0, stream>>>(a16, offsets, sorted_pairs, topk, S,
+                                                     max_rows, w, w_scale, N, Kd, ct);
+    };
+    if (M == 1 || max_rows <= kSplitRows1 * S) {
+      if (aligned)
+        go(integral_constant<int, 1>{}, std::true_type{});
+      else
+        go(integral_constant<int, 1>{}, std::false_type{});
+    } else if constexpr (M == 2) {
+      if (aligned)
+        go(integral_constant<int, 2>{}, std::true_type{});
+      else
+        go(integral_constant<int, 2>{}, std::false_type{});
+    }
+    return;
+  }
+  const int lines = max_rows < S ? max_rows : S;  // slots that can have rows
+  auto go = [&](auto wk, auto rb, auto run, auto pipe, auto al) {
+    constexpr int WK = decltype(wk)::value, RB = decltype(rb)::value;
+    const size_t rows_lds = (size_t)RB * stream_row_vecs(stream_window(Kd, RB, WK)) * 16;
+    const size_t red_lds = WK > 1 ? (size_t)kStreamWaves * M * kWave * 16 : 0;
+    mxfp4_stream_kernel<OP, GATHER, CT, WK, RB, decltype(run)::value, decltype(pipe)::value,
+                        decltype(al)::value>
+        <<<dim3(ceil_div(N, 16 * kStreamWaves / WK), lines), 64 * kStreamWaves,
+           rows_lds > red_lds ? rows_lds : red_lds, stream>>>(
+            a16, offsets, sorted_pairs, topk, S, max_rows, max_rows < S, w, w_scale, N, Kd, ct);
+  };
+  // The contraction is split among waves where the columns alone leave the
+  // chip without a block for every compute unit, and where it is short: up to 1024
+  // a wave's part is one step, and many light blocks beat few that walk two
+  // steps (S = 64, N = 4096, Kd = 1024: 28 against 36 us).
+  int split = Kd <= 512 || Kd > 1024 ? 1 : 2;
+  const long long want = device_cu_count();
+  while (split < kStreamWaves && split * 512 < Kd &&
+         (long long)ceil_div(N, 16 * kStreamWaves / split) * lines < want)
+    split *= 2;
+  const bool one = ceil_div(ceil_div(Kd, 128), split) <= 4;  // one step of 512 a wave
+  using i1 = integral_constant<int, 1>;
+  using i2 = integral_constant<int, 2>;
+  using i4 = integral_constant<int, 4>;
+  using i8 = integral_constant<int, 8>;
+  auto pick = [&](auto rb) {
+    if (!aligned) {
+      if (split == 1)
+        go(i1{}, rb, i2{}, std::true_type{}, std::false_type{});
+      else
+        go(i8{}, rb, i2{}, std::true_type{}, std::false_type{});
+    } else if (one) {
+      if (split == 1)
+        go(i1{}, rb, i4{}, std::false_type{}, std::true_type{});
+      else if (split == 2)
+        go(i2{}, rb, i4{}, std::false_type{}, std::true_type{});
+      else if (split == 4)
+        go(i4{}, rb, i4{}, std::false_type{}, std::true_type{});
+      else
+        go(i8{}, rb, i4{}, std::false_type{}, std::true_type{});
+    } else if (split > 1) {
+      go(i8{}, rb, i2{}, std::true_type{}, std::true_type{});
+    } else if (M == 1 || (Kd >= 4096 && decltype(rb)::value == 8)) {
+      // 512 a step: one block of gate/up a compute unit (164 registers), 60 against 66 us at
+      // S = 64, N = 1024, Kd = 4096; at Kd = 2048 two blocks with steps of 256 win, 15.5
+      // against 16.6 us (N = 512)
+      go(i1{}, rb, i4{}, std::true_type{}, std::true_type{});
+    } else {
+      go(i1{}, rb, i2{}, std::true_type{}, std::true_type{});
+    }
+  };
+  if (max_rows <= 4 * S)
+    pick(i8{});
+  else
+    pick(integral_constant<int, 16>{});
 }
 
 }  // namespace
