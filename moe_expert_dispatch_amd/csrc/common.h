@@ -154,8 +154,8 @@ __host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b -
 // e mod E_local; TensorRT-LLM PR #4495: expert id -> engine-side slot). The
 // replica of a local expert is chosen by token index, t mod r. A null table
 // is the identity map; an entry outside [0, S) (or an expert without slots)
-// gives slot -1.
-__device__ __forceinline__ void map_pair(int p, int t, int e, float wv, int start, int E_local,
+// gives slot -1. Returns the slot.
+__device__ __forceinline__ int map_pair(int p, int t, int e, float wv, int start, int E_local,
                                          const int32_t* __restrict__ rep_off,
                                          const int32_t* __restrict__ rep_slots, int S,
                                          int32_t* __restrict__ slot,
@@ -177,6 +177,7 @@ __device__ __forceinline__ void map_pair(int p, int t, int e, float wv, int star
   slot[p] = s;
   w_masked[p] = wv * (local ? 1.0f : 0.0f);
   mask[p] = local ? 1 : 0;
+  return s;
 }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -284,6 +285,17 @@ moe_status_t launch_slot_map(const int32_t* ids, const float* w, int T, int K, i
                              int S, int32_t* slot, float* w_masked, uint8_t* mask,
                              hipStream_t stream);
 
+// Routing (or given ids and weights: logits null), slot map and permutation of
+// at most kPlanPairs pairs, with the results of launch_route_map or
+// launch_slot_map and of launch_permute, in one launch or two. ids and w are
+// scratch where logits are given (not always written).
+constexpr int kPlanPairs = 1024;
+moe_status_t launch_plan(const float* logits, int T, int E, int K, int renorm, int G, int TG,
+                         int32_t* ids, float* w, int start, int E_local, const int32_t* rep_off,
+                         const int32_t* rep_slots, int S, int32_t* slot, float* w_masked,
+                         uint8_t* mask, int32_t* offsets, int32_t* sorted_pairs,
+                         int32_t* pair_row, hipStream_t stream);
+
 // Quantization of a bf16 tensor of n values to E4M3 codes (scale 1 / inv),
 // run as extra blocks of the permutation's scatter launch (independent work).
 struct FusedQuant {
@@ -367,6 +379,17 @@ moe_status_t launch_gemm_mxfp4(moe_gemm_op_t op, const void* a, const int32_t* s
                                int topk, const int32_t* offsets, int S, int max_rows,
                                const uint8_t* w, const uint8_t* w_scale, int H, int I, void* c,
                                bool c_f32, hipStream_t stream);
+
+// The whole expert part of a few tokens' layer from the slot map, pair by
+// pair (no permutation): act [T * topk, I] = the SwiGLU rows, then out = the
+// weighted sum of the down products, with shared and accumulate as in
+// launch_combine.
+moe_status_t launch_mxfp4_pairs(const void* x, const int32_t* slot, const uint8_t* mask,
+                                const float* weight, int T, int topk, int S,
+                                const uint8_t* w_gate_up, const uint8_t* gate_up_scale,
+                                const uint8_t* w_down, const uint8_t* down_scale, int H, int I,
+                                void* act, void* out, bool out_bf16, int accumulate,
+                                const void* shared, hipStream_t stream);
 
 constexpr int kMaxNormWidth = 32768;
 // h = x + residual (null: x), the norm of h times gamma as y (dtype of x)

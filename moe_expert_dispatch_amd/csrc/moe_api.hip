@@ -121,6 +121,9 @@ moe_status_t launch_gemm(moe_gemm_op_t op, moe_dtype_t dt, const void* a, const 
              : launch_gemm_f32(op, a, offsets, S, max_rows, w, H, I, c, stream);
 }
 
+// Tokens up to which an MXFP4 layer takes its pairs one by one.
+constexpr int kPairTokens = 2;
+
 // Workspace of moe_forward, carved in this order (each 256-byte aligned).
 struct ForwardLayout {
   size_t ids, w, slot, w_masked, mask, offsets, sorted_pairs, pair_row, perm_ws, x_perm, act, xq;
@@ -427,7 +430,19 @@ moe_status_t moe_forward(const moe_config_t* cfg, const moe_forward_args_t* args
   MOE_TRY(mark(MOE_EV_START));
   const int32_t* ids_in = args->topk_ids;
   const float* w_in = args->topk_w;
-  if (args->logits) {
+  const bool on_input = cfg->routing_on_input != 0;
+  // MXFP4, few tokens: every pair by itself, without a permutation; a few
+  // more: routing, slot map and permutation in one launch or two
+  const bool pairs = mx && !on_input && T > 0 && T <= kPairTokens;
+  const bool plan = mx && !on_input && !pairs && T > 0 && T * K <= kPlanPairs;
+  if (plan) {
+    MOE_TRY(launch_plan(args->logits, T, cfg->E_global, K, cfg->renormalize ? 1 : 0,
+                        cfg->num_expert_group, cfg->topk_group,
+                        args->logits ? ids : const_cast<int32_t*>(ids_in),
+                        args->logits ? w : const_cast<float*>(w_in), cfg->ep_rank * E_local,
+                        E_local, args->rep_off, args->rep_slots, S, slot, w_masked, mask, offsets,
+                        sorted_pairs, pair_row, stream));
+  } else if (args->logits) {
     MOE_TRY(launch_route_map(args->logits, T, cfg->E_global, K, cfg->renormalize ? 1 : 0,
                              cfg->num_expert_group, cfg->topk_group, ids, w,
                              cfg->ep_rank * E_local, E_local, args->rep_off, args->rep_slots, S,
@@ -440,18 +455,28 @@ moe_status_t moe_forward(const moe_config_t* cfg, const moe_forward_args_t* args
   // bf16 with a direct-to-LDS shape: the gate/up GEMM fetches token rows of x
   // itself, so the permutation only orders the pairs (no x_perm copy).
   // Input-side routing gathers rows scaled by the pair weight instead.
-  const bool on_input = cfg->routing_on_input != 0;
   // FP8: x is quantized once per token and GEMM 1 gathers the code rows.
   const bool fused_gather =
       fp8 || (!on_input && (mx || (cfg->dtype == MOE_DTYPE_BF16 && gemm_bf16_gather_ok(T, H))));
   // FP8: x is quantized by extra blocks of the permutation's scatter launch
   const FusedQuant fq{static_cast<const uint16_t*>(args->x), (int64_t)T * H,
                       1.0f / cfg->a1_scale, xq_ws};
-  MOE_TRY(launch_permute(args->x, fp8 ? 2 : dtype_bytes(cfg->dtype), T, H, K, slot, mask, S,
-                         offsets, sorted_pairs, pair_row, fused_gather ? nullptr : x_perm,
-                         perm_ws, stream, on_input ? w_masked : nullptr,
-                         quant ? &fq : nullptr));
+  if (!pairs && !plan)
+    MOE_TRY(launch_permute(args->x, fp8 ? 2 : dtype_bytes(cfg->dtype), T, H, K, slot, mask, S,
+                           offsets, sorted_pairs, pair_row, fused_gather ? nullptr : x_perm,
+                           perm_ws, stream, on_input ? w_masked : nullptr,
+                           quant ? &fq : nullptr));
   MOE_TRY(mark(MOE_EV_PERMUTED));
+  if (pairs) {
+    MOE_TRY(launch_mxfp4_pairs(args->x, slot, mask, w_masked, T, K, S,
+                               static_cast<const uint8_t*>(args->w_gate_up), args->w_gate_up_e8m0,
+                               static_cast<const uint8_t*>(args->w_down), args->w_down_e8m0, H, I,
+                               act, args->out, cfg->out_dtype == MOE_DTYPE_BF16, cfg->accumulate,
+                               args->shared_out, stream));
+    MOE_TRY(mark(MOE_EV_GATE_UP));
+    MOE_TRY(mark(MOE_EV_DOWN));
+    return mark(MOE_EV_COMBINED);
+  }
   if (fp8)
     MOE_TRY(launch_gemm_fp8_gate_up_gathered(
         xq, T, K, sorted_pairs, offsets, S, T * K, static_cast<const uint8_t*>(args->w_gate_up),

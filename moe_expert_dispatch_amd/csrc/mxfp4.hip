@@ -187,20 +187,27 @@ __host__ __device__ inline int stream_window(int Kd, int RB, int WK) {
 // 16-byte vectors of a row in LDS: one more, so that rows start in other banks
 __host__ __device__ inline int stream_row_vecs(int window) { return window / 8 + 1; }
 
-template <int OP, bool GATHER, typename CT, int WK, int RB, int RUN, bool PIPE, bool ALIGNED>
+template <int OP, bool GATHER, typename CT, int WK, int RB, int RUN, bool PIPE, bool ALIGNED,
+          bool PAIRS = false>
 __global__ __launch_bounds__(64 * kStreamWaves) void mxfp4_stream_kernel(
     const uint16_t* __restrict__ a, const int32_t* __restrict__ offsets,
     const int32_t* __restrict__ sorted_pairs, int topk, int S, int max_rows, int find,
     const uint8_t* __restrict__ w, const uint8_t* __restrict__ w_scale, int N, int Kd,
-    CT* __restrict__ c) {
+    CT* __restrict__ c, const uint8_t* __restrict__ mask) {
   constexpr int M = OP == MOE_GEMM_GATE_UP_SWIGLU ? 2 : 1;  // matrices (gate and up, or down)
   constexpr int WN = kStreamWaves / WK;
   extern __shared__ uint4 lds[];
   int s, r0, r1;
-  if (!block_slot(offsets, S, max_rows, find != 0, &s, &r0, &r1)) return;
-  const int tid = threadIdx.x;
+  if constexpr (PAIRS) {  // a pair a line, row = pair; offsets holds the pairs' slots
+    r0 = blockIdx.y;
+    r1 = r0 + 1;
+    s = offsets[r0];
+    if (mask[r0] == 0 || s < 0 || s >= S) return;
+  } else {
+    if (!block_slot(offsets, S, max_rows, find != 0, &s, &r0, &r1)) return;
+  }
   const int lane = lane_id();
-  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
   const int wk = wave % WK, wn = wave / WK;
   const int m = lane & 15, g = lane >> 4;
   const int n0 = (blockIdx.x * WN + wn) * 16;
@@ -230,7 +237,10 @@ __global__ __launch_bounds__(64 * kStreamWaves) void mxfp4_stream_kernel(
         const int r = u / pieces;
         const int v = (u - r * pieces) * kWave + lane;
         int row = rt + r;
-        if constexpr (GATHER) row = sorted_pairs[row] / topk;
+        if constexpr (PAIRS)
+          row = row / topk;
+        else if constexpr (GATHER)
+          row = sorted_pairs[row] / topk;
         if (v < window / 8)
           lds[r * rvecs + v] =
               base + 8 * v < Kd
@@ -703,6 +713,88 @@ __global__ __launch_bounds__(512, U == 2 ? 2 : 1) void mxfp4_split_kernel(
   }
 }
 
+// ---------------------------------------------------------------- a few tokens
+// The down product of a token's pairs and their weighted sum in one: block
+// (16 output columns, token). The waves share the token's (pair, run of 512
+// k's) units; each adds weight * partial product to its sums, and the sums
+// are added in LDS in wave order. Of the 16 token columns of the matrix
+// instruction one is used: the codes' stream, not the product, is the bound.
+template <typename OT, bool ALIGNED>
+__global__ __launch_bounds__(512) void mxfp4_pair_down_kernel(
+    const uint16_t* __restrict__ act, const int32_t* __restrict__ slot,
+    const uint8_t* __restrict__ mask, const float* __restrict__ weight, int topk, int S,
+    const uint8_t* __restrict__ w, const uint8_t* __restrict__ w_scale, int N, int Kd,
+    OT* __restrict__ out, int accumulate, const uint16_t* __restrict__ shared) {
+  constexpr int RUN = 4;
+  __shared__ floatx4 red[kStreamWaves][4];
+  const int lane = lane_id();
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
+  const int m = lane & 15, g = lane >> 4;
+  const int n0 = blockIdx.x * 16;
+  const int t = blockIdx.y;
+  const uint32_t row[1] = {(uint32_t)(n0 + m)};
+  const int runs = ceil_div(Kd, 128 * RUN);
+  floatx4 sum = {0.f, 0.f, 0.f, 0.f};
+  for (int u = wave; u < topk * runs; u += kStreamWaves) {
+    const int p = t * topk + u / runs;
+    const int k0 = (u % runs) * 128 * RUN;
+    const int s = slot[p];
+    if (mask[p] == 0 || s < 0 || s >= S) continue;  // the same for the whole wave
+    const float wt = weight[p];
+    StepWeights<1, RUN> v;
+    load_step<1, RUN, ALIGNED>(v, w + (size_t)s * N * (size_t)(Kd / 2),
+                               w_scale + (size_t)s * N * (size_t)(Kd / 32), row, Kd, k0,
+                               min(k0 + 128 * RUN, Kd), g);
+    const uint16_t* x = act + (size_t)p * Kd + k0 + 32 * g;
+    uint4 b[RUN][4];
+#pragma unroll
+    for (int j = 0; j < RUN; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        b[j][e] = m == 0 && k0 + 128 * j + 32 * g < Kd
+                      ? *reinterpret_cast<const uint4*>(x + 128 * j + 8 * e)
+                      : make_uint4(0, 0, 0, 0);
+    floatx4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < RUN; ++j) {
+      const float sc = e8m0((v.s[0][j] >> (8 * g)) & 255u);
+      const uint32_t qq[4] = {v.q[0][j].x, v.q[0][j].y, v.q[0][j].z, v.q[0][j].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+            __builtin_bit_cast(bf16x8_t, cvt8(qq[e], sc)), __builtin_bit_cast(bf16x8_t, b[j][e]),
+            acc, 0, 0, 0);
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) sum[r] = fmaf(wt, acc[r], sum[r]);
+  }
+  if (m == 0) red[wave][g] = sum;
+  __syncthreads();
+  if (threadIdx.x < 4) {
+    floatx4 o = red[0][threadIdx.x];
+    for (int v = 1; v < kStreamWaves; ++v) o += red[v][threadIdx.x];
+    const size_t at = (size_t)t * N + n0 + 4 * threadIdx.x;
+    if (shared != nullptr) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) o[r] += bf16_to_f32(shared[at + r]);
+    }
+    OT* p = out + at;
+    if constexpr (sizeof(OT) == 2) {
+      if (accumulate) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) o[r] = bf16_to_f32(p[r]) + o[r];
+      }
+      *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+    } else {
+      if (accumulate) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) o[r] = p[r] + o[r];
+      }
+      *reinterpret_cast<float4*>(p) = make_float4(o[0], o[1], o[2], o[3]);
+    }
+  }
+}
+
 // Which kernel, by the rows a slot has on the average of all (max_rows / S:
 // the host knows no more).
 constexpr int kStreamRows = 10;
@@ -758,7 +850,8 @@ void launch_product(const void* a, const int32_t* offsets, const int32_t* sorted
                         decltype(al)::value>
         <<<dim3(ceil_div(N, 16 * kStreamWaves / WK), lines), 64 * kStreamWaves,
            rows_lds > red_lds ? rows_lds : red_lds, stream>>>(
-            a16, offsets, sorted_pairs, topk, S, max_rows, max_rows < S, w, w_scale, N, Kd, ct);
+            a16, offsets, sorted_pairs, topk, S, max_rows, max_rows < S, w, w_scale, N, Kd, ct,
+            nullptr);
   };
   // The contraction is split among waves where the columns alone leave the
   // chip without a block for every compute unit, and where it is short: up to 1024
@@ -856,6 +949,57 @@ moe_status_t launch_gemm_mxfp4(moe_gemm_op_t op, const void* a, const int32_t* s
   } else {
     launch_product<MOE_GEMM_DOWN, false, uint16_t>(a, offsets, nullptr, 1, S, max_rows, w,
                                                    w_scale, H, I, c, stream);
+  }
+  return launch_status();
+}
+
+moe_status_t launch_mxfp4_pairs(const void* x, const int32_t* slot, const uint8_t* mask,
+                                const float* weight, int T, int topk, int S,
+                                const uint8_t* w_gate_up, const uint8_t* gate_up_scale,
+                                const uint8_t* w_down, const uint8_t* down_scale, int H, int I,
+                                void* act, void* out, bool out_bf16, int accumulate,
+                                const void* shared, hipStream_t stream) {
+  using std::integral_constant;
+  const int P = T * topk;
+  uint16_t* act16 = static_cast<uint16_t*>(act);
+  auto gate_up = [&](auto wk, auto pipe, auto al) {
+    constexpr int WK = decltype(wk)::value, RB = 8;
+    constexpr int RUN = decltype(pipe)::value ? 2 : 4;
+    const size_t rows_lds = (size_t)stream_row_vecs(stream_window(H, RB, WK)) * 16;  // one row
+    const size_t red_lds = WK > 1 ? (size_t)kStreamWaves * 2 * kWave * 16 : 0;
+    mxfp4_stream_kernel<MOE_GEMM_GATE_UP_SWIGLU, true, uint16_t, WK, RB, RUN,
+                        decltype(pipe)::value, decltype(al)::value, true>
+        <<<dim3(ceil_div(I, 16 * kStreamWaves / WK), P), 64 * kStreamWaves,
+           rows_lds > red_lds ? rows_lds : red_lds, stream>>>(
+            static_cast<const uint16_t*>(x), slot, nullptr, topk, S, P, 0, w_gate_up,
+            gate_up_scale, I, H, act16, mask);
+  };
+  if (H % 128 != 0)
+    gate_up(integral_constant<int, 8>{}, std::true_type{}, std::false_type{});
+  else if (H > 4096)
+    gate_up(integral_constant<int, 8>{}, std::true_type{}, std::true_type{});
+  else if (H > 2048)
+    gate_up(integral_constant<int, 8>{}, std::false_type{}, std::true_type{});
+  else
+    gate_up(integral_constant<int, 4>{}, std::false_type{}, std::true_type{});
+  const moe_status_t st = launch_status();
+  if (st != MOE_OK) return st;
+  auto down = [&](auto o, auto al) {
+    using OT = decltype(o);
+    mxfp4_pair_down_kernel<OT, decltype(al)::value><<<dim3(H / 16, T), 512, 0, stream>>>(
+        act16, slot, mask, weight, topk, S, w_down, down_scale, H, I, static_cast<OT*>(out),
+        accumulate, static_cast<const uint16_t*>(shared));
+  };
+  if (out_bf16) {
+    if (I % 128 == 0)
+      down(uint16_t{}, std::true_type{});
+    else
+      down(uint16_t{}, std::false_type{});
+  } else {
+    if (I % 128 == 0)
+      down(float{}, std::true_type{});
+    else
+      down(float{}, std::false_type{});
   }
   return launch_status();
 }

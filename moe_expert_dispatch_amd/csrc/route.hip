@@ -82,20 +82,13 @@ __device__ __forceinline__ void sort_desc(uint64_t (&k)[N]) {
   }
 }
 
-// L lanes per token, EPL logits per lane (a power of two); K <= L,
-// E <= L * EPL. Lanes of
-// tokens past T carry empty keys and store nothing, but stay active, so every
-// DPP step reads live lanes.
-template <int L, int EPL, bool MAP>
-__global__ __launch_bounds__(256) void route_lanes_kernel(const float* __restrict__ logits,
-                                                          int T, int E, int K, int renorm,
-                                                          int32_t* __restrict__ ids,
-                                                          float* __restrict__ w, MapOut mo) {
-  const int q = threadIdx.x & (L - 1);
-  const int t = (int)((blockIdx.x * blockDim.x + threadIdx.x) / L);
-  const bool live = t < T;
-  const float* row = logits + (size_t)(live ? t : 0) * E;
-
+// The selection of one token by the L lanes of its group (q: the lane in it):
+// lane q < K ends with the q-th expert and its weight. EPL logits per lane (a
+// power of two); K <= L, E <= L * EPL. Lanes of tokens that do not exist (not
+// live) carry empty keys, but stay active, so every DPP step reads live lanes.
+template <int L, int EPL>
+__device__ __forceinline__ void route_token(const float* __restrict__ row, bool live, int E, int K,
+                                            int renorm, int q, int* id, float* weight) {
   float v[EPL];
   uint64_t key[EPL];
 #pragma unroll
@@ -139,14 +132,116 @@ __global__ __launch_bounds__(256) void route_lanes_kernel(const float* __restric
     const float s = group_sum<L>(p);
     p = p / s;
   }
+  *id = (int)(0xffffffffu - (uint32_t)my_key);
+  *weight = p;
+}
+
+template <int L, int EPL, bool MAP>
+__global__ __launch_bounds__(256) void route_lanes_kernel(const float* __restrict__ logits,
+                                                          int T, int E, int K, int renorm,
+                                                          int32_t* __restrict__ ids,
+                                                          float* __restrict__ w, MapOut mo) {
+  const int q = threadIdx.x & (L - 1);
+  const int t = (int)((blockIdx.x * blockDim.x + threadIdx.x) / L);
+  const bool live = t < T;
+  int id;
+  float p;
+  route_token<L, EPL>(logits + (size_t)(live ? t : 0) * E, live, E, K, renorm, q, &id, &p);
   if (live && q < K) {
-    const int id = (int)(0xffffffffu - (uint32_t)my_key);
     const int pi = t * K + q;
     ids[pi] = id;
     w[pi] = p;
     if constexpr (MAP)
       map_pair(pi, t, id, p, mo.start, mo.E_local, mo.rep_off, mo.rep_slots, mo.S, mo.slot,
                mo.w_masked, mo.mask);
+  }
+}
+
+// A plan in one block, for the few pairs of a decoding batch (P <=
+// kPlanPairs): the counting sort of launch_permute with the same results, and
+// before it, where the block's lanes hold all tokens at once (L > 1), routing
+// and slot map. L == 1: the slot map is given. A wave holds 64 pairs in pair
+// order; a pair's rank in its slot is the number of lower lanes with the same
+// slot (one ballot per bit of the slot id) plus what the earlier waves hold
+// of it (counts in LDS).
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanWaves = kPlanThreads / kWave;
+static_assert(kPlanThreads >= MOE_MAX_SLOTS && kPlanThreads >= kPlanPairs,
+              "a thread for every slot and pair");
+
+template <int L, int EPL>
+__global__ __launch_bounds__(kPlanThreads) void plan_kernel(
+    const float* __restrict__ logits, int T, int E, int K, int renorm, MapOut mo,
+    int32_t* __restrict__ offsets, int32_t* __restrict__ sorted_pairs,
+    int32_t* __restrict__ pair_row) {
+  extern __shared__ int32_t wave_count[];  // [waves with pairs][S]
+  __shared__ int32_t pair_slot[kPlanPairs];  // -1: not included
+  __shared__ int32_t first[MOE_MAX_SLOTS];
+  __shared__ int32_t wsum[kPlanWaves];
+  const int tid = threadIdx.x;
+  const int lane = lane_id();
+  const int wave = tid / kWave;
+  const int P = T * K;
+  const int S = mo.S;
+  const int nw = ceil_div(P, kWave);
+  for (int i = tid; i < nw * S; i += kPlanThreads) wave_count[i] = 0;
+  if constexpr (L > 1) {
+    const int q = tid & (L - 1);
+    const int t = tid / L;
+    const bool live = t < T;
+    int id;
+    float p;
+    route_token<L, EPL>(logits + (size_t)(live ? t : 0) * E, live, E, K, renorm, q, &id, &p);
+    if (live && q < K) {
+      const int pi = t * K + q;
+      const int s = map_pair(pi, t, id, p, mo.start, mo.E_local, mo.rep_off, mo.rep_slots, S,
+                             mo.slot, mo.w_masked, mo.mask);
+      pair_slot[pi] = id >= mo.start && id < mo.start + mo.E_local ? s : -1;
+    }
+  } else if (tid < P) {
+    const int s = mo.slot[tid];
+    pair_slot[tid] = mo.mask[tid] != 0 && s >= 0 && s < S ? s : -1;
+  }
+  __syncthreads();
+  const int s = tid < P ? pair_slot[tid] : -1;
+  const int sbits = S > 1 ? 32 - __clz(S - 1) : 0;
+  uint64_t same = __ballot(s >= 0);
+  for (int bit = 0; bit < sbits; ++bit) {
+    const bool on = (s >> bit) & 1;
+    const uint64_t ones = __ballot(s >= 0 && on);
+    same &= on ? ones : ~ones;
+  }
+  const uint64_t below = same & lanemask_lt();
+  if (s >= 0 && below == 0) wave_count[wave * S + s] = __popcll(same);
+  __syncthreads();
+  // exclusive scan of the slots' counts, a slot a thread
+  int n = 0;
+  if (tid < S)
+    for (int v = 0; v < nw; ++v) n += wave_count[v * S + tid];
+  int incl = n;
+#pragma unroll
+  for (int o = 1; o < kWave; o <<= 1) {
+    const int v = __shfl_up(incl, o, kWave);
+    if (lane >= o) incl += v;
+  }
+  if (lane == kWave - 1) wsum[wave] = incl;
+  __syncthreads();
+  int at = incl - n;
+  for (int v = 0; v < wave; ++v) at += wsum[v];
+  if (tid < S) {
+    first[tid] = at;
+    offsets[tid] = at;
+    if (tid == S - 1) offsets[S] = at + n;
+  }
+  __syncthreads();
+  if (tid < P) {
+    int row = -1;
+    if (s >= 0) {
+      row = first[s] + __popcll(below);
+      for (int v = 0; v < wave; ++v) row += wave_count[v * S + s];
+      sorted_pairs[row] = tid;
+    }
+    pair_row[tid] = row;
   }
 }
 
@@ -305,6 +400,27 @@ void launch_lanes_any(int L, const float* logits, int T, int E, int K, int renor
     launch_lanes<32, MAP>(logits, T, E, K, renorm, ids, w, mo, stream);
 }
 
+size_t plan_lds(int P, int S) { return (size_t)ceil_div(P, kWave) * S * sizeof(int32_t); }
+
+template <int L>
+void launch_plan_lanes(const float* logits, int T, int E, int K, int renorm, const MapOut& mo,
+                       int32_t* offsets, int32_t* sorted_pairs, int32_t* pair_row,
+                       hipStream_t stream) {
+  auto go = [&](auto epl) {
+    plan_kernel<L, decltype(epl)::value><<<1, kPlanThreads, plan_lds(T * K, mo.S), stream>>>(
+        logits, T, E, K, renorm, mo, offsets, sorted_pairs, pair_row);
+  };
+  const int epl = ceil_div(E, L);
+  if (epl <= 1)
+    go(std::integral_constant<int, 1>{});
+  else if (epl <= 2)
+    go(std::integral_constant<int, 2>{});
+  else if (epl <= 4)
+    go(std::integral_constant<int, 4>{});
+  else
+    go(std::integral_constant<int, 8>{});
+}
+
 }  // namespace
 
 moe_status_t launch_route_map(const float* logits, int T, int E, int K, int renorm, int G,
@@ -330,6 +446,34 @@ moe_status_t launch_route(const float* logits, int T, int E, int K, int renorm, 
     return launch_status();
   }
   launch_waves<false>(logits, T, E, K, renorm, G, TG, ids, w, MapOut{}, stream);
+  return launch_status();
+}
+
+moe_status_t launch_plan(const float* logits, int T, int E, int K, int renorm, int G, int TG,
+                         int32_t* ids, float* w, int start, int E_local, const int32_t* rep_off,
+                         const int32_t* rep_slots, int S, int32_t* slot, float* w_masked,
+                         uint8_t* mask, int32_t* offsets, int32_t* sorted_pairs,
+                         int32_t* pair_row, hipStream_t stream) {
+  const MapOut mo{start, E_local, S, rep_off, rep_slots, slot, w_masked, mask};
+  const int L = logits != nullptr ? lanes_for(E, K, G) : 0;
+  if (L > 0 && T * L <= kPlanThreads) {
+    if (L == 8)
+      launch_plan_lanes<8>(logits, T, E, K, renorm, mo, offsets, sorted_pairs, pair_row, stream);
+    else if (L == 16)
+      launch_plan_lanes<16>(logits, T, E, K, renorm, mo, offsets, sorted_pairs, pair_row, stream);
+    else
+      launch_plan_lanes<32>(logits, T, E, K, renorm, mo, offsets, sorted_pairs, pair_row, stream);
+    return launch_status();
+  }
+  const moe_status_t st =
+      logits != nullptr
+          ? launch_route_map(logits, T, E, K, renorm, G, TG, ids, w, start, E_local, rep_off,
+                             rep_slots, S, slot, w_masked, mask, stream)
+          : launch_slot_map(ids, w, T, K, start, E_local, rep_off, rep_slots, S, slot, w_masked,
+                            mask, stream);
+  if (st != MOE_OK) return st;
+  plan_kernel<1, 1><<<1, kPlanThreads, plan_lds(T * K, S), stream>>>(
+      nullptr, T, E, K, renorm, mo, offsets, sorted_pairs, pair_row);
   return launch_status();
 }
 

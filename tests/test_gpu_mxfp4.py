@@ -225,6 +225,12 @@ def _reference(L, T, ids, w, rank=0, on_input=False):
 LAYERS = {
     "one_token": dict(T=1, H=256, I=96, E=8, K=2, seed=1),
     "one_token_ep": dict(T=1, H=512, I=64, E=16, K=4, seed=2, ep=4),
+    "two_tokens": dict(T=2, H=4224, I=608, E=12, K=5, seed=10, ep=2, extra=2),
+    "two_odd": dict(T=2, H=160, I=96, E=6, K=6, seed=11, extra=1),
+    "long_rows": dict(T=3, H=5216, I=1056, E=3, K=2, seed=12),
+    "plan_limit": dict(T=128, H=64, I=32, E=24, K=8, seed=13, extra=5),
+    "past_plan": dict(T=129, H=64, I=32, E=24, K=8, seed=14, ep=2),
+    "many_experts": dict(T=6, H=64, I=32, E=512, K=6, seed=15),
     "few": dict(T=5, H=320, I=160, E=12, K=3, seed=3),
     "replicas": dict(T=33, H=128, I=128, E=8, K=4, seed=4, extra=3),
     "skewed": dict(T=200, H=256, I=64, E=10, K=2, seed=5, skew=3.0),
