@@ -225,6 +225,9 @@ __global__ __launch_bounds__(64 * kStreamWaves) void mxfp4_stream_kernel(
 
   for (int rt = r0; rt < r1; rt += RB) {
     const int nr = min(r1 - rt, RB);
+    // keeps the first loads, and with them the conversions, from being moved
+    // out of the loop, where the converted codes would fill 128 registers
+    asm volatile("" ::: "memory");
     floatx4 acc[M];
 #pragma unroll
     for (int i = 0; i < M; ++i) acc[i] = floatx4{0.f, 0.f, 0.f, 0.f};
@@ -303,6 +306,104 @@ __global__ __launch_bounds__(64 * kStreamWaves) void mxfp4_stream_kernel(
         *reinterpret_cast<float4*>(p) = make_float4(o[0], o[1], o[2], o[3]);
     }
     if (rt + RB < r1) __syncthreads();  // rows and partial sums are read
+  }
+}
+
+// The same for contractions of at most 512 WK k's and very few rows: a wave's
+// part is one step, and it keeps its own k's of the rows, RB = 4 of them, in
+// its own LDS, so waves meet only to add up. Many short blocks leave no tail:
+// T = 16 over 64 experts in 80 slots (66 with rows, 8 columns tiles of 128
+// each: 528 blocks of the kernel below for 256 places) 66 against 77 us.
+template <int OP, bool GATHER, typename CT, int WK>
+__global__ __launch_bounds__(64 * kStreamWaves) void mxfp4_quick_kernel(
+    const uint16_t* __restrict__ a, const int32_t* __restrict__ offsets,
+    const int32_t* __restrict__ sorted_pairs, int topk, int S, int max_rows, int find,
+    const uint8_t* __restrict__ w, const uint8_t* __restrict__ w_scale, int N, int Kd,
+    CT* __restrict__ c) {
+  constexpr int M = OP == MOE_GEMM_GATE_UP_SWIGLU ? 2 : 1;
+  constexpr int WN = kStreamWaves / WK;
+  constexpr int RUN = 4;
+  constexpr int RB = 4;
+  constexpr int kRowVecs = 128 * RUN / 8 + 1;
+  __shared__ uint4 lds[kStreamWaves][RB * kRowVecs];
+  __shared__ floatx4 red[WK > 1 ? kStreamWaves : 1][M][kWave];
+  int s, r0, r1;
+  if (!block_slot(offsets, S, max_rows, find != 0, &s, &r0, &r1)) return;
+  const int lane = lane_id();
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
+  const int wk = wave % WK, wn = wave / WK;
+  const int m = lane & 15, g = lane >> 4;
+  const int n0 = (blockIdx.x * WN + wn) * 16;
+  const bool tile = n0 < N;
+  uint32_t wrow[M];
+#pragma unroll
+  for (int i = 0; i < M; ++i) wrow[i] = (uint32_t)(i * N + (tile ? n0 : 0) + m);
+  const size_t rows_s = (size_t)s * M * N;
+  const uint8_t* ws = w + rows_s * (size_t)(Kd / 2);
+  const uint8_t* ss = w_scale + rows_s * (size_t)(Kd / 32);
+  const int per = ceil_div(Kd / 128, WK) * 128;  // at most 128 * RUN
+  const int k0 = wk * per;
+  const int kend = min(k0 + per, Kd);
+  for (int rt = r0; rt < r1; rt += RB) {
+    // keeps the loads, and with them the conversions, from being moved out of the loop, where
+    // the converted codes would fill 128 registers
+    asm volatile("" ::: "memory");
+    const int nr = min(r1 - rt, RB);
+    StepWeights<M, RUN> v;
+    load_step<M, RUN, true>(v, ws, ss, wrow, Kd, k0, kend, g);
+    for (int r = 0; r < nr; ++r) {
+      int row = rt + r;
+      if constexpr (GATHER) row = sorted_pairs[row] / topk;
+      lds[wave][r * kRowVecs + lane] =
+          k0 + 8 * lane < kend
+              ? *reinterpret_cast<const uint4*>(a + (size_t)row * Kd + k0 + 8 * lane)
+              : make_uint4(0, 0, 0, 0);
+    }
+    __builtin_amdgcn_wave_barrier();  // LDS accesses of a wave run in order
+    floatx4 acc[M];
+#pragma unroll
+    for (int i = 0; i < M; ++i) acc[i] = floatx4{0.f, 0.f, 0.f, 0.f};
+    const uint4* x = &lds[wave][(m < nr ? m : 0) * kRowVecs + 4 * g];
+#pragma unroll
+    for (int j = 0; j < RUN; ++j) {
+      uint4 b[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) b[e] = m < nr ? x[16 * j + e] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < M; ++i) {
+        const float sc = e8m0((v.s[i][j] >> (8 * g)) & 255u);
+        const uint32_t qq[4] = {v.q[i][j].x, v.q[i][j].y, v.q[i][j].z, v.q[i][j].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              __builtin_bit_cast(bf16x8_t, cvt8(qq[e], sc)), __builtin_bit_cast(bf16x8_t, b[e]),
+              acc[i], 0, 0, 0);
+      }
+    }
+    if constexpr (WK > 1) {
+#pragma unroll
+      for (int i = 0; i < M; ++i) red[wave][i][lane] = acc[i];
+      __syncthreads();
+      if (wk == 0) {
+#pragma unroll
+        for (int i = 0; i < M; ++i)
+          for (int u = 1; u < WK; ++u) acc[i] += red[wave + u][i][lane];
+      }
+    }
+    if (wk == 0 && tile && m < nr) {
+      float o[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        o[r] = acc[0][r];
+        if constexpr (M == 2) o[r] = o[r] / (1.0f + expf(-o[r])) * acc[1][r];
+      }
+      CT* p = c + (size_t)(rt + m) * N + n0 + 4 * g;
+      if constexpr (sizeof(CT) == 2)
+        *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+      else
+        *reinterpret_cast<float4*>(p) = make_float4(o[0], o[1], o[2], o[3]);
+    }
+    if (WK > 1 && rt + RB < r1) __syncthreads();
   }
 }
 
@@ -862,12 +963,29 @@ void launch_product(const void* a, const int32_t* offsets, const int32_t* sorted
   while (split < kStreamWaves && split * 512 < Kd &&
          (long long)ceil_div(N, 16 * kStreamWaves / split) * lines < want)
     split *= 2;
-  const bool one = ceil_div(ceil_div(Kd, 128), split) <= 4;  // one step of 512 a wave
   using i1 = integral_constant<int, 1>;
   using i2 = integral_constant<int, 2>;
   using i4 = integral_constant<int, 4>;
   using i8 = integral_constant<int, 8>;
+  if constexpr (M == 2) {
+    if (aligned && Kd > 1024 && Kd <= 4096 && max_rows <= 2 * S && lines >= 16) {
+      auto quick = [&](auto wk) {
+        constexpr int WK = decltype(wk)::value;
+        mxfp4_quick_kernel<OP, GATHER, CT, WK>
+            <<<dim3(ceil_div(N, 16 * kStreamWaves / WK), lines), 64 * kStreamWaves, 0, stream>>>(
+                a16, offsets, sorted_pairs, topk, S, max_rows, max_rows < S, w, w_scale, N, Kd, ct);
+      };
+      if (Kd <= 2048)
+        quick(i4{});
+      else
+        quick(i8{});
+      return;
+    }
+  }
   auto pick = [&](auto rb) {
+    // one window, and of it one step of 512 a wave
+    const int window = stream_window(Kd, decltype(rb)::value, split);
+    const bool one = window >= Kd && window <= 512 * split;
     if (!aligned) {
       if (split == 1)
         go(i1{}, rb, i2{}, std::true_type{}, std::false_type{});
@@ -884,12 +1002,18 @@ void launch_product(const void* a, const int32_t* offsets, const int32_t* sorted
         go(i8{}, rb, i4{}, std::false_type{}, std::true_type{});
     } else if (split > 1) {
       go(i8{}, rb, i2{}, std::true_type{}, std::true_type{});
-    } else if (M == 1 || (Kd >= 4096 && decltype(rb)::value == 8)) {
-      // 512 a step: one block of gate/up a compute unit (164 registers), 60 against 66 us at
-      // S = 64, N = 1024, Kd = 4096; at Kd = 2048 two blocks with steps of 256 win, 15.5
-      // against 16.6 us (N = 512)
+    } else if constexpr (M == 1) {
       go(i1{}, rb, i4{}, std::true_type{}, std::true_type{});
     } else {
+      // 512 a step: one block of gate/up a compute unit (164 registers), 60 against 66 us at
+      // S = 64, N = 1024, Kd = 4096; at Kd = 2048 two blocks with steps of 256 win, 15.5
+      // against 16.6 us (N = 512), and with 16 rows everywhere (71 against 75 us)
+      if constexpr (decltype(rb)::value == 8) {
+        if (Kd >= 4096) {
+          go(i1{}, rb, i4{}, std::true_type{}, std::true_type{});
+          return;
+        }
+      }
       go(i1{}, rb, i2{}, std::true_type{}, std::true_type{});
     }
   };

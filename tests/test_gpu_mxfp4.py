@@ -104,6 +104,36 @@ def _offsets(sizes):
     return torch.tensor(np.concatenate([[0], np.cumsum(sizes)]), dtype=torch.int32)
 
 
+def _products_check(sizes, H, I):
+    dev = device()
+    announce(f"mxfp4 products {sizes} H={H} I={I}")
+    S, rows, off = len(sizes), int(sum(sizes)), _offsets(sizes)
+    gu, gs = _weights((S, 2 * I, H), H + I, H)
+    wd, ds = _weights((S, H, I), H * 3 + I, I)
+    x = _rows(rows, H, rows + H)
+    act = moe.grouped_gemm_mxfp4(moe.GATE_UP_SWIGLU, x.to(dev), off.to(dev), gu.to(dev), gs.to(dev))
+    want, g, u, gm, um = oracle.mxfp4_grouped_gate_up(x, off, gu, gs, I)
+    dg, du = 2 * H * U * gm, 2 * H * U * um
+    tol = (1.1 * dg * (np.abs(u) + du) + np.abs(oracle.silu(g)) * du + (2.0 ** -8 + 16 * U) * np.abs(want)) * 1.01
+    assert (np.abs(np64(act) - want) <= tol + 1e-38).all()
+    y = moe.grouped_gemm_mxfp4(moe.DOWN, act, off.to(dev), wd.to(dev), ds.to(dev), c_dtype=torch.float32)
+    want, m = oracle.mxfp4_grouped_down(act.cpu(), off, wd, ds)
+    assert (np.abs(np64(y) - want) <= (2 * I * U * m + 2 * U * np.abs(want)) * 1.01 + 1e-38).all()
+
+
+# every way the products are split: rows a slot (up to 2, 4, 10, 24, 56 and more on the average, with
+# slots far over and under it) by short, middle and long contractions and ones that are no multiple of 128
+ROWS = {"two": [2, 0, 1, 9, 0, 2] * 4, "four": [4, 0, 9, 3], "ten": [0, 10, 17, 13], "twenty": [33, 0, 40, 7],
+        "fifty": [65, 50, 0, 70], "hundred": [1, 300, 0, 96]}
+
+
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("H,I", [(96, 1056), (384, 640), (1152, 160), (2176, 64), (3968, 32), (4096, 32), (4128, 32),
+                                 (8320, 32), (9248, 32)])
+def test_products_every_split(rows, H, I):
+    _products_check(ROWS[rows], H, I)
+
+
 @pytest.mark.parametrize("sizes", SIZES, ids=str)
 @pytest.mark.parametrize("H,I", [(32, 32), (64, 96), (160, 32), (512, 224), (1024, 128), (2048, 64)])
 def test_products_against_oracle(sizes, H, I):
