@@ -144,6 +144,12 @@ def _stream() -> int:
     return torch.cuda.current_stream().cuda_stream
 
 
+# The current stream's handle by device index: torch.cuda.current_stream() builds an object for
+# it, which took longer than a small kernel runs (about 2 us of a 12 us call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
@@ -151,15 +157,15 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 def _dev(t: torch.Tensor, name: str, dtype=None, shape=None) -> torch.Tensor:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a device (HIP) tensor, got {t.device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if dtype is not None:
+    if dtype is not None and t.dtype != dtype:
         ok = dtype if isinstance(dtype, tuple) else (dtype,)
         if t.dtype not in ok:
             raise TypeError(f"{name} has dtype {t.dtype}, expected {ok}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     return t
 
@@ -168,12 +174,21 @@ def _empty(shape, dtype, like: torch.Tensor) -> torch.Tensor:
     return torch.empty(shape, dtype=dtype, device=like.device)
 
 
-def _on(t: torch.Tensor, *others: Optional[torch.Tensor]):
-    """A context in which t's device is the current one; the others have to be on it too."""
+def _launch(what: str, like: torch.Tensor, others: Sequence[Optional[torch.Tensor]], *args) -> None:
+    """Calls entry point `what` with args and the current stream of like's device, which is made
+    the current device for the call; the other tensors have to be on it too."""
+    dev = like.get_device()
     for o in others:
-        if o is not None and o.device != t.device:
-            raise ValueError(f"tensors on {t.device} and {o.device}: one device is needed")
-    return torch.cuda.device(t.device)
+        if o is not None and o.get_device() != dev:
+            raise ValueError(f"tensors on {like.device} and {o.device}: one device is needed")
+    fn = getattr(_lib or lib(), what)
+    if torch.cuda.current_device() == dev:
+        code = fn(*args, _raw_stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            code = fn(*args, _raw_stream(dev))
+    if code != 0:
+        _check(code, what)
 
 
 # ---------------------------------------------------------------- stages
@@ -390,9 +405,8 @@ def quantize_mxfp4(w: torch.Tensor, codes: Optional[torch.Tensor] = None,
              else _dev(codes, "codes", torch.uint8, (*lead, K // 2)))
     scale = (_empty((*lead, K // MX_GROUP), torch.uint8, w) if scale is None
              else _dev(scale, "scale", torch.uint8, (*lead, K // MX_GROUP)))
-    with _on(w, codes, scale):
-        _check(lib().moe_quantize_mxfp4(_ptr(w), _DT[w.dtype], w.numel(), _ptr(codes),
-                                        _ptr(scale), _stream()), "moe_quantize_mxfp4")
+    _launch("moe_quantize_mxfp4", w, (codes, scale), w.data_ptr(), _DT[w.dtype], w.numel(),
+            codes.data_ptr(), scale.data_ptr())
     return codes, scale
 
 
@@ -412,9 +426,8 @@ def dequantize_mxfp4(codes: torch.Tensor, scale: torch.Tensor,
         out = _empty((*lead, K), dtype, codes)
     else:
         _dev(out, "out", (torch.float32, torch.bfloat16), (*lead, K))
-    with _on(codes, scale, out):
-        _check(lib().moe_dequantize_mxfp4(_ptr(codes), _ptr(scale), out.numel(), _ptr(out),
-                                          _DT[out.dtype], _stream()), "moe_dequantize_mxfp4")
+    _launch("moe_dequantize_mxfp4", codes, (scale, out), codes.data_ptr(), scale.data_ptr(),
+            out.numel(), out.data_ptr(), _DT[out.dtype])
     return out
 
 
@@ -450,10 +463,9 @@ def grouped_gemm_mxfp4(op: int, a: torch.Tensor, offsets: torch.Tensor, w: torch
         c = _empty((rows, cols), c_dtype, a)
     else:
         _dev(c, "c", kinds, (rows, cols))
-    with _on(a, offsets, w, w_scale, c):
-        _check(lib().moe_grouped_gemm_mxfp4(op, _ptr(a), _ptr(offsets), S, rows, _ptr(w),
-                                            _ptr(w_scale), H, I, _ptr(c), _DT[c.dtype],
-                                            _stream()), "moe_grouped_gemm_mxfp4")
+    _launch("moe_grouped_gemm_mxfp4", a, (offsets, w, w_scale, c), op, a.data_ptr(),
+            offsets.data_ptr(), S, rows, w.data_ptr(), w_scale.data_ptr(), H, I, c.data_ptr(),
+            _DT[c.dtype])
     return c
 
 
@@ -484,11 +496,9 @@ def rms_norm(x: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-6,
     elif q is not None:
         raise ValueError("q needs a q_scale")
     y = torch.empty_like(x) if y is None else _dev(y, "y", x.dtype, (T, H))
-    with _on(x, gamma, residual, residual_out, y, q):
-        _check(lib().moe_rms_norm(_ptr(x), _ptr(residual), _ptr(gamma), _DT[x.dtype], T, H,
-                                  float(eps), _ptr(residual_out), _ptr(y), _ptr(q),
-                                  0.0 if q_scale is None else float(q_scale), _stream()),
-               "moe_rms_norm")
+    _launch("moe_rms_norm", x, (gamma, residual, residual_out, y, q), x.data_ptr(),
+            _ptr(residual), gamma.data_ptr(), _DT[x.dtype], T, H, eps, _ptr(residual_out),
+            y.data_ptr(), _ptr(q), 0.0 if q_scale is None else q_scale)
     return y, residual_out, q
 
 
@@ -520,11 +530,9 @@ def balance_loss(logits: torch.Tensor, ids: torch.Tensor, coef: float,
     loss = _empty((), torch.float32, logits)
     if ws is None:
         ws = _empty((max(balance_loss_workspace_size(T, E, K), 1),), torch.uint8, logits)
-    with _on(logits, ids, token_mask, ws):
-        _check(lib().moe_balance_loss(_ptr(logits), _ptr(ids), _ptr(token_mask), T, E, K,
-                                      float(coef), _ptr(counts), _ptr(prob), _ptr(loss),
-                                      _ptr(ws), ws.numel() * ws.element_size(), _stream()),
-               "moe_balance_loss")
+    _launch("moe_balance_loss", logits, (ids, token_mask, ws), logits.data_ptr(),
+            ids.data_ptr(), _ptr(token_mask), T, E, K, coef, counts.data_ptr(), prob.data_ptr(),
+            loss.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
     return loss, counts, prob
 
 
@@ -547,11 +555,9 @@ def route_backward(logits: torch.Tensor, ids: torch.Tensor, dw: Optional[torch.T
             raise ValueError("dloss must hold one value")
     dlogits = (torch.empty_like(logits) if dlogits is None
                else _dev(dlogits, "dlogits", torch.float32, (T, E)))
-    with _on(logits, ids, dw, counts, dloss, token_mask, dlogits):
-        _check(lib().moe_route_backward(_ptr(logits), _ptr(ids), _ptr(dw), _ptr(token_mask),
-                                        _ptr(counts), _ptr(dloss), T, E, K,
-                                        int(bool(renormalize)), float(coef), _ptr(dlogits),
-                                        _stream()), "moe_route_backward")
+    _launch("moe_route_backward", logits, (ids, dw, counts, dloss, token_mask, dlogits),
+            logits.data_ptr(), ids.data_ptr(), _ptr(dw), _ptr(token_mask), _ptr(counts),
+            _ptr(dloss), T, E, K, 1 if renormalize else 0, coef, dlogits.data_ptr())
     return dlogits
 
 
@@ -623,12 +629,18 @@ class ForwardConfig:
                        self.a1_scale, self.a2_scale, self.gemm_blocks, int(self.x_codes))
 
 
-def forward_workspace_size(cfg: ForwardConfig) -> int:
-    c = cfg.c_struct()
+def _workspace_size(c: _Config) -> int:
     n = int(lib().moe_forward_workspace_size(ctypes.byref(c)))
     if n == 0:
         raise RuntimeError("moe_forward_workspace_size: invalid configuration")
     return n
+
+
+def forward_workspace_size(cfg: ForwardConfig) -> int:
+    return _workspace_size(cfg.c_struct())
+
+
+_NO_EVENTS = (_p * NUM_EVENTS)()
 
 
 def forward(cfg: ForwardConfig, x: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Tensor,
@@ -675,11 +687,13 @@ def forward(cfg: ForwardConfig, x: torch.Tensor, w_gate_up: torch.Tensor, w_down
             out.zero_()
     else:
         _dev(out, "out", cfg.out_dtype, (T, H))
-    need = forward_workspace_size(cfg)
+    c = cfg.c_struct()
+    need = _workspace_size(c)
     if ws is None:
         ws = _empty((need,), torch.uint8, x)
-    ev = (_p * NUM_EVENTS)(*([0] * NUM_EVENTS))
+    ev = _NO_EVENTS
     if events is not None:
+        ev = (_p * NUM_EVENTS)()
         for i, e in enumerate(list(events)[:NUM_EVENTS]):
             ev[i] = e or 0
     if shared_out is not None:
@@ -690,9 +704,8 @@ def forward(cfg: ForwardConfig, x: torch.Tensor, w_gate_up: torch.Tensor, w_down
                         None if mx else _ptr(w_down_scale),
                         _ptr(w_gate_up_scale) if mx else None,
                         _ptr(w_down_scale) if mx else None)
-    c = cfg.c_struct()
-    _check(lib().moe_forward(ctypes.byref(c), ctypes.byref(args), _ptr(ws),
-                             ws.numel() * ws.element_size(), _stream()), "moe_forward")
+    _launch("moe_forward", x, (ws,), ctypes.byref(c), ctypes.byref(args), ws.data_ptr(),
+            ws.numel() * ws.element_size())
     return out
 
 
