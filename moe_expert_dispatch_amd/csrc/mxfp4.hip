@@ -502,7 +502,7 @@ __device__ __forceinline__ void tile_product(uint4 (*stage)[kTileRows * 8],
   auto put = [&](int b) {
     const int r = tid >> 3;
 #pragma unroll
-    for (int i = 0; i < NT; ++i) stage[b][(r + 32 * i) * 8 + (chunk ^ (r & 7))] = fa[i];
+    for (int i = 0; i < NT; ++i) stage[b][(r + 32 * i) * 8 + (chunk ^ ((r >> 1) & 7))] = fa[i];
   };
   uint4 q[2][2], qn[2][2];
   uint32_t sc[2][2], scn[2][2];
@@ -531,7 +531,7 @@ __device__ __forceinline__ void tile_product(uint4 (*stage)[kTileRows * 8],
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const bf16x8_t x = __builtin_bit_cast(
-            bf16x8_t, stage[b][(32 * t + m) * 8 + ((4 * h + j) ^ (m & 7))]);
+            bf16x8_t, stage[b][(32 * t + m) * 8 + ((4 * h + j) ^ ((m >> 1) & 7))]);
         acc[0][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a0, x, acc[0][t], 0, 0, 0);
         acc[1][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a1, x, acc[1][t], 0, 0, 0);
       }
@@ -718,7 +718,7 @@ __global__ __launch_bounds__(512, U == 2 ? 2 : 1) void mxfp4_split_kernel(
 #pragma unroll
     for (int i = 0; i < kFetch; ++i) {
       const int r = (tid >> 3) + 32 * (i % NT);
-      stage[half][b][(i / NT) * TR * 8 + r * 8 + ((tid & 7) ^ (r & 7))] = fa[i];
+      stage[half][b][(i / NT) * TR * 8 + r * 8 + ((tid & 7) ^ ((r >> 1) & 7))] = fa[i];
     }
   };
 
@@ -756,7 +756,7 @@ __global__ __launch_bounds__(512, U == 2 ? 2 : 1) void mxfp4_split_kernel(
         for (int t = 0; t < NT; ++t) {
           const bf16x8_t x = __builtin_bit_cast(
               bf16x8_t,
-              stage[half][b][u * TR * 8 + (32 * t + m) * 8 + ((4 * h + j) ^ (m & 7))]);
+              stage[half][b][u * TR * 8 + (32 * t + m) * 8 + ((4 * h + j) ^ ((m >> 1) & 7))]);
           acc[0][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a0, x, acc[0][t], 0, 0, 0);
           acc[1][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a1, x, acc[1][t], 0, 0, 0);
         }
