@@ -33,7 +33,9 @@ __device__ __forceinline__ uint4 cvt8(uint32_t codes, float scale) {
 }
 
 
-// Four lanes a group, 8 values each. b = floor(log2 amax) - 2 + 127 puts the
+// Four lanes a group, 8 values each, one pass. 131072 x 4096 bf16: 240 us (5.7
+// TB/s), the inverse to bf16 228 us (6.0 TB/s): bound by the bytes, the
+// rounding is one instruction for two values. b = floor(log2 amax) - 2 + 127 puts the
 // largest magnitude into [4, 8): above 6 it saturates. The exponent is read
 // from amax's bits (a subnormal amax gives b = 0). A group with a non-finite
 // value gets the NaN scale.
@@ -95,6 +97,12 @@ __global__ __launch_bounds__(256) void dequantize_mxfp4_kernel(const uint32_t* _
 // the token rows, RB at a time, wait in LDS (all their k's, or a window of
 // them where they are too long), fetched once for the block's columns. The
 // WK partial sums are added in LDS in wave order.
+//
+// 64 slots, N = 1024 gate/up columns of Kd = 4096 (285 MB of codes and scales):
+// 59 us at 1 to 4 rows a slot, 67 at 8 and 10 (4.8 and 4.2 TB/s; reading the
+// same bytes and nothing else 52 us). Every wave loading its own 16-row
+// fragments of the tokens from the caches instead: 84 us at 2 rows, 101 at 8.
+
 // The codes and scales of one lane for a step: of its weight row the 16 bytes
 // at k0 + 128 i + 32 g, and in byte g of s[i] their scale.
 template <int M, int RUN>
@@ -312,8 +320,10 @@ __global__ __launch_bounds__(64 * kStreamWaves) void mxfp4_stream_kernel(
 // The same for contractions of at most 512 WK k's and very few rows: a wave's
 // part is one step, and it keeps its own k's of the rows, RB = 4 of them, in
 // its own LDS, so waves meet only to add up. Many short blocks leave no tail:
-// T = 16 over 64 experts in 80 slots (66 with rows, 8 columns tiles of 128
-// each: 528 blocks of the kernel below for 256 places) 66 against 77 us.
+// with 66 of 80 slots in use (N = 1024, Kd = 4096) the kernel above has 528
+// blocks for 256 places, a third round for 16 of them: 77 us, this one 66.
+// Past RB rows a slot it reads the codes again: 69 against 60 us at 4 rows a
+// slot everywhere.
 template <int OP, bool GATHER, typename CT, int WK>
 __global__ __launch_bounds__(64 * kStreamWaves) void mxfp4_quick_kernel(
     const uint16_t* __restrict__ a, const int32_t* __restrict__ offsets,
@@ -359,7 +369,7 @@ __global__ __launch_bounds__(64 * kStreamWaves) void mxfp4_quick_kernel(
               ? *reinterpret_cast<const uint4*>(a + (size_t)row * Kd + k0 + 8 * lane)
               : make_uint4(0, 0, 0, 0);
     }
-    __builtin_amdgcn_wave_barrier();  // LDS accesses of a wave run in order
+    wave_lds_fence();
     floatx4 acc[M];
 #pragma unroll
     for (int i = 0; i < M; ++i) acc[i] = floatx4{0.f, 0.f, 0.f, 0.f};
@@ -417,7 +427,14 @@ __global__ __launch_bounds__(64 * kStreamWaves) void mxfp4_quick_kernel(
 // (v_mfma_f32_32x32x16_bf16, weights first). Lane l holds weight row
 // l mod 32 and the k's 32 (l / 32) .. + 31 of a stage: 16 bytes of codes
 // under one scale. LDS rows are 128 bytes, their 16-byte chunks XOR-swizzled
-// by (row mod 8).
+// by (row / 2 mod 8): 16 lanes then read from all 64 banks.
+//
+// 64 slots of N = 1024 gate/up columns, Kd = 4096: 172 us at 128 rows a slot
+// (800 TFLOP/s), 573 at 512 (960; a library product of 8192^3 reaches 1240).
+// The matrix cores are busy 38% of the time at two waves a SIMD; LDS and the
+// conversions take a quarter each. Stages of 128 k's (half the barriers, twice
+// the distance of the fetches) were no faster, nor were 8 waves that share the
+// tile by rows and convert every weight twice (533 TFLOP/s at 128 rows).
 constexpr int kTileRows = 128;
 constexpr int kTileWeights = 256;
 constexpr int kStage = 64;
@@ -632,8 +649,13 @@ __global__ __launch_bounds__(256, 2) void mxfp4_tile_kernel(
 // bound by the stream of the codes. Eight waves: four of 64 weight rows, as
 // above, twice, the two halves taking every other run of 64 U k's, so a block
 // has twice the loads in flight and half the steps; the second half's sums
-// are added in LDS at the end. A step's codes are whole 128-byte lines
-// (U = 4), fetched a step ahead with the tokens' rows.
+// are added in LDS at the end. A step's codes and the tokens' rows are fetched
+// a step ahead. NT = 1 with steps of 128 k's (U = 2: two blocks a compute unit)
+// 64 slots of N = 1024 gate/up columns, Kd = 4096: 88 us from 4 to 32 rows a
+// slot, where the tiles above take 120 to 130; NT = 2, U = 4: 113 us at
+// 64 rows against 137. For the down product (Kd = 1024) NT = 1 takes 43 to 47
+// us against 51 to 57, NT = 2 no less than the tiles above (68 to 88 against
+// 57 to 65), so it is not there.
 template <int OP, bool GATHER, typename CT, int NT, int U, bool ALIGNED>
 __global__ __launch_bounds__(512, U == 2 ? 2 : 1) void mxfp4_split_kernel(
     const uint16_t* __restrict__ a, const int32_t* __restrict__ offsets,
@@ -897,7 +919,11 @@ __global__ __launch_bounds__(512) void mxfp4_pair_down_kernel(
 }
 
 // Which kernel, by the rows a slot has on the average of all (max_rows / S:
-// the host knows no more).
+// the host knows no more). Both sides in us at 64 slots, Kd = 4096 / N = 1024
+// gate/up and Kd = 1024 / N = 4096 down: 16 rows a slot 71 and 42 streamed
+// (16 rows at a time), 88 and 45 split, but a slot past 16 streams its codes
+// twice (12 rows a slot on the average already have one in six past it); at 31
+// 88 and 46 split, but past 32 twice; at 64 113 split by 64 rows, 137 in tiles.
 constexpr int kStreamRows = 10;
 constexpr int kSplitRows1 = 24;
 constexpr int kSplitRows2 = 56;
@@ -957,7 +983,7 @@ void launch_product(const void* a, const int32_t* offsets, const int32_t* sorted
   // The contraction is split among waves where the columns alone leave the
   // chip without a block for every compute unit, and where it is short: up to 1024
   // a wave's part is one step, and many light blocks beat few that walk two
-  // steps (S = 64, N = 4096, Kd = 1024: 28 against 36 us).
+  // steps (S = 64, N = 4096, Kd = 1024: 32 against 36 us).
   int split = Kd <= 512 || Kd > 1024 ? 1 : 2;
   const long long want = device_cu_count();
   while (split < kStreamWaves && split * 512 < Kd &&

@@ -10,6 +10,11 @@
 // outputs come from the unrounded v. The sum of squares is f32: per thread,
 // then per wave, then over the waves in order, so it does not depend on
 // scheduling.
+//
+// Bound by the bytes: 8192 rows of 5120 bf16 with residual and codes 71 us,
+// 5.3 TB/s; 16384 of 4096 103 us, 5.9 TB/s. One vector a thread (VPT = 1) is
+// the fastest wherever 1024 threads hold a row: with two a thread 72 and 111
+// us, with four 79 and 121. A single row of 4096 takes 2.4 us.
 #include "common.h"
 #include "vec8.h"
 
