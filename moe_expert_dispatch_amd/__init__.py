@@ -704,8 +704,9 @@ def forward(cfg: ForwardConfig, x: torch.Tensor, w_gate_up: torch.Tensor, w_down
                         None if mx else _ptr(w_down_scale),
                         _ptr(w_gate_up_scale) if mx else None,
                         _ptr(w_down_scale) if mx else None)
-    _launch("moe_forward", x, (ws,), ctypes.byref(c), ctypes.byref(args), ws.data_ptr(),
-            ws.numel() * ws.element_size())
+    _launch("moe_forward", x, (w_gate_up, w_down, logits, topk_ids, topk_w, rep_off, rep_slots, out,
+                               ws, shared_out, w_gate_up_scale, w_down_scale),
+            ctypes.byref(c), ctypes.byref(args), ws.data_ptr(), ws.numel() * ws.element_size())
     return out
 
 

@@ -261,6 +261,7 @@ LAYERS = {
     "plan_limit": dict(T=128, H=64, I=32, E=24, K=8, seed=13, extra=5),
     "past_plan": dict(T=129, H=64, I=32, E=24, K=8, seed=14, ep=2),
     "many_experts": dict(T=6, H=64, I=32, E=512, K=6, seed=15),
+    "most_slots": dict(T=128, H=32, I=32, E=1024, K=8, seed=16),
     "few": dict(T=5, H=320, I=160, E=12, K=3, seed=3),
     "replicas": dict(T=33, H=128, I=128, E=8, K=4, seed=4, extra=3),
     "skewed": dict(T=200, H=256, I=64, E=10, K=2, seed=5, skew=3.0),
@@ -321,6 +322,45 @@ def test_layer_routing_on_input():
                     cfg=dict(routing_on_input=True)))
     want, tol = _reference(L, 5, ids, np64(wt), on_input=True)
     assert (np.abs(got - want) <= tol + 2.0 ** -8 * (np.abs(want) + tol)).all()
+
+
+@pytest.mark.parametrize("T", [1, 5, 60, 300, 900])
+def test_layer_keeps_rows_apart(T):
+    """A token of NaN and one of infinities change no other token's bits, whichever kernels run; and an
+    expert whose slot the table does not give takes no part."""
+    dev = device()
+    announce(f"mxfp4 layer rows apart T={T}")
+    H, I, E, K = 192, 96, 8, 3
+    L = _layer(T + 2, H, I, E, K, 31)
+    a, b = T // 2, T + 1
+    clean = _run(dev, L, T + 2, logits=L["logits"])
+    x = L["x"].clone()
+    L["x"][a] = float("nan")
+    L["x"][b] = float("inf")
+    got = _run(dev, L, T + 2, logits=L["logits"])
+    rest = [t for t in range(T + 2) if t not in (a, b)]
+    assert torch.equal(got[rest], clean[rest])
+    assert torch.isnan(got[a]).all() and not torch.isfinite(got[b]).any()
+    L["x"] = x
+    bad = dict(L)
+    bad["rs"] = L["rs"].clone()
+    bad["rs"][2], bad["rs"][5] = 99, -7
+    ids, w = oracle.route(L["logits"], K, True)
+    w[(ids == 2) | (ids == 5)] = 0.0
+    want, tol = _reference(L, T + 2, ids, w)
+    got = np64(_run(dev, bad, T + 2, logits=L["logits"]))
+    assert (np.abs(got - want) <= tol + 2.0 ** -8 * (np.abs(want) + tol) + 1e-38).all()
+
+
+@pytest.mark.parametrize("T", [1, 2, 7, 200])
+def test_layer_grouped_routing(T):
+    dev = device()
+    announce(f"mxfp4 layer grouped routing T={T}")
+    L = _layer(T, 64, 32, 16, 3, 41)
+    ids, w = oracle.route_grouped(L["logits"], 3, True, 4, 2)
+    want, tol = _reference(L, T, ids, w)
+    got = np64(_run(dev, L, T, logits=L["logits"], cfg=dict(num_expert_group=4, topk_group=2)))
+    assert (np.abs(got - want) <= tol + 2.0 ** -8 * (np.abs(want) + tol) + 1e-38).all()
 
 
 def test_layer_is_its_stages():
