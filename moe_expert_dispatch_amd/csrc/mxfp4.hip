@@ -418,9 +418,9 @@ __global__ __launch_bounds__(64 * kStreamWaves) void mxfp4_quick_kernel(
 }
 
 // ---------------------------------------------------------------- products, many rows
-// One block per (128 token rows of a slot, 256 weight rows): the same 128
-// gate and up rows, or 256 rows of down. Four waves, each with 64 weight rows
-// (gate and up of 32 columns, or 64 columns) against all 128 tokens, so a
+// One block per (up to 160 token rows of a slot, 256 weight rows): the same
+// 128 gate and up rows, or 256 rows of down. Four waves, each with 64 weight rows
+// (gate and up of 32 columns, or 64 columns) against all the tokens, so a
 // weight is converted once in a block and never passes through LDS; the
 // tokens' rows, which all waves need, do: stages of 64 k's, two of them,
 // fetched into registers while the other feeds the matrix cores
@@ -429,21 +429,27 @@ __global__ __launch_bounds__(64 * kStreamWaves) void mxfp4_quick_kernel(
 // under one scale. LDS rows are 128 bytes, their 16-byte chunks XOR-swizzled
 // by (row / 2 mod 8): 16 lanes then read from all 64 banks.
 //
-// 64 slots of N = 1024 gate/up columns, Kd = 4096: 172 us at 128 rows a slot
-// (800 TFLOP/s), 573 at 512 (960; a library product of 8192^3 reaches 1240).
-// The matrix cores are busy 38% of the time at two waves a SIMD; LDS and the
-// conversions take a quarter each. Stages of 128 k's (half the barriers, twice
-// the distance of the fetches) were no faster, nor were 8 waves that share the
-// tile by rows and convert every weight twice (533 TFLOP/s at 128 rows).
-constexpr int kTileRows = 128;
+// 64 slots of N = 1024 gate/up columns, Kd = 4096: 177 us at 128 rows a slot
+// (780 TFLOP/s), 190 at 160 (900), 328 at 320 (1050; a library product of
+// 8192^3 reaches 1240). Tiles up to 128 rows took 307 us at 256 rows a slot
+// and 393 at 260, where a third tile of 4 rows costs half of a whole one: now
+// 303 and 315. Their sums fill 160 registers of 256, so the codes of a tile
+// over 128 rows are fetched one unit ahead instead of two (7 registers of the
+// addresses still wait in scratch). The matrix cores are busy 38% of the time
+// at two waves a SIMD; LDS and the conversions take a quarter each. Stages of
+// 128 k's (half the barriers, twice the distance of the fetches) were no
+// faster, nor were 8 waves that share the tile by rows and convert every
+// weight twice (533 TFLOP/s at 128 rows).
+constexpr int kTileRows = 160;
 constexpr int kTileWeights = 256;
 constexpr int kStage = 64;
 
 typedef float floatx16 __attribute__((ext_vector_type(16)));
 
-// Finds row tile `tile` of the slots' tiles of TR rows, in slot order: the
-// slot, its rows [r0, r1) in the tile; false behind the last. Every wave
-// computes it for itself (a scan over 64 slots at a time).
+// Finds row tile `tile` of the slots, in slot order: the slot, its rows
+// [r0, r1) in the tile; false behind the last. A slot has as few tiles of at
+// most TR rows as hold its rows, of one size in whole 32s (the last one less).
+// Every wave computes it for itself (a scan over 64 slots at a time).
 template <int TR>
 __device__ __forceinline__ bool find_tile(const int32_t* __restrict__ offsets, int S,
                                           int max_rows, int tile, int* slot, int* r0, int* r1) {
@@ -465,11 +471,14 @@ __device__ __forceinline__ bool find_tile(const int32_t* __restrict__ offsets, i
     const uint64_t hit = __ballot(incl > tile);
     if (hit != 0) {
       const int l = __ffsll((unsigned long long)hit) - 1;
-      const int first = tile - (__builtin_amdgcn_readlane(incl, l) -
-                                __builtin_amdgcn_readlane(n, l));
+      const int count = __builtin_amdgcn_readlane(n, l);
+      const int at = tile - (__builtin_amdgcn_readlane(incl, l) - count);
+      const int first = __builtin_amdgcn_readlane(a, l);
+      const int end = __builtin_amdgcn_readlane(b, l);
+      const int step = ceil_div(ceil_div(end - first, count), 32) * 32;
       *slot = s0 + l;
-      *r0 = __builtin_amdgcn_readlane(a, l) + first * TR;
-      *r1 = min(*r0 + TR, __builtin_amdgcn_readlane(b, l));
+      *r0 = first + at * step;
+      *r1 = min(*r0 + step, end);
       return true;
     }
     tile -= __builtin_amdgcn_readlane(incl, kWave - 1);
@@ -480,7 +489,7 @@ __device__ __forceinline__ bool find_tile(const int32_t* __restrict__ offsets, i
 // NT: 32-token blocks of the tile that hold rows.
 template <int OP, typename CT, int NT>
 __device__ __forceinline__ void tile_product(uint4 (*stage)[kTileRows * 8],
-                                             const uint16_t* const (&src)[4], int r0, int rows,
+                                             const uint16_t* const (&src)[5], int r0, int rows,
                                              const uint8_t* __restrict__ w,
                                              const uint8_t* __restrict__ w_scale, int n0, int N,
                                              int Kd, CT* __restrict__ c) {
@@ -495,11 +504,10 @@ __device__ __forceinline__ void tile_product(uint4 (*stage)[kTileRows * 8],
   const int col1 = GU ? col0 : col0 + 32;
   const int row0 = min(col0, N - 32) + m;
   const int row1 = GU ? N + row0 : min(col1, N - 32) + m;
-  // 32-bit offsets into the slot's panel (below 2^31 bytes: weight_panel_ok)
+  // 32-bit offsets into the slot's panel (below 2^31 bytes: weight_panel_ok);
+  // a sixteenth of a code's offset is that of its scale
   const uint32_t wp[2] = {(uint32_t)row0 * (uint32_t)(Kd / 2) + 16 * h,
                           (uint32_t)row1 * (uint32_t)(Kd / 2) + 16 * h};
-  const uint32_t sp[2] = {(uint32_t)row0 * (uint32_t)(Kd / 32) + h,
-                          (uint32_t)row1 * (uint32_t)(Kd / 32) + h};
 
   floatx16 acc[2][NT];
 #pragma unroll
@@ -521,19 +529,23 @@ __device__ __forceinline__ void tile_product(uint4 (*stage)[kTileRows * 8],
 #pragma unroll
     for (int i = 0; i < NT; ++i) stage[b][(r + 32 * i) * 8 + (chunk ^ ((r >> 1) & 7))] = fa[i];
   };
-  uint4 q[2][2], qn[2][2];
-  uint32_t sc[2][2], scn[2][2];
-  auto load_codes = [&](int k0, uint4 (&qq)[2][2], uint32_t (&ss)[2][2]) {
+  // Codes and scales of U units of 64 k's, fetched as many ahead: two, or one
+  // where the sums of 160 rows leave no registers.
+  constexpr int U = NT <= 4 ? 2 : 1;
+  uint4 q[2][U], qn[2][U];
+  uint32_t sc[2][U], scn[2][U];
+  auto load_codes = [&](int k0, uint4 (&qq)[2][U], uint32_t (&ss)[2][U]) {
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
+      for (int u = 0; u < U; ++u) {
         const bool in = k0 + kStage * u + 32 * h < Kd;
         qq[i][u] = make_uint4(0, 0, 0, 0);
         ss[i][u] = 127;
         if (in) {
-          qq[i][u] = *reinterpret_cast<const uint4*>(w + (wp[i] + (uint32_t)(k0 + kStage * u) / 2));
-          ss[i][u] = w_scale[sp[i] + (uint32_t)(k0 + kStage * u) / 32];
+          const uint32_t at = wp[i] + (uint32_t)(k0 + kStage * u) / 2;
+          qq[i][u] = *reinterpret_cast<const uint4*>(w + at);
+          ss[i][u] = w_scale[at / 16];
         }
       }
   };
@@ -560,22 +572,23 @@ __device__ __forceinline__ void tile_product(uint4 (*stage)[kTileRows * 8],
   put(0);
   __syncthreads();
   for (int k0 = 0; k0 < Kd; k0 += 2 * kStage) {
-    fetch(k0 + kStage);
-    load_codes(k0 + 2 * kStage, qn, scn);
-    compute(0, 0);
-    put(1);
-    __syncthreads();
-    fetch(k0 + 2 * kStage);
-    compute(1, 1);
-    put(0);
-    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int v = 0; v < 2; ++v) {  // the stage in buffer v, the next into the other
+      fetch(k0 + (v + 1) * kStage);
+      if (U == 1 || v == 0) load_codes(k0 + (U == 1 ? v + 1 : 2) * kStage, qn, scn);
+      compute(v, U == 1 ? 0 : v);
+      put(v ^ 1);
+      __syncthreads();
+      if (U == 1 || v == 1) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        q[i][u] = qn[i][u];
-        sc[i][u] = scn[i][u];
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            q[i][u] = qn[i][u];
+            sc[i][u] = scn[i][u];
+          }
       }
+    }
   }
 
 #pragma unroll
@@ -624,9 +637,9 @@ __global__ __launch_bounds__(256, 2) void mxfp4_tile_kernel(
   int s = 0, r0 = 0, r1 = 0;
   if (!find_tile<kTileRows>(offsets, S, max_rows, tile, &s, &r0, &r1)) return;
   const int rows = r1 - r0;
-  const uint16_t* src[4];
+  const uint16_t* src[5];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 5; ++i) {
     int row = r0 + min((int)(threadIdx.x >> 3) + 32 * i, rows - 1);
     if constexpr (GATHER) row = sorted_pairs[row] / topk;
     src[i] = a + (size_t)row * Kd + 8 * (threadIdx.x & 7);
@@ -640,8 +653,10 @@ __global__ __launch_bounds__(256, 2) void mxfp4_tile_kernel(
     tile_product<OP, CT, 2>(stage, src, r0, rows, ws, ss, n0, N, Kd, c);
   else if (rows <= 96)
     tile_product<OP, CT, 3>(stage, src, r0, rows, ws, ss, n0, N, Kd, c);
-  else
+  else if (rows <= 128)
     tile_product<OP, CT, 4>(stage, src, r0, rows, ws, ss, n0, N, Kd, c);
+  else
+    tile_product<OP, CT, 5>(stage, src, r0, rows, ws, ss, n0, N, Kd, c);
 }
 
 // ---------------------------------------------------------------- products, some rows

@@ -124,7 +124,9 @@ def _products_check(sizes, H, I):
 # every way the products are split: rows a slot (up to 2, 4, 10, 24, 56 and more on the average, with
 # slots far over and under it) by short, middle and long contractions and ones that are no multiple of 128
 ROWS = {"two": [2, 0, 1, 9, 0, 2] * 4, "four": [4, 0, 9, 3], "ten": [0, 10, 17, 13], "twenty": [33, 0, 40, 7],
-        "fifty": [65, 50, 0, 70], "hundred": [1, 300, 0, 96]}
+        "fifty": [65, 50, 0, 70], "hundred": [1, 300, 0, 96],
+        # tiles of 160: one, one row past it, two of one size, three, and every number of 32s in the last
+        "tiles": [160, 161, 320, 321, 0, 130, 481, 641]}
 
 
 @pytest.mark.parametrize("rows", ROWS)
