@@ -506,9 +506,9 @@ __device__ __forceinline__ void tile_product(uint4 (*stage)[kTileRows * 8],
   const int row1 = GU ? N + row0 : min(col1, N - 32) + m;
   // 32-bit offsets into the slot's panel (below 2^31 bytes: weight_panel_ok);
   // a sixteenth of a code's offset is that of its scale
-  const uint32_t wp[2] = {(uint32_t)row0 * (uint32_t)(Kd / 2) + 16 * h,
-                          (uint32_t)row1 * (uint32_t)(Kd / 2) + 16 * h};
+  const uint32_t wp[2] = {(uint32_t)row0 * (uint32_t)(Kd / 2), (uint32_t)row1 * (uint32_t)(Kd / 2)};
 
+  constexpr int AHEAD = 2;
   floatx16 acc[2][NT];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
@@ -519,13 +519,15 @@ __device__ __forceinline__ void tile_product(uint4 (*stage)[kTileRows * 8],
   const int chunk = tid & 7;
   uint4 fa[NT];
   auto fetch = [&](int k0) {
-    const bool in = k0 + 8 * chunk < Kd;
+    const int at = min(k0 + 8 * chunk, Kd - 8);
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
-      fa[i] = in ? *reinterpret_cast<const uint4*>(src[i] + k0) : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < NT; ++i) fa[i] = *reinterpret_cast<const uint4*>(src[i] + at);
   };
-  auto put = [&](int b) {
+  auto put = [&](int b, int k0) {
     const int r = tid >> 3;
+    if (k0 + kStage > Kd && k0 + 8 * chunk >= Kd)
+#pragma unroll
+      for (int i = 0; i < NT; ++i) fa[i] = make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < NT; ++i) stage[b][(r + 32 * i) * 8 + (chunk ^ ((r >> 1) & 7))] = fa[i];
   };
@@ -539,17 +541,19 @@ __device__ __forceinline__ void tile_product(uint4 (*stage)[kTileRows * 8],
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const bool in = k0 + kStage * u + 32 * h < Kd;
-        qq[i][u] = make_uint4(0, 0, 0, 0);
-        ss[i][u] = 127;
-        if (in) {
-          const uint32_t at = wp[i] + (uint32_t)(k0 + kStage * u) / 2;
-          qq[i][u] = *reinterpret_cast<const uint4*>(w + at);
-          ss[i][u] = w_scale[at / 16];
-        }
+        const uint32_t at = wp[i] + (uint32_t)min(k0 + kStage * u + 32 * h, Kd - 32) / 2;
+        qq[i][u] = *reinterpret_cast<const uint4*>(w + at);
+        ss[i][u] = w_scale[at / 16];
       }
   };
-  auto compute = [&](int b, int u) {
+  auto compute = [&](int b, int u, int k0) {
+    if (k0 + kStage > Kd && k0 + 32 * h >= Kd) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        q[i][u] = make_uint4(0, 0, 0, 0);
+        sc[i][u] = 127;
+      }
+    }
     const float s0 = e8m0(sc[0][u]), s1 = e8m0(sc[1][u]);
     const uint32_t q0[4] = {q[0][u].x, q[0][u].y, q[0][u].z, q[0][u].w};
     const uint32_t q1[4] = {q[1][u].x, q[1][u].y, q[1][u].z, q[1][u].w};
@@ -565,19 +569,26 @@ __device__ __forceinline__ void tile_product(uint4 (*stage)[kTileRows * 8],
         acc[1][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a1, x, acc[1][t], 0, 0, 0);
       }
     }
+    __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);
+#pragma unroll
+    for (int i = 0; i < 4 * NT - AHEAD; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x008, 2 * AHEAD, 0);
   };
 
   fetch(0);
   load_codes(0, q, sc);
-  put(0);
+  put(0, 0);
   __syncthreads();
   for (int k0 = 0; k0 < Kd; k0 += 2 * kStage) {
 #pragma unroll
     for (int v = 0; v < 2; ++v) {  // the stage in buffer v, the next into the other
       fetch(k0 + (v + 1) * kStage);
       if (U == 1 || v == 0) load_codes(k0 + (U == 1 ? v + 1 : 2) * kStage, qn, scn);
-      compute(v, U == 1 ? 0 : v);
-      put(v ^ 1);
+      compute(v, U == 1 ? 0 : v, k0 + v * kStage);
+      put(v ^ 1, k0 + (v + 1) * kStage);
       __syncthreads();
       if (U == 1 || v == 1) {
 #pragma unroll
@@ -642,7 +653,7 @@ __global__ __launch_bounds__(256, 2) void mxfp4_tile_kernel(
   for (int i = 0; i < 5; ++i) {
     int row = r0 + min((int)(threadIdx.x >> 3) + 32 * i, rows - 1);
     if constexpr (GATHER) row = sorted_pairs[row] / topk;
-    src[i] = a + (size_t)row * Kd + 8 * (threadIdx.x & 7);
+    src[i] = a + (size_t)row * Kd;
   }
   const size_t wrow = (size_t)s * M * N;
   const uint8_t* ws = w + wrow * (Kd / 2);
