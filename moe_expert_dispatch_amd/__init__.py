@@ -148,6 +148,7 @@ def _stream() -> int:
 # it, which took longer than a small kernel runs (about 2 us of a 12 us call).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -171,7 +172,7 @@ def _dev(t: torch.Tensor, name: str, dtype=None, shape=None) -> torch.Tensor:
 
 
 def _empty(shape, dtype, like: torch.Tensor) -> torch.Tensor:
-    return torch.empty(shape, dtype=dtype, device=like.device)
+    return like.new_empty(shape, dtype=dtype)
 
 
 def _launch(what: str, like: torch.Tensor, others: Sequence[Optional[torch.Tensor]], *args) -> None:
@@ -182,7 +183,7 @@ def _launch(what: str, like: torch.Tensor, others: Sequence[Optional[torch.Tenso
         if o is not None and o.get_device() != dev:
             raise ValueError(f"tensors on {like.device} and {o.device}: one device is needed")
     fn = getattr(_lib or lib(), what)
-    if torch.cuda.current_device() == dev:
+    if _current_device() == dev:
         code = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
@@ -492,7 +493,7 @@ def rms_norm(x: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-6,
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
     if q_scale is not None:
-        q = (_empty((T, H), torch.uint8, x) if q is None else _dev(q, "q", _CODES, (T, H)))
+        q = (torch.empty_like(x, dtype=torch.uint8) if q is None else _dev(q, "q", _CODES, (T, H)))
     elif q is not None:
         raise ValueError("q needs a q_scale")
     y = torch.empty_like(x) if y is None else _dev(y, "y", x.dtype, (T, H))

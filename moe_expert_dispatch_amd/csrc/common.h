@@ -162,12 +162,9 @@ __host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b -
 // replica of a local expert is chosen by token index, t mod r. A null table
 // is the identity map; an entry outside [0, S) (or an expert without slots)
 // gives slot -1. Returns the slot.
-__device__ __forceinline__ int map_pair(int p, int t, int e, float wv, int start, int E_local,
+__device__ __forceinline__ int map_slot(int t, int e, int start, int E_local,
                                          const int32_t* __restrict__ rep_off,
-                                         const int32_t* __restrict__ rep_slots, int S,
-                                         int32_t* __restrict__ slot,
-                                         float* __restrict__ w_masked,
-                                         uint8_t* __restrict__ mask) {
+                                         const int32_t* __restrict__ rep_slots, int S) {
   const bool local = e >= start && e < start + E_local;
   const int lid = local ? e - start : ((e % E_local) + E_local) % E_local;
   int s = lid;
@@ -181,11 +178,45 @@ __device__ __forceinline__ int map_pair(int p, int t, int e, float wv, int start
       s = (v >= 0 && v < S) ? v : -1;
     }
   }
+  return s;
+}
+
+// The slot, masked weight and mask of a pair, written; returns the slot.
+__device__ __forceinline__ int map_pair(int p, int t, int e, float wv, int start, int E_local,
+                                         const int32_t* __restrict__ rep_off,
+                                         const int32_t* __restrict__ rep_slots, int S,
+                                         int32_t* __restrict__ slot,
+                                         float* __restrict__ w_masked,
+                                         uint8_t* __restrict__ mask) {
+  const bool local = e >= start && e < start + E_local;
+  const int s = map_slot(t, e, start, E_local, rep_off, rep_slots, S);
   slot[p] = s;
   w_masked[p] = wv * (local ? 1.0f : 0.0f);
   mask[p] = local ? 1 : 0;
   return s;
 }
+
+// Where a fused router writes the slot map (null slot: route only).
+struct MapOut {
+  int start, E_local, S;
+  const int32_t* rep_off;
+  const int32_t* rep_slots;
+  int32_t* slot;
+  float* w_masked;
+  uint8_t* mask;
+};
+
+// Routing that a product does for its own pairs: lanes as route_lanes gives
+// them (0: the slot map is there already).
+struct PairRouting {
+  const float* logits;
+  int E, renorm, lanes;
+  MapOut map;
+};
+
+// Lanes of a token in the lane-group router; 0: a whole wave (expert groups,
+// many experts or selections).
+int route_lanes(int E, int K, int G);
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -391,8 +422,7 @@ moe_status_t launch_gemm_mxfp4(moe_gemm_op_t op, const void* a, const int32_t* s
 // pair (no permutation): act [T * topk, I] = the SwiGLU rows, then out = the
 // weighted sum of the down products, with shared and accumulate as in
 // launch_combine.
-moe_status_t launch_mxfp4_pairs(const void* x, const int32_t* slot, const uint8_t* mask,
-                                const float* weight, int T, int topk, int S,
+moe_status_t launch_mxfp4_pairs(const void* x, const PairRouting& routing, int T, int topk,
                                 const uint8_t* w_gate_up, const uint8_t* gate_up_scale,
                                 const uint8_t* w_down, const uint8_t* down_scale, int H, int I,
                                 void* act, void* out, bool out_bf16, int accumulate,

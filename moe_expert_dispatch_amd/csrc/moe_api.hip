@@ -435,7 +435,14 @@ moe_status_t moe_forward(const moe_config_t* cfg, const moe_forward_args_t* args
   // more: routing, slot map and permutation in one launch or two
   const bool pairs = mx && !on_input && T > 0 && T <= kPairTokens;
   const bool plan = mx && !on_input && !pairs && T > 0 && T * K <= kPlanPairs;
-  if (plan) {
+  // the pairs' gate/up blocks route for themselves where lane groups do it
+  const PairRouting pair_routing{
+      args->logits, cfg->E_global, cfg->renormalize ? 1 : 0,
+      args->logits ? route_lanes(cfg->E_global, K, cfg->num_expert_group) : 0,
+      {cfg->ep_rank * E_local, E_local, S, args->rep_off, args->rep_slots, slot, w_masked, mask}};
+  if (pairs && pair_routing.lanes > 0) {
+    // nothing to launch
+  } else if (plan) {
     MOE_TRY(launch_plan(args->logits, T, cfg->E_global, K, cfg->renormalize ? 1 : 0,
                         cfg->num_expert_group, cfg->topk_group,
                         args->logits ? ids : const_cast<int32_t*>(ids_in),
@@ -468,7 +475,7 @@ moe_status_t moe_forward(const moe_config_t* cfg, const moe_forward_args_t* args
                            quant ? &fq : nullptr));
   MOE_TRY(mark(MOE_EV_PERMUTED));
   if (pairs) {
-    MOE_TRY(launch_mxfp4_pairs(args->x, slot, mask, w_masked, T, K, S,
+    MOE_TRY(launch_mxfp4_pairs(args->x, pair_routing, T, K,
                                static_cast<const uint8_t*>(args->w_gate_up), args->w_gate_up_e8m0,
                                static_cast<const uint8_t*>(args->w_down), args->w_down_e8m0, H, I,
                                act, args->out, cfg->out_dtype == MOE_DTYPE_BF16, cfg->accumulate,

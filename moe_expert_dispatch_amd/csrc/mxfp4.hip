@@ -7,7 +7,7 @@
 // bits), so the products run on the bf16 matrix cores without any rounding
 // of the weights: gfx950 converts two codes and applies the scale in one
 // instruction (v_cvt_scalef32_pk_bf16_fp4).
-#include "common.h"
+#include "route_token.h"
 #include "vec8.h"
 
 namespace moe {
@@ -201,16 +201,33 @@ __global__ __launch_bounds__(64 * kStreamWaves) void mxfp4_stream_kernel(
     const uint16_t* __restrict__ a, const int32_t* __restrict__ offsets,
     const int32_t* __restrict__ sorted_pairs, int topk, int S, int max_rows, int find,
     const uint8_t* __restrict__ w, const uint8_t* __restrict__ w_scale, int N, int Kd,
-    CT* __restrict__ c, const uint8_t* __restrict__ mask) {
+    CT* __restrict__ c, PairRouting routing) {
   constexpr int M = OP == MOE_GEMM_GATE_UP_SWIGLU ? 2 : 1;  // matrices (gate and up, or down)
   constexpr int WN = kStreamWaves / WK;
   extern __shared__ uint4 lds[];
   int s, r0, r1;
-  if constexpr (PAIRS) {  // a pair a line, row = pair; offsets holds the pairs' slots
+  if constexpr (PAIRS) {  // a pair a line, row = pair
     r0 = blockIdx.y;
     r1 = r0 + 1;
-    s = offsets[r0];
-    if (mask[r0] == 0 || s < 0 || s >= S) return;
+    if (routing.lanes > 0) {
+      // Every block routes its pair's token; the first of a pair writes the map
+      // for the down product. One token of 60 experts: 4.4 + 7.5 us as a launch
+      // of its own, 11.0 in here, and the call 22.0 -> 17.9 us.
+      __shared__ int routed;
+      if (threadIdx.x < kWave) {
+        const bool write = blockIdx.x == 0;
+        const int got = routing.lanes == 8    ? route_pair<8>(routing, r0, topk, write)
+                        : routing.lanes == 16 ? route_pair<16>(routing, r0, topk, write)
+                                              : route_pair<32>(routing, r0, topk, write);
+        if (threadIdx.x == 0) routed = got;
+      }
+      __syncthreads();
+      s = __builtin_amdgcn_readfirstlane(routed);
+      if (s < 0) return;
+    } else {
+      s = routing.map.slot[r0];
+      if (routing.map.mask[r0] == 0 || s < 0 || s >= S) return;
+    }
   } else {
     if (!block_slot(offsets, S, max_rows, find != 0, &s, &r0, &r1)) return;
   }
@@ -1004,7 +1021,7 @@ void launch_product(const void* a, const int32_t* offsets, const int32_t* sorted
         <<<dim3(ceil_div(N, 16 * kStreamWaves / WK), lines), 64 * kStreamWaves,
            rows_lds > red_lds ? rows_lds : red_lds, stream>>>(
             a16, offsets, sorted_pairs, topk, S, max_rows, max_rows < S, w, w_scale, N, Kd, ct,
-            nullptr);
+            PairRouting{});
   };
   // The contraction is split among waves where the columns alone leave the
   // chip without a block for every compute unit, and where it is short: up to 1024
@@ -1129,14 +1146,14 @@ moe_status_t launch_gemm_mxfp4(moe_gemm_op_t op, const void* a, const int32_t* s
   return launch_status();
 }
 
-moe_status_t launch_mxfp4_pairs(const void* x, const int32_t* slot, const uint8_t* mask,
-                                const float* weight, int T, int topk, int S,
+moe_status_t launch_mxfp4_pairs(const void* x, const PairRouting& routing, int T, int topk,
                                 const uint8_t* w_gate_up, const uint8_t* gate_up_scale,
                                 const uint8_t* w_down, const uint8_t* down_scale, int H, int I,
                                 void* act, void* out, bool out_bf16, int accumulate,
                                 const void* shared, hipStream_t stream) {
   using std::integral_constant;
   const int P = T * topk;
+  const int S = routing.map.S;
   uint16_t* act16 = static_cast<uint16_t*>(act);
   auto gate_up = [&](auto wk, auto pipe, auto al) {
     constexpr int WK = decltype(wk)::value, RB = 8;
@@ -1147,8 +1164,8 @@ moe_status_t launch_mxfp4_pairs(const void* x, const int32_t* slot, const uint8_
                         decltype(pipe)::value, decltype(al)::value, true>
         <<<dim3(ceil_div(I, 16 * kStreamWaves / WK), P), 64 * kStreamWaves,
            rows_lds > red_lds ? rows_lds : red_lds, stream>>>(
-            static_cast<const uint16_t*>(x), slot, nullptr, topk, S, P, 0, w_gate_up,
-            gate_up_scale, I, H, act16, mask);
+            static_cast<const uint16_t*>(x), nullptr, nullptr, topk, S, P, 0, w_gate_up,
+            gate_up_scale, I, H, act16, routing);
   };
   if (H % 128 != 0)
     gate_up(integral_constant<int, 8>{}, std::true_type{}, std::false_type{});
@@ -1163,7 +1180,7 @@ moe_status_t launch_mxfp4_pairs(const void* x, const int32_t* slot, const uint8_
   auto down = [&](auto o, auto al) {
     using OT = decltype(o);
     mxfp4_pair_down_kernel<OT, decltype(al)::value><<<dim3(H / 16, T), 512, 0, stream>>>(
-        act16, slot, mask, weight, topk, S, w_down, down_scale, H, I, static_cast<OT*>(out),
+        act16, routing.map.slot, routing.map.mask, routing.map.w_masked, topk, S, w_down, down_scale, H, I, static_cast<OT*>(out),
         accumulate, static_cast<const uint16_t*>(shared));
   };
   if (out_bf16) {

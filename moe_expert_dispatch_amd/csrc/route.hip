@@ -27,114 +27,10 @@
 // gets group g's key (best ordered logit, 0xffffffff - g), topk_group rounds
 // of a wave max pick the groups, and the keys of experts outside them are
 // cleared before the K rounds. The softmax still runs over all E experts.
-#include "common.h"
+#include "route_token.h"
 
 namespace moe {
 namespace {
-
-__device__ __forceinline__ uint32_t ordered_bits(float f) {
-  uint32_t u = __float_as_uint(f);
-  if ((u & 0x7fffffffu) > 0x7f800000u) return 0u;  // NaN ranks below everything
-  if ((u & 0x7fffffffu) == 0u) u = 0u;              // -0.0 -> +0.0
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
-
-
-// Inverse of ordered_bits for non-NaN keys (-0.0 comes back as +0.0, which
-// gives the same exponentials).
-__device__ __forceinline__ float from_ordered(uint32_t o) {
-  return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
-}
-
-// Where the fused router writes the slot map (null slot: route only).
-struct MapOut {
-  int start, E_local, S;
-  const int32_t* rep_off;
-  const int32_t* rep_slots;
-  int32_t* slot;
-  float* w_masked;
-  uint8_t* mask;
-};
-
-// Sorts n <= 8 keys into descending order with a comparator network
-// (Batcher's odd-even merge sort: 1, 5 or 19 compare-exchanges).
-template <int N>
-__device__ __forceinline__ void sort_desc(uint64_t (&k)[N]) {
-  auto cx = [&](int a, int b) {
-    const uint64_t hi = k[a] > k[b] ? k[a] : k[b];
-    const uint64_t lo = k[a] > k[b] ? k[b] : k[a];
-    k[a] = hi;
-    k[b] = lo;
-  };
-  if constexpr (N == 2) {
-    cx(0, 1);
-  } else if constexpr (N == 4) {
-    cx(0, 1); cx(2, 3); cx(0, 2); cx(1, 3); cx(1, 2);
-  } else if constexpr (N == 8) {
-    cx(0, 1); cx(2, 3); cx(4, 5); cx(6, 7);
-    cx(0, 2); cx(1, 3); cx(4, 6); cx(5, 7);
-    cx(1, 2); cx(5, 6);
-    cx(0, 4); cx(1, 5); cx(2, 6); cx(3, 7);
-    cx(2, 4); cx(3, 5);
-    cx(1, 2); cx(3, 4); cx(5, 6);
-  } else {
-    static_assert(N == 1, "1, 2, 4 or 8 keys per lane");
-  }
-}
-
-// The selection of one token by the L lanes of its group (q: the lane in it):
-// lane q < K ends with the q-th expert and its weight. EPL logits per lane (a
-// power of two); K <= L, E <= L * EPL. Lanes of tokens that do not exist (not
-// live) carry empty keys, but stay active, so every DPP step reads live lanes.
-template <int L, int EPL>
-__device__ __forceinline__ void route_token(const float* __restrict__ row, bool live, int E, int K,
-                                            int renorm, int q, int* id, float* weight) {
-  float v[EPL];
-  uint64_t key[EPL];
-#pragma unroll
-  for (int j = 0; j < EPL; ++j) {
-    const int e = q + L * j;
-    if (live && e < E) {
-      v[j] = row[e];
-      key[j] = ((uint64_t)ordered_bits(v[j]) << 32) | (0xffffffffu - (uint32_t)e);
-    } else {
-      v[j] = -INFINITY;
-      key[j] = 0;
-    }
-  }
-
-  // K rounds; lane k of the group keeps the k-th selection's key. The
-  // lane's keys are sorted once, so a round's candidate is key[0] and only
-  // the lane holding the group's maximum (keys are unique) moves its list up.
-  sort_desc<EPL>(key);
-  uint64_t my_key = 0;
-  uint64_t top = 0;
-  for (int k = 0; k < K; ++k) {
-    const uint64_t best = group_max_u64<L>(key[0]);
-    // all ones in the lane that held it (as a bit mask: one select per word)
-    const uint64_t mv = 0ull - (uint64_t)(key[0] == best);
-#pragma unroll
-    for (int j = 0; j + 1 < EPL; ++j) key[j] = (key[j + 1] & mv) | (key[j] & ~mv);
-    key[EPL - 1] &= ~mv;
-    if (q == k) my_key = best;
-    if (k == 0) top = best;
-  }
-
-  // Softmax with the top logit as the shift.
-  const float m = from_ordered((uint32_t)(top >> 32));
-  float part = 0.f;
-#pragma unroll
-  for (int j = 0; j < EPL; ++j)
-    if (q + L * j < E) part += expf(v[j] - m);
-  const float denom = group_sum<L>(part);
-  float p = (q < K) ? expf(from_ordered((uint32_t)(my_key >> 32)) - m) / denom : 0.f;
-  if (renorm) {
-    const float s = group_sum<L>(p);
-    p = p / s;
-  }
-  *id = (int)(0xffffffffu - (uint32_t)my_key);
-  *weight = p;
-}
 
 template <int L, int EPL, bool MAP>
 __global__ __launch_bounds__(256) void route_lanes_kernel(const float* __restrict__ logits,
@@ -344,16 +240,6 @@ __global__ __launch_bounds__(256) void route_kernel(const float* __restrict__ lo
   }
 }
 
-// Lanes per token for the grouped-lane router (at most 8 logits per lane and
-// K <= L), or 0 where the wave-per-token kernel runs (group-limited routing,
-// more than 256 experts, K > 32).
-int lanes_for(int E, int K, int G) {
-  if (G != 0 || E > 256 || K > 32) return 0;
-  if (E <= 64 && K <= 8) return 8;
-  if (E <= 128 && K <= 16) return 16;
-  return 32;
-}
-
 template <int L, bool MAP>
 void launch_lanes(const float* logits, int T, int E, int K, int renorm, int32_t* ids, float* w,
                   const MapOut& mo, hipStream_t stream) {
@@ -423,13 +309,23 @@ void launch_plan_lanes(const float* logits, int T, int E, int K, int renorm, con
 
 }  // namespace
 
+// Lanes per token for the grouped-lane router (at most 8 logits per lane and
+// K <= L), or 0 where the wave-per-token kernel runs (group-limited routing,
+// more than 256 experts, K > 32).
+int route_lanes(int E, int K, int G) {
+  if (G != 0 || E > 256 || K > 32) return 0;
+  if (E <= 64 && K <= 8) return 8;
+  if (E <= 128 && K <= 16) return 16;
+  return 32;
+}
+
 moe_status_t launch_route_map(const float* logits, int T, int E, int K, int renorm, int G,
                               int TG, int32_t* ids, float* w, int start, int E_local,
                               const int32_t* rep_off, const int32_t* rep_slots, int S,
                               int32_t* slot, float* w_masked, uint8_t* mask,
                               hipStream_t stream) {
   if (T == 0) return MOE_OK;
-  const int L = lanes_for(E, K, G);
+  const int L = route_lanes(E, K, G);
   const MapOut mo{start, E_local, S, rep_off, rep_slots, slot, w_masked, mask};
   if (L == 0)
     launch_waves<true>(logits, T, E, K, renorm, G, TG, ids, w, mo, stream);
@@ -441,7 +337,7 @@ moe_status_t launch_route_map(const float* logits, int T, int E, int K, int reno
 moe_status_t launch_route(const float* logits, int T, int E, int K, int renorm, int G, int TG,
                           int32_t* ids, float* w, hipStream_t stream) {
   if (T == 0) return MOE_OK;
-  if (const int L = lanes_for(E, K, G)) {
+  if (const int L = route_lanes(E, K, G)) {
     launch_lanes_any<false>(L, logits, T, E, K, renorm, ids, w, MapOut{}, stream);
     return launch_status();
   }
@@ -455,7 +351,7 @@ moe_status_t launch_plan(const float* logits, int T, int E, int K, int renorm, i
                          uint8_t* mask, int32_t* offsets, int32_t* sorted_pairs,
                          int32_t* pair_row, hipStream_t stream) {
   const MapOut mo{start, E_local, S, rep_off, rep_slots, slot, w_masked, mask};
-  const int L = logits != nullptr ? lanes_for(E, K, G) : 0;
+  const int L = logits != nullptr ? route_lanes(E, K, G) : 0;
   if (L > 0 && T * L <= kPlanThreads) {
     if (L == 8)
       launch_plan_lanes<8>(logits, T, E, K, renorm, mo, offsets, sorted_pairs, pair_row, stream);
