@@ -418,10 +418,10 @@ moe_status_t launch_gemm_mxfp4(moe_gemm_op_t op, const void* a, const int32_t* s
                                const uint8_t* w, const uint8_t* w_scale, int H, int I, void* c,
                                bool c_f32, hipStream_t stream);
 
-// The whole expert part of a few tokens' layer from the slot map, pair by
-// pair (no permutation): act [T * topk, I] = the SwiGLU rows, then out = the
-// weighted sum of the down products, with shared and accumulate as in
-// launch_combine.
+// The layer of a few tokens, pair by pair (no permutation): the pairs' slots
+// (routed here, or from the slot map), act [T * topk, I] = the SwiGLU rows,
+// then out = the weighted sum of the down products, with shared and
+// accumulate as in launch_combine.
 moe_status_t launch_mxfp4_pairs(const void* x, const PairRouting& routing, int T, int topk,
                                 const uint8_t* w_gate_up, const uint8_t* gate_up_scale,
                                 const uint8_t* w_down, const uint8_t* down_scale, int H, int I,

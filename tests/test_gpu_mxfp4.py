@@ -365,6 +365,33 @@ def test_layer_grouped_routing(T):
     assert (np.abs(got - want) <= tol + 2.0 ** -8 * (np.abs(want) + tol) + 1e-38).all()
 
 
+@pytest.mark.parametrize("E,K", [(1, 1), (6, 6), (8, 2), (60, 4), (64, 8), (64, 9), (96, 8), (128, 16), (130, 2),
+                                 (256, 8), (200, 32), (300, 4)])
+@pytest.mark.parametrize("renormalize", [True, False])
+def test_few_tokens_in_every_router_form(E, K, renormalize):
+    """One and two tokens, whose products route for themselves where lanes of a wave hold the experts: the bits
+    of the same call on routed ids and weights, with logits that tie, one of two tokens with a NaN, a slot table that gives an
+    expert no slot, and a share."""
+    dev = device()
+    announce(f"mxfp4 few tokens E={E} K={K} renormalize={renormalize}")
+    for T in (1, 2):
+        for ep in (1, 2):
+            if E % ep:
+                continue
+            L = _layer(T, 64, 32, E, K, 51 + T, ep=ep, extra=1)
+            L["logits"][:, E // 3:2 * E // 3] = 0.5
+            if E > K and T == 2:
+                L["logits"][0, E - 1] = float("nan")
+            L["rs"] = L["rs"].clone()
+            L["rs"][-1] = 10 ** 6
+            ids, w = moe.route(L["logits"].to(dev), K, renormalize)
+            for rank in range(ep):
+                cfg = dict(out_dtype=torch.float32, renormalize=renormalize)
+                got = _run(dev, L, T, rank, logits=L["logits"], cfg=cfg)
+                want = _run(dev, L, T, rank, topk_ids=ids, topk_w=w, cfg=cfg)
+                assert torch.equal(torch.nan_to_num(got, 7e9), torch.nan_to_num(want, 7e9)), (T, ep, rank)
+
+
 def test_layer_is_its_stages():
     """forward against route, slot_map, permute, the two products and combine called one by one."""
     dev = device()
