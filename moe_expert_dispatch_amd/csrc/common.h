@@ -412,9 +412,10 @@ moe_status_t launch_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scale,
                                      void* w, bool bf16, hipStream_t stream);
 // Grouped products with MXFP4 weights and bf16 rows a. sorted_pairs non-null
 // (gate/up only): row r is a[sorted_pairs[r] / topk]. c is bf16, or f32 for
-// the down product with c_f32.
+// the down product with c_f32. rows: how many of at most max_rows to expect
+// (only the choice of the kernel goes by it).
 moe_status_t launch_gemm_mxfp4(moe_gemm_op_t op, const void* a, const int32_t* sorted_pairs,
-                               int topk, const int32_t* offsets, int S, int max_rows,
+                               int topk, const int32_t* offsets, int S, int max_rows, int rows,
                                const uint8_t* w, const uint8_t* w_scale, int H, int I, void* c,
                                bool c_f32, hipStream_t stream);
 

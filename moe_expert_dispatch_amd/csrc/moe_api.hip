@@ -435,6 +435,7 @@ moe_status_t moe_forward(const moe_config_t* cfg, const moe_forward_args_t* args
   // more: routing, slot map and permutation in one launch or two
   const bool pairs = mx && !on_input && T > 0 && T <= kPairTokens;
   const bool plan = mx && !on_input && !pairs && T > 0 && T * K <= kPlanPairs;
+  const int share_rows = (T * K + cfg->ep_size - 1) / cfg->ep_size;  // rows to expect here
   // the pairs' gate/up blocks route for themselves where lane groups do it
   const PairRouting pair_routing{
       args->logits, cfg->E_global, cfg->renormalize ? 1 : 0,
@@ -491,8 +492,8 @@ moe_status_t moe_forward(const moe_config_t* cfg, const moe_forward_args_t* args
   else if (mx)
     MOE_TRY(launch_gemm_mxfp4(MOE_GEMM_GATE_UP_SWIGLU, fused_gather ? args->x : x_perm,
                               fused_gather ? sorted_pairs : nullptr, K, offsets, S, T * K,
-                              static_cast<const uint8_t*>(args->w_gate_up), args->w_gate_up_e8m0,
-                              H, I, act, false, stream));
+                              share_rows, static_cast<const uint8_t*>(args->w_gate_up),
+                              args->w_gate_up_e8m0, H, I, act, false, stream));
   else if (fused_gather)
     MOE_TRY(launch_gemm_bf16_gate_up_gathered(args->x, T, K, sorted_pairs, offsets, S, T * K,
                                               args->w_gate_up, H, I, act, stream, gb));
@@ -505,7 +506,7 @@ moe_status_t moe_forward(const moe_config_t* cfg, const moe_forward_args_t* args
                             offsets, S, T * K, static_cast<const uint8_t*>(args->w_down),
                             args->w_down_scale, H, I, y, 1.0f, stream, gb));
   else if (mx)
-    MOE_TRY(launch_gemm_mxfp4(MOE_GEMM_DOWN, act, nullptr, 1, offsets, S, T * K,
+    MOE_TRY(launch_gemm_mxfp4(MOE_GEMM_DOWN, act, nullptr, 1, offsets, S, T * K, share_rows,
                               static_cast<const uint8_t*>(args->w_down), args->w_down_e8m0, H, I,
                               y, true, stream));
   else
@@ -571,7 +572,7 @@ moe_status_t moe_grouped_gemm_mxfp4(moe_gemm_op_t op, const void* a, const int32
   if (H % 32 != 0 || I % 32 != 0 || !dtype_ok(c_dt)) return MOE_ERR_UNSUPPORTED;
   if (op == MOE_GEMM_GATE_UP_SWIGLU && c_dt != MOE_DTYPE_BF16) return MOE_ERR_UNSUPPORTED;
   if (max_rows > 0 && (!w_scale || !aligned16(w_scale))) return MOE_ERR_INVALID_ARG;
-  return launch_gemm_mxfp4(op, a, nullptr, 1, offsets, S, max_rows, w, w_scale, H, I, c,
+  return launch_gemm_mxfp4(op, a, nullptr, 1, offsets, S, max_rows, max_rows, w, w_scale, H, I, c,
                            c_dt == MOE_DTYPE_F32, stream);
 }
 

@@ -961,8 +961,9 @@ __global__ __launch_bounds__(512) void mxfp4_pair_down_kernel(
   }
 }
 
-// Which kernel, by the rows a slot has on the average of all (max_rows / S:
-// the host knows no more). Both sides in us at 64 slots, Kd = 4096 / N = 1024
+// Which kernel, by the rows a slot has on the average of all (rows / S: the
+// rows to expect, those of one share of the tokens' pairs; the host knows no
+// more, and max_rows bounds them all). Both sides in us at 64 slots, Kd = 4096 / N = 1024
 // gate/up and Kd = 1024 / N = 4096 down: 16 rows a slot 71 and 42 streamed
 // (16 rows at a time), 88 and 45 split, but a slot past 16 streams its codes
 // twice (12 rows a slot on the average already have one in six past it); at 31
@@ -973,8 +974,8 @@ constexpr int kSplitRows2 = 56;
 
 template <int OP, bool GATHER, typename CT>
 void launch_product(const void* a, const int32_t* offsets, const int32_t* sorted_pairs, int topk,
-                    int S, int max_rows, const uint8_t* w, const uint8_t* w_scale, int N, int Kd,
-                    void* c, hipStream_t stream) {
+                    int S, int max_rows, int rows, const uint8_t* w, const uint8_t* w_scale,
+                    int N, int Kd, void* c, hipStream_t stream) {
   using std::integral_constant;
   constexpr int M = OP == MOE_GEMM_GATE_UP_SWIGLU ? 2 : 1;
   // Blocks for all tiles of `tr` rows, of which there are at most this many
@@ -986,19 +987,19 @@ void launch_product(const void* a, const int32_t* offsets, const int32_t* sorted
   const uint16_t* a16 = static_cast<const uint16_t*>(a);
   CT* ct = static_cast<CT*>(c);
   const bool aligned = Kd % 128 == 0;
-  if (max_rows > (M == 2 ? kSplitRows2 : kSplitRows1) * S) {
+  if (rows > (M == 2 ? kSplitRows2 : kSplitRows1) * S) {
     mxfp4_tile_kernel<OP, GATHER, CT><<<tile_blocks(kTileRows), 256, 0, stream>>>(
         a16, offsets, sorted_pairs, topk, S, max_rows, w, w_scale, N, Kd, ct);
     return;
   }
-  if (max_rows > kStreamRows * S) {
+  if (rows > kStreamRows * S) {
     auto go = [&](auto nt, auto al) {
       constexpr int NT = decltype(nt)::value;
       mxfp4_split_kernel<OP, GATHER, CT, NT, NT == 1 ? 2 : 4, decltype(al)::value>
           <<<tile_blocks(32 * NT), 512, 0, stream>>>(a16, offsets, sorted_pairs, topk, S,
                                                      max_rows, w, w_scale, N, Kd, ct);
     };
-    if (M == 1 || max_rows <= kSplitRows1 * S) {
+    if (M == 1 || rows <= kSplitRows1 * S) {
       if (aligned)
         go(integral_constant<int, 1>{}, std::true_type{});
       else
@@ -1036,20 +1037,37 @@ void launch_product(const void* a, const int32_t* offsets, const int32_t* sorted
   using i2 = integral_constant<int, 2>;
   using i4 = integral_constant<int, 4>;
   using i8 = integral_constant<int, 8>;
-  if constexpr (M == 2) {
-    if (aligned && Kd > 1024 && Kd <= 4096 && max_rows <= 2 * S && lines >= 16) {
-      auto quick = [&](auto wk) {
-        constexpr int WK = decltype(wk)::value;
-        mxfp4_quick_kernel<OP, GATHER, CT, WK>
-            <<<dim3(ceil_div(N, 16 * kStreamWaves / WK), lines), 64 * kStreamWaves, 0, stream>>>(
-                a16, offsets, sorted_pairs, topk, S, max_rows, max_rows < S, w, w_scale, N, Kd, ct);
-      };
+  // Short blocks (mxfp4_quick_kernel), us against the streaming kernel's at
+  // rows drawn evenly over the slots. Gate/up: up to two rows a slot (past that
+  // the codes come twice: 81 at 4), where three quarters of the steps hold k's
+  // (Kd = 4096 66 : 77, 2048 36 : 46; but 2560 49 : 40, 1536 25 : 19) and the
+  // other's blocks are more than one round (64 x 4 blocks, Kd = 2048: 19 : 15).
+  // Down, one step or two: up to 1.5 rows (Kd = 1024 26 : 27 and 512 8.0 : 9.2 at one
+  // row, 35 : 34 and 10.5 : 10.4 at two; Kd = 1536 152 : 123).
+  const long long blocks = (long long)ceil_div(N, 16 * kStreamWaves) * lines;
+  const bool one_round = split == 1 && blocks <= want;
+  const int steps = Kd <= 2048 ? 2048 : 4096;  // k's of the gate/up form's 4 or 8 steps
+  if (aligned && lines >= 16 &&
+      (M == 2 ? Kd <= 4096 && 4 * Kd > 3 * steps && rows <= 2 * S && !one_round
+              : Kd <= 1024 && 2 * rows <= 3 * S)) {
+    auto quick = [&](auto wk) {
+      constexpr int WK = decltype(wk)::value;
+      mxfp4_quick_kernel<OP, GATHER, CT, WK>
+          <<<dim3(ceil_div(N, 16 * kStreamWaves / WK), lines), 64 * kStreamWaves, 0, stream>>>(
+              a16, offsets, sorted_pairs, topk, S, max_rows, max_rows < S, w, w_scale, N, Kd, ct);
+    };
+    if constexpr (M == 2) {
       if (Kd <= 2048)
         quick(i4{});
       else
         quick(i8{});
-      return;
+    } else {
+      if (Kd <= 512)
+        quick(i1{});
+      else
+        quick(i2{});
     }
+    return;
   }
   auto pick = [&](auto rb) {
     // one window, and of it one step of 512 a wave
@@ -1086,7 +1104,11 @@ void launch_product(const void* a, const int32_t* offsets, const int32_t* sorted
       go(i1{}, rb, i2{}, std::true_type{}, std::true_type{});
     }
   };
-  if (max_rows <= 4 * S)
+  // Rows at a time: 16, so that few slots read their codes twice (at 4 rows a
+  // slot on the average 16 us against 26, S = 64, N = 512, Kd = 2048), but 8 where
+  // they fill the rows' LDS by themselves (Kd = 4096: 80 against 99 us at 3, 94
+  // and 94 at 6).
+  if (M == 2 && Kd >= 4096 && rows <= 4 * S)
     pick(i8{});
   else
     pick(integral_constant<int, 16>{});
@@ -1125,22 +1147,22 @@ moe_status_t launch_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scale,
 }
 
 moe_status_t launch_gemm_mxfp4(moe_gemm_op_t op, const void* a, const int32_t* sorted_pairs,
-                               int topk, const int32_t* offsets, int S, int max_rows,
+                               int topk, const int32_t* offsets, int S, int max_rows, int rows,
                                const uint8_t* w, const uint8_t* w_scale, int H, int I, void* c,
                                bool c_f32, hipStream_t stream) {
   if (max_rows == 0) return MOE_OK;
   if (op == MOE_GEMM_GATE_UP_SWIGLU) {
     if (sorted_pairs != nullptr)
       launch_product<MOE_GEMM_GATE_UP_SWIGLU, true, uint16_t>(
-          a, offsets, sorted_pairs, topk, S, max_rows, w, w_scale, I, H, c, stream);
+          a, offsets, sorted_pairs, topk, S, max_rows, rows, w, w_scale, I, H, c, stream);
     else
       launch_product<MOE_GEMM_GATE_UP_SWIGLU, false, uint16_t>(
-          a, offsets, nullptr, 1, S, max_rows, w, w_scale, I, H, c, stream);
+          a, offsets, nullptr, 1, S, max_rows, rows, w, w_scale, I, H, c, stream);
   } else if (c_f32) {
-    launch_product<MOE_GEMM_DOWN, false, float>(a, offsets, nullptr, 1, S, max_rows, w, w_scale,
-                                                H, I, c, stream);
+    launch_product<MOE_GEMM_DOWN, false, float>(a, offsets, nullptr, 1, S, max_rows, rows, w,
+                                                w_scale, H, I, c, stream);
   } else {
-    launch_product<MOE_GEMM_DOWN, false, uint16_t>(a, offsets, nullptr, 1, S, max_rows, w,
+    launch_product<MOE_GEMM_DOWN, false, uint16_t>(a, offsets, nullptr, 1, S, max_rows, rows, w,
                                                    w_scale, H, I, c, stream);
   }
   return launch_status();
