@@ -111,42 +111,38 @@ struct StepWeights {
   uint32_t s[M][RUN];
 };
 
-// ALIGNED: Kd is a multiple of 128, so a row's scales start at a whole word
-// and a 128 has one word of them.
-template <int M, int RUN, bool ALIGNED>
+// The codes' loads stand in no branch, so that they can be waited for one by
+// one: at and behind kend (a wave's last k, Kd at most) they fetch the row's
+// last 32 k's before it again, and the token rows in LDS hold zeros there (a
+// NaN scale among them is one of the same row, whose outputs are NaN already).
+// The scales of a whole step come in one load, of whatever alignment the row
+// has (a load for each 128 costs a quarter of the time at Kd = 4096).
+template <int M, int RUN>
 __device__ __forceinline__ void load_step(StepWeights<M, RUN>& v, const uint8_t* __restrict__ w,
                                           const uint8_t* __restrict__ w_scale,
                                           const uint32_t (&row)[M], int Kd, int k0, int kend,
                                           int g) {
 #pragma unroll
   for (int i = 0; i < M; ++i) {
-    const uint32_t cb = row[i] * (uint32_t)(Kd / 2) + (uint32_t)k0 / 2 + 16 * g;
-    const uint32_t sb = row[i] * (uint32_t)(Kd / 32) + (uint32_t)k0 / 32;
+    const uint32_t cb = row[i] * (uint32_t)(Kd / 2);
+    const uint32_t sb = row[i] * (uint32_t)(Kd / 32);
 #pragma unroll
     for (int j = 0; j < RUN; ++j)
-      v.q[i][j] = k0 + 128 * j + 32 * g < kend
-                      ? *reinterpret_cast<const uint4*>(w + (cb + 64 * j))
-                      : make_uint4(0, 0, 0, 0);
-    if (ALIGNED && k0 + 128 * RUN <= kend) {
-      uint32_t t[RUN];
-      __builtin_memcpy(t, __builtin_assume_aligned(w_scale + sb, 4), sizeof(t));
-#pragma unroll
-      for (int j = 0; j < RUN; ++j) v.s[i][j] = t[j];
+      v.q[i][j] = *reinterpret_cast<const uint4*>(
+          w + (cb + (uint32_t)min(k0 + 128 * j + 32 * g, kend - 32) / 2));
+    if (k0 + 128 * RUN <= kend) {
+      __builtin_memcpy(v.s[i], w_scale + (sb + (uint32_t)k0 / 32), 4 * RUN);
     } else {
 #pragma unroll
-      for (int j = 0; j < RUN; ++j) {
-        v.s[i][j] = 0;
-        if constexpr (ALIGNED) {
-          if (k0 + 128 * j < kend)
-            v.s[i][j] = *reinterpret_cast<const uint32_t*>(w_scale + (sb + 4 * j));
-        } else {
-          if (k0 + 128 * j + 32 * g < kend)
-            v.s[i][j] = (uint32_t)w_scale[sb + 4 * j + g] << (8 * g);
-        }
-      }
+      for (int j = 0; j < RUN; ++j)
+        v.s[i][j] =
+            (uint32_t)w_scale[sb + (uint32_t)min(k0 + 128 * j + 32 * g, kend - 32) / 32] << (8 * g);
     }
   }
 }
+
+// The scale of a lane's codes of one run.
+__device__ __forceinline__ float step_scale(uint32_t s, int g) { return e8m0((s >> (8 * g)) & 255u); }
 
 // The slot of blockIdx.y: itself, or with `find` the blockIdx.y-th slot that
 // has rows (fewer rows than slots: the grid then has one line a row). Every
@@ -195,7 +191,7 @@ __host__ __device__ inline int stream_window(int Kd, int RB, int WK) {
 // 16-byte vectors of a row in LDS: one more, so that rows start in other banks
 __host__ __device__ inline int stream_row_vecs(int window) { return window / 8 + 1; }
 
-template <int OP, bool GATHER, typename CT, int WK, int RB, int RUN, bool PIPE, bool ALIGNED,
+template <int OP, bool GATHER, typename CT, int WK, int RB, int RUN, bool PIPE,
           bool PAIRS = false>
 __global__ __launch_bounds__(64 * kStreamWaves) void mxfp4_stream_kernel(
     const uint16_t* __restrict__ a, const int32_t* __restrict__ offsets,
@@ -257,7 +253,7 @@ __global__ __launch_bounds__(64 * kStreamWaves) void mxfp4_stream_kernel(
 #pragma unroll
     for (int i = 0; i < M; ++i) acc[i] = floatx4{0.f, 0.f, 0.f, 0.f};
     StepWeights<M, RUN> cur, next;
-    load_step<M, RUN, ALIGNED>(cur, ws, ss, wrow, Kd, wk * per, min((wk + 1) * per, Kd), g);
+    load_step<M, RUN>(cur, ws, ss, wrow, Kd, wk * per, min((wk + 1) * per, Kd), g);
     for (int base = 0; base < Kd; base += window) {
       if (base != 0) __syncthreads();  // the last window is read
       // a wave fetches 512 k's of a row at a time
@@ -281,7 +277,7 @@ __global__ __launch_bounds__(64 * kStreamWaves) void mxfp4_stream_kernel(
           // the next step's codes: in this window, or the first of the next
           const bool last = at + 128 * RUN >= per;
           const int nbase = base + (last ? window : 0) + wk * per;
-          load_step<M, RUN, ALIGNED>(next, ws, ss, wrow, Kd, nbase + (last ? 0 : at + 128 * RUN),
+          load_step<M, RUN>(next, ws, ss, wrow, Kd, nbase + (last ? 0 : at + 128 * RUN),
                                      min(nbase + per, Kd), g);
         }
         const uint4* x = lds + (m < nr ? m : 0) * rvecs + (wk * per + at) / 8 + 4 * g;
@@ -293,7 +289,7 @@ __global__ __launch_bounds__(64 * kStreamWaves) void mxfp4_stream_kernel(
           for (int e = 0; e < 4; ++e) b[e] = m < nr ? x[16 * j + e] : make_uint4(0, 0, 0, 0);
 #pragma unroll
           for (int i = 0; i < M; ++i) {
-            const float sc = e8m0((cur.s[i][j] >> (8 * g)) & 255u);
+            const float sc = step_scale(cur.s[i][j], g);
             const uint32_t qq[4] = {cur.q[i][j].x, cur.q[i][j].y, cur.q[i][j].z, cur.q[i][j].w};
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -368,7 +364,7 @@ __global__ __launch_bounds__(64 * kStreamWaves) void mxfp4_quick_kernel(
   const size_t rows_s = (size_t)s * M * N;
   const uint8_t* ws = w + rows_s * (size_t)(Kd / 2);
   const uint8_t* ss = w_scale + rows_s * (size_t)(Kd / 32);
-  const int per = ceil_div(Kd / 128, WK) * 128;  // at most 128 * RUN
+  const int per = ceil_div(ceil_div(Kd, 128), WK) * 128;  // at most 128 * RUN
   const int k0 = wk * per;
   const int kend = min(k0 + per, Kd);
   for (int rt = r0; rt < r1; rt += RB) {
@@ -377,7 +373,7 @@ __global__ __launch_bounds__(64 * kStreamWaves) void mxfp4_quick_kernel(
     asm volatile("" ::: "memory");
     const int nr = min(r1 - rt, RB);
     StepWeights<M, RUN> v;
-    load_step<M, RUN, true>(v, ws, ss, wrow, Kd, k0, kend, g);
+    load_step<M, RUN>(v, ws, ss, wrow, Kd, k0, kend, g);
     for (int r = 0; r < nr; ++r) {
       int row = rt + r;
       if constexpr (GATHER) row = sorted_pairs[row] / topk;
@@ -398,7 +394,7 @@ __global__ __launch_bounds__(64 * kStreamWaves) void mxfp4_quick_kernel(
       for (int e = 0; e < 4; ++e) b[e] = m < nr ? x[16 * j + e] : make_uint4(0, 0, 0, 0);
 #pragma unroll
       for (int i = 0; i < M; ++i) {
-        const float sc = e8m0((v.s[i][j] >> (8 * g)) & 255u);
+        const float sc = step_scale(v.s[i][j], g);
         const uint32_t qq[4] = {v.q[i][j].x, v.q[i][j].y, v.q[i][j].z, v.q[i][j].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -885,7 +881,7 @@ __global__ __launch_bounds__(512, U == 2 ? 2 : 1) void mxfp4_split_kernel(
 // k's) units; each adds weight * partial product to its sums, and the sums
 // are added in LDS in wave order. Of the 16 token columns of the matrix
 // instruction one is used: the codes' stream, not the product, is the bound.
-template <typename OT, bool ALIGNED>
+template <typename OT>
 __global__ __launch_bounds__(512) void mxfp4_pair_down_kernel(
     const uint16_t* __restrict__ act, const int32_t* __restrict__ slot,
     const uint8_t* __restrict__ mask, const float* __restrict__ weight, int topk, int S,
@@ -908,7 +904,7 @@ __global__ __launch_bounds__(512) void mxfp4_pair_down_kernel(
     if (mask[p] == 0 || s < 0 || s >= S) continue;  // the same for the whole wave
     const float wt = weight[p];
     StepWeights<1, RUN> v;
-    load_step<1, RUN, ALIGNED>(v, w + (size_t)s * N * (size_t)(Kd / 2),
+    load_step<1, RUN>(v, w + (size_t)s * N * (size_t)(Kd / 2),
                                w_scale + (size_t)s * N * (size_t)(Kd / 32), row, Kd, k0,
                                min(k0 + 128 * RUN, Kd), g);
     const uint16_t* x = act + (size_t)p * Kd + k0 + 32 * g;
@@ -923,7 +919,7 @@ __global__ __launch_bounds__(512) void mxfp4_pair_down_kernel(
     floatx4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < RUN; ++j) {
-      const float sc = e8m0((v.s[0][j] >> (8 * g)) & 255u);
+      const float sc = step_scale(v.s[0][j], g);
       const uint32_t qq[4] = {v.q[0][j].x, v.q[0][j].y, v.q[0][j].z, v.q[0][j].w};
 #pragma unroll
       for (int e = 0; e < 4; ++e)
@@ -1013,12 +1009,11 @@ void launch_product(const void* a, const int32_t* offsets, const int32_t* sorted
     return;
   }
   const int lines = max_rows < S ? max_rows : S;  // slots that can have rows
-  auto go = [&](auto wk, auto rb, auto run, auto pipe, auto al) {
+  auto go = [&](auto wk, auto rb, auto run, auto pipe) {
     constexpr int WK = decltype(wk)::value, RB = decltype(rb)::value;
     const size_t rows_lds = (size_t)RB * stream_row_vecs(stream_window(Kd, RB, WK)) * 16;
     const size_t red_lds = WK > 1 ? (size_t)kStreamWaves * M * kWave * 16 : 0;
-    mxfp4_stream_kernel<OP, GATHER, CT, WK, RB, decltype(run)::value, decltype(pipe)::value,
-                        decltype(al)::value>
+    mxfp4_stream_kernel<OP, GATHER, CT, WK, RB, decltype(run)::value, decltype(pipe)::value>
         <<<dim3(ceil_div(N, 16 * kStreamWaves / WK), lines), 64 * kStreamWaves,
            rows_lds > red_lds ? rows_lds : red_lds, stream>>>(
             a16, offsets, sorted_pairs, topk, S, max_rows, max_rows < S, w, w_scale, N, Kd, ct,
@@ -1047,7 +1042,7 @@ void launch_product(const void* a, const int32_t* offsets, const int32_t* sorted
   const long long blocks = (long long)ceil_div(N, 16 * kStreamWaves) * lines;
   const bool one_round = split == 1 && blocks <= want;
   const int steps = Kd <= 2048 ? 2048 : 4096;  // k's of the gate/up form's 4 or 8 steps
-  if (aligned && lines >= 16 &&
+  if (lines >= 16 &&
       (M == 2 ? Kd <= 4096 && 4 * Kd > 3 * steps && rows <= 2 * S && !one_round
               : Kd <= 1024 && 2 * rows <= 3 * S)) {
     auto quick = [&](auto wk) {
@@ -1073,45 +1068,41 @@ void launch_product(const void* a, const int32_t* offsets, const int32_t* sorted
     // one window, and of it one step of 512 a wave
     const int window = stream_window(Kd, decltype(rb)::value, split);
     const bool one = window >= Kd && window <= 512 * split;
-    if (!aligned) {
-      if (split == 1)
-        go(i1{}, rb, i2{}, std::true_type{}, std::false_type{});
-      else
-        go(i8{}, rb, i2{}, std::true_type{}, std::false_type{});
+    if constexpr (decltype(rb)::value == 8) {  // 4096 k's or more
+      if (one)
+        go(i8{}, rb, i4{}, std::false_type{});
+      else if (split > 1)
+        go(i8{}, rb, i2{}, std::true_type{});
+      else  // 512 a step: one block a compute unit (164 registers), 60 against 66 us
+        go(i1{}, rb, i4{}, std::true_type{});
     } else if (one) {
       if (split == 1)
-        go(i1{}, rb, i4{}, std::false_type{}, std::true_type{});
+        go(i1{}, rb, i4{}, std::false_type{});
       else if (split == 2)
-        go(i2{}, rb, i4{}, std::false_type{}, std::true_type{});
+        go(i2{}, rb, i4{}, std::false_type{});
       else if (split == 4)
-        go(i4{}, rb, i4{}, std::false_type{}, std::true_type{});
+        go(i4{}, rb, i4{}, std::false_type{});
       else
-        go(i8{}, rb, i4{}, std::false_type{}, std::true_type{});
+        go(i8{}, rb, i4{}, std::false_type{});
     } else if (split > 1) {
-      go(i8{}, rb, i2{}, std::true_type{}, std::true_type{});
+      go(i8{}, rb, i2{}, std::true_type{});
     } else if constexpr (M == 1) {
-      go(i1{}, rb, i4{}, std::true_type{}, std::true_type{});
-    } else {
-      // 512 a step: one block of gate/up a compute unit (164 registers), 60 against 66 us at
-      // S = 64, N = 1024, Kd = 4096; at Kd = 2048 two blocks with steps of 256 win, 15.5
-      // against 16.6 us (N = 512), and with 16 rows everywhere (71 against 75 us)
-      if constexpr (decltype(rb)::value == 8) {
-        if (Kd >= 4096) {
-          go(i1{}, rb, i4{}, std::true_type{}, std::true_type{});
-          return;
-        }
-      }
-      go(i1{}, rb, i2{}, std::true_type{}, std::true_type{});
+      go(i1{}, rb, i4{}, std::true_type{});
+    } else {  // 256 a step, two blocks of gate/up: 15.5 against 16.6 us (N = 512, Kd = 2048)
+      go(i1{}, rb, i2{}, std::true_type{});
     }
   };
   // Rows at a time: 16, so that few slots read their codes twice (at 4 rows a
   // slot on the average 16 us against 26, S = 64, N = 512, Kd = 2048), but 8 where
   // they fill the rows' LDS by themselves (Kd = 4096: 80 against 99 us at 3, 94
   // and 94 at 6).
-  if (M == 2 && Kd >= 4096 && rows <= 4 * S)
-    pick(i8{});
-  else
-    pick(integral_constant<int, 16>{});
+  if constexpr (M == 2) {
+    if (Kd >= 4096 && rows <= 4 * S) {
+      pick(i8{});
+      return;
+    }
+  }
+  pick(integral_constant<int, 16>{});
 }
 
 }  // namespace
@@ -1177,45 +1168,37 @@ moe_status_t launch_mxfp4_pairs(const void* x, const PairRouting& routing, int T
   const int P = T * topk;
   const int S = routing.map.S;
   uint16_t* act16 = static_cast<uint16_t*>(act);
-  auto gate_up = [&](auto wk, auto pipe, auto al) {
+  auto gate_up = [&](auto wk, auto pipe) {
     constexpr int WK = decltype(wk)::value, RB = 8;
     constexpr int RUN = decltype(pipe)::value ? 2 : 4;
     const size_t rows_lds = (size_t)stream_row_vecs(stream_window(H, RB, WK)) * 16;  // one row
     const size_t red_lds = WK > 1 ? (size_t)kStreamWaves * 2 * kWave * 16 : 0;
     mxfp4_stream_kernel<MOE_GEMM_GATE_UP_SWIGLU, true, uint16_t, WK, RB, RUN,
-                        decltype(pipe)::value, decltype(al)::value, true>
+                        decltype(pipe)::value, true>
         <<<dim3(ceil_div(I, 16 * kStreamWaves / WK), P), 64 * kStreamWaves,
            rows_lds > red_lds ? rows_lds : red_lds, stream>>>(
             static_cast<const uint16_t*>(x), nullptr, nullptr, topk, S, P, 0, w_gate_up,
             gate_up_scale, I, H, act16, routing);
   };
-  if (H % 128 != 0)
-    gate_up(integral_constant<int, 8>{}, std::true_type{}, std::false_type{});
-  else if (H > 4096)
-    gate_up(integral_constant<int, 8>{}, std::true_type{}, std::true_type{});
+  if (H > 4096)
+    gate_up(integral_constant<int, 8>{}, std::true_type{});
   else if (H > 2048)
-    gate_up(integral_constant<int, 8>{}, std::false_type{}, std::true_type{});
+    gate_up(integral_constant<int, 8>{}, std::false_type{});
   else
-    gate_up(integral_constant<int, 4>{}, std::false_type{}, std::true_type{});
+    gate_up(integral_constant<int, 4>{}, std::false_type{});
   const moe_status_t st = launch_status();
   if (st != MOE_OK) return st;
-  auto down = [&](auto o, auto al) {
+  auto down = [&](auto o) {
     using OT = decltype(o);
-    mxfp4_pair_down_kernel<OT, decltype(al)::value><<<dim3(H / 16, T), 512, 0, stream>>>(
-        act16, routing.map.slot, routing.map.mask, routing.map.w_masked, topk, S, w_down, down_scale, H, I, static_cast<OT*>(out),
-        accumulate, static_cast<const uint16_t*>(shared));
+    mxfp4_pair_down_kernel<OT><<<dim3(H / 16, T), 512, 0, stream>>>(
+        act16, routing.map.slot, routing.map.mask, routing.map.w_masked, topk, S, w_down,
+        down_scale, H, I, static_cast<OT*>(out), accumulate,
+        static_cast<const uint16_t*>(shared));
   };
-  if (out_bf16) {
-    if (I % 128 == 0)
-      down(uint16_t{}, std::true_type{});
-    else
-      down(uint16_t{}, std::false_type{});
-  } else {
-    if (I % 128 == 0)
-      down(float{}, std::true_type{});
-    else
-      down(float{}, std::false_type{});
-  }
+  if (out_bf16)
+    down(uint16_t{});
+  else
+    down(float{});
   return launch_status();
 }
 
