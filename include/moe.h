@@ -341,7 +341,8 @@ moe_status_t moe_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scale, in
  * the down product (c_dt). H % 32 == 0 and I % 32 == 0. Products are exact
  * (a code times its scale is a bf16 value), sums f32, one rounding to c_dt;
  * the order of the sums depends on max_rows, S and the shape, not on the
- * scheduling. A weight whose scale byte is 255 makes its outputs NaN. The
+ * scheduling. A weight whose scale byte is 255 makes its outputs NaN, one past
+ * bf16's range (scale bytes 253 and 254 with large codes) not finite. The
  * other rules are those of moe_grouped_gemm; w_scale is 16-byte aligned.
  */
 moe_status_t moe_grouped_gemm_mxfp4(moe_gemm_op_t op, const void* a, const int32_t* offsets,

@@ -114,7 +114,8 @@ struct StepWeights {
 // The codes' loads stand in no branch, so that they can be waited for one by
 // one: at and behind kend (a wave's last k, Kd at most) they fetch the row's
 // last 32 k's before it again, and the token rows in LDS hold zeros there (a
-// NaN scale among them is one of the same row, whose outputs are NaN already).
+// weight among them that is no number is one of the same row, whose outputs
+// are none already).
 // The scales of a whole step come in one load, of whatever alignment the row
 // has (a load for each 128 costs a quarter of the time at Kd = 4096).
 template <int M, int RUN>
@@ -528,7 +529,9 @@ __device__ __forceinline__ void tile_product(uint4 (*stage)[kTileRows * 8],
 #pragma unroll
     for (int t = 0; t < NT; ++t) acc[i][t] = floatx16{};
 
-  // thread tid fetches chunk tid % 8 of rows tid / 8 + 32 i
+  // Thread tid fetches chunk tid % 8 of rows tid / 8 + 32 i. Loads stand in no
+  // branch (see load_step): past Kd they fetch what was before it again, and
+  // zeros are put for the tokens.
   const int chunk = tid & 7;
   uint4 fa[NT];
   auto fetch = [&](int k0) {
@@ -559,14 +562,8 @@ __device__ __forceinline__ void tile_product(uint4 (*stage)[kTileRows * 8],
         ss[i][u] = w_scale[at / 16];
       }
   };
-  auto compute = [&](int b, int u, int k0) {
-    if (k0 + kStage > Kd && k0 + 32 * h >= Kd) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        q[i][u] = make_uint4(0, 0, 0, 0);
-        sc[i][u] = 127;
-      }
-    }
+  auto compute = [&](int b, int u) {
+    __builtin_amdgcn_sched_barrier(0);  // the next stage's loads are on their way
     const float s0 = e8m0(sc[0][u]), s1 = e8m0(sc[1][u]);
     const uint32_t q0[4] = {q[0][u].x, q[0][u].y, q[0][u].z, q[0][u].w};
     const uint32_t q1[4] = {q[1][u].x, q[1][u].y, q[1][u].z, q[1][u].w};
@@ -600,7 +597,7 @@ __device__ __forceinline__ void tile_product(uint4 (*stage)[kTileRows * 8],
     for (int v = 0; v < 2; ++v) {  // the stage in buffer v, the next into the other
       fetch(k0 + (v + 1) * kStage);
       if (U == 1 || v == 0) load_codes(k0 + (U == 1 ? v + 1 : 2) * kStage, qn, scn);
-      compute(v, U == 1 ? 0 : v, k0 + v * kStage);
+      compute(v, U == 1 ? 0 : v);
       put(v ^ 1, k0 + (v + 1) * kStage);
       __syncthreads();
       if (U == 1 || v == 1) {
@@ -695,7 +692,7 @@ __global__ __launch_bounds__(256, 2) void mxfp4_tile_kernel(
 // 64 rows against 137. For the down product (Kd = 1024) NT = 1 takes 43 to 47
 // us against 51 to 57, NT = 2 no less than the tiles above (68 to 88 against
 // 57 to 65), so it is not there.
-template <int OP, bool GATHER, typename CT, int NT, int U, bool ALIGNED>
+template <int OP, bool GATHER, typename CT, int NT, int U>
 __global__ __launch_bounds__(512, U == 2 ? 2 : 1) void mxfp4_split_kernel(
     const uint16_t* __restrict__ a, const int32_t* __restrict__ offsets,
     const int32_t* __restrict__ sorted_pairs, int topk, int S, int max_rows,
@@ -737,24 +734,21 @@ __global__ __launch_bounds__(512, U == 2 ? 2 : 1) void mxfp4_split_kernel(
   auto load_codes = [&](Codes& v, int kb) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const uint32_t cb = row[i] * (uint32_t)(Kd / 2) + (uint32_t)kb / 2 + 16 * h;
-      const uint32_t sb = row[i] * (uint32_t)(Kd / 32) + (uint32_t)kb / 32;
+      const uint32_t cb = row[i] * (uint32_t)(Kd / 2);
+      const uint32_t sb = row[i] * (uint32_t)(Kd / 32);
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        v.q[i][u] = kb + 64 * u + 32 * h < Kd
-                        ? *reinterpret_cast<const uint4*>(ws + (cb + 32 * u))
-                        : make_uint4(0, 0, 0, 0);
-      if (ALIGNED && kb + kRun64 <= Kd) {
-#pragma unroll
-        for (int x = 0; x < U / 2; ++x)
-          v.s[i][x] = *reinterpret_cast<const uint32_t*>(ss + (sb + 4 * x));
+        v.q[i][u] = *reinterpret_cast<const uint4*>(
+            ws + (cb + (uint32_t)min(kb + 64 * u + 32 * h, Kd - 32) / 2));
+      if (kb + kRun64 <= Kd) {
+        __builtin_memcpy(v.s[i], ss + (sb + (uint32_t)kb / 32), 2 * U);
       } else {
 #pragma unroll
         for (int x = 0; x < U / 2; ++x) v.s[i][x] = 0;
 #pragma unroll
         for (int u = 0; u < U; ++u)
-          if (kb + 64 * u + 32 * h < Kd)
-            v.s[i][u / 2] |= (uint32_t)ss[sb + 2 * u + h] << (16 * (u & 1) + 8 * h);
+          v.s[i][u / 2] |= (uint32_t)ss[sb + (uint32_t)min(kb + 64 * u + 32 * h, Kd - 32) / 32]
+                           << (16 * (u & 1) + 8 * h);
       }
     }
   };
@@ -764,22 +758,26 @@ __global__ __launch_bounds__(512, U == 2 ? 2 : 1) void mxfp4_split_kernel(
   for (int i = 0; i < NT; ++i) {
     int r = r0 + min((tid >> 3) + 32 * i, rows - 1);
     if constexpr (GATHER) r = sorted_pairs[r] / topk;
-    src[i] = a + (size_t)r * Kd + 8 * (tid & 7);
+    src[i] = a + (size_t)r * Kd;
   }
   uint4 fa[kFetch];
+  const int chunk = tid & 7;
   auto fetch = [&](int kb) {
 #pragma unroll
-    for (int i = 0; i < kFetch; ++i) {
-      const int k = kb + 64 * (i / NT);
-      fa[i] = k + 8 * (tid & 7) < Kd ? *reinterpret_cast<const uint4*>(src[i % NT] + k)
-                                     : make_uint4(0, 0, 0, 0);
-    }
+    for (int i = 0; i < kFetch; ++i)
+      fa[i] = *reinterpret_cast<const uint4*>(src[i % NT] +
+                                              min(kb + 64 * (i / NT) + 8 * chunk, Kd - 8));
   };
-  auto put = [&](int b) {
+  auto put = [&](int b, int kb) {
+    if (kb + kRun64 > Kd) {
+#pragma unroll
+      for (int i = 0; i < kFetch; ++i)
+        if (kb + 64 * (i / NT) + 8 * chunk >= Kd) fa[i] = make_uint4(0, 0, 0, 0);
+    }
 #pragma unroll
     for (int i = 0; i < kFetch; ++i) {
       const int r = (tid >> 3) + 32 * (i % NT);
-      stage[half][b][(i / NT) * TR * 8 + r * 8 + ((tid & 7) ^ ((r >> 1) & 7))] = fa[i];
+      stage[half][b][(i / NT) * TR * 8 + r * 8 + (chunk ^ ((r >> 1) & 7))] = fa[i];
     }
   };
 
@@ -793,7 +791,7 @@ __global__ __launch_bounds__(512, U == 2 ? 2 : 1) void mxfp4_split_kernel(
   Codes cur, next;
   load_codes(cur, kb0);
   fetch(kb0);
-  put(0);
+  put(0, kb0);
   __syncthreads();
   for (int st = 0; st < steps; ++st) {
     const int kn = kb0 + (st + 1) * 2 * kRun64;
@@ -824,7 +822,7 @@ __global__ __launch_bounds__(512, U == 2 ? 2 : 1) void mxfp4_split_kernel(
       }
     }
     if (st + 1 < steps) {
-      put(b ^ 1);
+      put(b ^ 1, kn);
       cur = next;
     }
     __syncthreads();
@@ -982,30 +980,22 @@ void launch_product(const void* a, const int32_t* offsets, const int32_t* sorted
   };
   const uint16_t* a16 = static_cast<const uint16_t*>(a);
   CT* ct = static_cast<CT*>(c);
-  const bool aligned = Kd % 128 == 0;
   if (rows > (M == 2 ? kSplitRows2 : kSplitRows1) * S) {
     mxfp4_tile_kernel<OP, GATHER, CT><<<tile_blocks(kTileRows), 256, 0, stream>>>(
         a16, offsets, sorted_pairs, topk, S, max_rows, w, w_scale, N, Kd, ct);
     return;
   }
   if (rows > kStreamRows * S) {
-    auto go = [&](auto nt, auto al) {
+    auto go = [&](auto nt) {
       constexpr int NT = decltype(nt)::value;
-      mxfp4_split_kernel<OP, GATHER, CT, NT, NT == 1 ? 2 : 4, decltype(al)::value>
+      mxfp4_split_kernel<OP, GATHER, CT, NT, NT == 1 ? 2 : 4>
           <<<tile_blocks(32 * NT), 512, 0, stream>>>(a16, offsets, sorted_pairs, topk, S,
                                                      max_rows, w, w_scale, N, Kd, ct);
     };
-    if (M == 1 || rows <= kSplitRows1 * S) {
-      if (aligned)
-        go(integral_constant<int, 1>{}, std::true_type{});
-      else
-        go(integral_constant<int, 1>{}, std::false_type{});
-    } else if constexpr (M == 2) {
-      if (aligned)
-        go(integral_constant<int, 2>{}, std::true_type{});
-      else
-        go(integral_constant<int, 2>{}, std::false_type{});
-    }
+    if (M == 1 || rows <= kSplitRows1 * S)
+      go(integral_constant<int, 1>{});
+    else if constexpr (M == 2)
+      go(integral_constant<int, 2>{});
     return;
   }
   const int lines = max_rows < S ? max_rows : S;  // slots that can have rows
