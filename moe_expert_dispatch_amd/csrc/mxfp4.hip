@@ -962,6 +962,11 @@ __global__ __launch_bounds__(512) void mxfp4_pair_down_kernel(
 // (16 rows at a time), 88 and 45 split, but a slot past 16 streams its codes
 // twice (12 rows a slot on the average already have one in six past it); at 31
 // 88 and 46 split, but past 32 twice; at 64 113 split by 64 rows, 137 in tiles.
+// A few large slots leave the chip empty with tiles of 160 rows, so there the
+// smaller ones are taken while all of them run at once: 8 slots of 100 rows,
+// Kd = 4096 / N = 1024: 38 us by 32 rows, 41 by 64, 71 in tiles; of 160 rows 59, 43
+// and 70; of 500 115, 83 and 76. Down, Kd = 1024 / N = 4096, 32 rows and tiles:
+// 20 and 25 us at 100 rows, 35 and 27 at 250.
 constexpr int kStreamRows = 10;
 constexpr int kSplitRows1 = 24;
 constexpr int kSplitRows2 = 56;
@@ -980,22 +985,30 @@ void launch_product(const void* a, const int32_t* offsets, const int32_t* sorted
   };
   const uint16_t* a16 = static_cast<const uint16_t*>(a);
   CT* ct = static_cast<CT*>(c);
-  if (rows > (M == 2 ? kSplitRows2 : kSplitRows1) * S) {
-    mxfp4_tile_kernel<OP, GATHER, CT><<<tile_blocks(kTileRows), 256, 0, stream>>>(
-        a16, offsets, sorted_pairs, topk, S, max_rows, w, w_scale, N, Kd, ct);
-    return;
-  }
+  const long long want = device_cu_count();
   if (rows > kStreamRows * S) {
-    auto go = [&](auto nt) {
+    // tiles of `tr` rows to expect, the slots' last ones half full
+    auto tiles = [&](int tr) {
+      return ((long long)rows / tr + (S + 1) / 2) * ceil_div(N, kTileWeights / M);
+    };
+    auto split = [&](auto nt) {
       constexpr int NT = decltype(nt)::value;
       mxfp4_split_kernel<OP, GATHER, CT, NT, NT == 1 ? 2 : 4>
           <<<tile_blocks(32 * NT), 512, 0, stream>>>(a16, offsets, sorted_pairs, topk, S,
                                                      max_rows, w, w_scale, N, Kd, ct);
     };
-    if (M == 1 || rows <= kSplitRows1 * S)
-      go(integral_constant<int, 1>{});
-    else if constexpr (M == 2)
-      go(integral_constant<int, 2>{});
+    if (rows <= kSplitRows1 * S || tiles(32) <= (M == 2 ? want : 2 * want)) {
+      split(integral_constant<int, 1>{});
+      return;
+    }
+    if constexpr (M == 2) {
+      if (rows <= kSplitRows2 * S || tiles(64) <= want) {
+        split(integral_constant<int, 2>{});
+        return;
+      }
+    }
+    mxfp4_tile_kernel<OP, GATHER, CT><<<tile_blocks(kTileRows), 256, 0, stream>>>(
+        a16, offsets, sorted_pairs, topk, S, max_rows, w, w_scale, N, Kd, ct);
     return;
   }
   const int lines = max_rows < S ? max_rows : S;  // slots that can have rows
@@ -1014,7 +1027,6 @@ void launch_product(const void* a, const int32_t* offsets, const int32_t* sorted
   // a wave's part is one step, and many light blocks beat few that walk two
   // steps (S = 64, N = 4096, Kd = 1024: 32 against 36 us).
   int split = Kd <= 512 || Kd > 1024 ? 1 : 2;
-  const long long want = device_cu_count();
   while (split < kStreamWaves && split * 512 < Kd &&
          (long long)ceil_div(N, 16 * kStreamWaves / split) * lines < want)
     split *= 2;

@@ -136,6 +136,13 @@ def test_products_every_split(rows, H, I):
     _products_check(ROWS[rows], H, I)
 
 
+@pytest.mark.parametrize("rows", [[160, 161, 320, 321, 0, 130, 481, 1727], [33, 2900, 0, 400]])
+@pytest.mark.parametrize("H,I", [(1120, 672), (2176, 640), (32, 2720)])
+def test_products_in_large_tiles(rows, H, I):
+    """As many rows and columns as fill the chip with the largest tiles, over whole and broken steps."""
+    _products_check(rows, H, I)
+
+
 @pytest.mark.parametrize("sizes", SIZES, ids=str)
 @pytest.mark.parametrize("H,I", [(32, 32), (64, 96), (160, 32), (512, 224), (1024, 128), (2048, 64)])
 def test_products_against_oracle(sizes, H, I):
@@ -268,6 +275,7 @@ LAYERS = {
     "replicas": dict(T=33, H=128, I=128, E=8, K=4, seed=4, extra=3),
     "skewed": dict(T=200, H=256, I=64, E=10, K=2, seed=5, skew=3.0),
     "many_rows": dict(T=700, H=128, I=96, E=4, K=2, seed=6),
+    "large_tiles": dict(T=900, H=160, I=672, E=6, K=4, seed=17),
     "share": dict(T=64, H=192, I=64, E=32, K=8, seed=7, ep=2, extra=2),
     "wide_k": dict(T=9, H=64, I=32, E=64, K=32, seed=8),
     "one_expert": dict(T=40, H=1024, I=512, E=1, K=1, seed=9),
@@ -326,13 +334,13 @@ def test_layer_routing_on_input():
     assert (np.abs(got - want) <= tol + 2.0 ** -8 * (np.abs(want) + tol)).all()
 
 
-@pytest.mark.parametrize("T", [1, 5, 60, 300, 900])
-def test_layer_keeps_rows_apart(T):
+@pytest.mark.parametrize("T,I", [(1, 96), (5, 96), (60, 96), (300, 96), (900, 96), (950, 672)])
+def test_layer_keeps_rows_apart(T, I):
     """A token of NaN and one of infinities change no other token's bits, whichever kernels run; and an
     expert whose slot the table does not give takes no part."""
     dev = device()
-    announce(f"mxfp4 layer rows apart T={T}")
-    H, I, E, K = 192, 96, 8, 3
+    announce(f"mxfp4 layer rows apart T={T} I={I}")
+    H, E, K = 192, 8, 3
     L = _layer(T + 2, H, I, E, K, 31)
     a, b = T // 2, T + 1
     clean = _run(dev, L, T + 2, logits=L["logits"])
