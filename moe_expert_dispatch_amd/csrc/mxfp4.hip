@@ -443,17 +443,17 @@ __global__ __launch_bounds__(64 * kStreamWaves) void mxfp4_quick_kernel(
 // under one scale. LDS rows are 128 bytes, their 16-byte chunks XOR-swizzled
 // by (row / 2 mod 8): 16 lanes then read from all 64 banks.
 //
-// 64 slots of N = 1024 gate/up columns, Kd = 4096: 177 us at 128 rows a slot
-// (780 TFLOP/s), 190 at 160 (900), 328 at 320 (1050; a library product of
-// 8192^3 reaches 1240). Tiles up to 128 rows took 307 us at 256 rows a slot
-// and 393 at 260, where a third tile of 4 rows costs half of a whole one: now
-// 303 and 315. Their sums fill 160 registers of 256, so the codes of a tile
-// over 128 rows are fetched one unit ahead instead of two (7 registers of the
-// addresses still wait in scratch). The matrix cores are busy 38% of the time
-// at two waves a SIMD; LDS and the conversions take a quarter each. Stages of
-// 128 k's (half the barriers, twice the distance of the fetches) were no
-// faster, nor were 8 waves that share the tile by rows and convert every
-// weight twice (533 TFLOP/s at 128 rows).
+// 64 slots of N = 1024 gate/up columns, Kd = 4096: 165 us at 128 rows a slot
+// (835 TFLOP/s), 188 at 160 (910), 319 at 320 (1080; a library product of
+// 8192^3 reaches 1240). Tiles up to 128 rows need a third one, of 4 rows, at
+// 260 rows a slot, at half the cost of a whole one: 393 us, with these 315.
+// Their sums fill 160 registers of 256, so the codes of a tile over 128 rows
+// are fetched one unit ahead instead of two. LDS reads run two ahead of their
+// matrix instructions (left to the compiler's order and with loads in
+// branches: 171 us at 128 rows, 328 at 320; three or four ahead: no
+// difference). Stages of 128 k's (half the barriers, twice the distance of the
+// fetches) were no faster, nor were 8 waves that share the tile by rows and
+// convert every weight twice (533 TFLOP/s at 128 rows).
 constexpr int kTileRows = 160;
 constexpr int kTileWeights = 256;
 constexpr int kStage = 64;
@@ -522,7 +522,7 @@ __device__ __forceinline__ void tile_product(uint4 (*stage)[kTileRows * 8],
   // a sixteenth of a code's offset is that of its scale
   const uint32_t wp[2] = {(uint32_t)row0 * (uint32_t)(Kd / 2), (uint32_t)row1 * (uint32_t)(Kd / 2)};
 
-  constexpr int AHEAD = 2;
+  constexpr int AHEAD = 2;  // LDS reads in flight before the first product
   floatx16 acc[2][NT];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
