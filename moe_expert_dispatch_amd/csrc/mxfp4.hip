@@ -962,6 +962,8 @@ __global__ __launch_bounds__(512) void mxfp4_pair_down_kernel(
 // (16 rows at a time), 88 and 45 split, but a slot past 16 streams its codes
 // twice (12 rows a slot on the average already have one in six past it); at 31
 // 88 and 46 split, but past 32 twice; at 64 113 split by 64 rows, 137 in tiles.
+// 64 rows pay where the contraction is long: at 48 rows a slot Kd = 4096 99
+// and 118 us, 2560 67 and 69, 1280 41 and 33, 640 32 and 20.
 // A few large slots leave the chip empty with tiles of 160 rows, so there the
 // smaller ones are taken while all of them run at once: 8 slots of 100 rows,
 // Kd = 4096 / N = 1024: 38 us by 32 rows, 41 by 64, 71 in tiles; of 160 rows 59, 43
@@ -1002,7 +1004,7 @@ void launch_product(const void* a, const int32_t* offsets, const int32_t* sorted
       return;
     }
     if constexpr (M == 2) {
-      if (rows <= kSplitRows2 * S || tiles(64) <= want) {
+      if ((rows <= kSplitRows2 * S && Kd > 2560) || tiles(64) <= want) {
         split(integral_constant<int, 2>{});
         return;
       }

@@ -137,9 +137,10 @@ def test_products_every_split(rows, H, I):
 
 
 @pytest.mark.parametrize("rows", [[160, 161, 320, 321, 0, 130, 481, 1727], [33, 2900, 0, 400]])
-@pytest.mark.parametrize("H,I", [(1120, 672), (2176, 640), (32, 2720)])
+@pytest.mark.parametrize("H,I", [(1120, 672), (2176, 640), (32, 2720), (1120, 320), (2176, 320)])
 def test_products_in_large_tiles(rows, H, I):
-    """As many rows and columns as fill the chip with the largest tiles, over whole and broken steps."""
+    """As many rows and columns as fill the chip with the largest tiles, or (320 columns) the middle ones, over
+    whole and broken steps."""
     _products_check(rows, H, I)
 
 
