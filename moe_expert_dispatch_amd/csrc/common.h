@@ -419,6 +419,9 @@ moe_status_t launch_gemm_mxfp4(moe_gemm_op_t op, const void* a, const int32_t* s
                                const uint8_t* w, const uint8_t* w_scale, int H, int I, void* c,
                                bool c_f32, hipStream_t stream);
 
+// Gate/up columns of a block where a layer goes pair by pair.
+constexpr int mxfp4_pair_columns(int H) { return H > 2048 ? 16 : 32; }
+
 // The layer of a few tokens, pair by pair (no permutation): the pairs' slots
 // (routed here, or from the slot map), act [T * topk, I] = the SwiGLU rows,
 // then out = the weighted sum of the down products, with shared and

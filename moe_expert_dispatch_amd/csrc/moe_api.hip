@@ -121,8 +121,24 @@ moe_status_t launch_gemm(moe_gemm_op_t op, moe_dtype_t dt, const void* a, const 
              : launch_gemm_f32(op, a, offsets, S, max_rows, w, H, I, c, stream);
 }
 
-// Tokens up to which an MXFP4 layer takes its pairs one by one.
+// An MXFP4 layer takes its pairs one by one, each reading its slot's weights
+// itself, for up to two tokens, whose pairs share no slot or few, and where so
+// few and small pairs leave less work than the two launches cost that this
+// saves: 64 pairs, 16 M weights of one matrix over all pairs (26 MB of codes and
+// scales), and 768 gate/up blocks (one and a half rounds; each routes its
+// token). 16 tokens, top-5 of 72 experts of 416 x 160 24 us a call with a permutation
+// and 19 without, 10 tokens, top-8, 1056 x 160 24 and 18; past the bounds 57 pairs
+// of 800 x 448 24 and 26, 44 of 256 x 1472 24 and 32.
 constexpr int kPairTokens = 2;
+constexpr int kPairCount = 64;
+constexpr int kPairBlocks = 768;
+constexpr long long kPairWeights = 16LL << 20;
+
+bool take_pairs(int T, int K, int H, int I) {
+  const long long pairs = (long long)T * K;
+  return T <= kPairTokens || (pairs <= kPairCount && pairs * H * I <= kPairWeights &&
+                              pairs * ceil_div(I, mxfp4_pair_columns(H)) <= kPairBlocks);
+}
 
 // Workspace of moe_forward, carved in this order (each 256-byte aligned).
 struct ForwardLayout {
@@ -433,7 +449,7 @@ moe_status_t moe_forward(const moe_config_t* cfg, const moe_forward_args_t* args
   const bool on_input = cfg->routing_on_input != 0;
   // MXFP4, few tokens: every pair by itself, without a permutation; a few
   // more: routing, slot map and permutation in one launch or two
-  const bool pairs = mx && !on_input && T > 0 && T <= kPairTokens;
+  const bool pairs = mx && !on_input && T > 0 && take_pairs(T, K, H, I);
   const bool plan = mx && !on_input && !pairs && T > 0 && T * K <= kPlanPairs;
   const int share_rows = (T * K + cfg->ep_size - 1) / cfg->ep_size;  // rows to expect here
   // the pairs' gate/up blocks route for themselves where lane groups do it

@@ -1174,12 +1174,14 @@ moe_status_t launch_mxfp4_pairs(const void* x, const PairRouting& routing, int T
   uint16_t* act16 = static_cast<uint16_t*>(act);
   auto gate_up = [&](auto wk, auto pipe) {
     constexpr int WK = decltype(wk)::value, RB = 8;
+    static_assert(mxfp4_pair_columns(WK == 8 ? 4096 : 2048) == 16 * kStreamWaves / WK,
+                  "columns of a block");
     constexpr int RUN = decltype(pipe)::value ? 2 : 4;
     const size_t rows_lds = (size_t)stream_row_vecs(stream_window(H, RB, WK)) * 16;  // one row
     const size_t red_lds = WK > 1 ? (size_t)kStreamWaves * 2 * kWave * 16 : 0;
     mxfp4_stream_kernel<MOE_GEMM_GATE_UP_SWIGLU, true, uint16_t, WK, RB, RUN,
                         decltype(pipe)::value, true>
-        <<<dim3(ceil_div(I, 16 * kStreamWaves / WK), P), 64 * kStreamWaves,
+        <<<dim3(ceil_div(I, mxfp4_pair_columns(H)), P), 64 * kStreamWaves,
            rows_lds > red_lds ? rows_lds : red_lds, stream>>>(
             static_cast<const uint16_t*>(x), nullptr, nullptr, topk, S, P, 0, w_gate_up,
             gate_up_scale, I, H, act16, routing);
