@@ -361,9 +361,10 @@ moe_status_t moe_grouped_gemm_mxfp4(moe_gemm_op_t op, const void* a, const int32
  * residual_out may be x or residual itself, and y may be x; no other overlap.
  * q's consumer is moe_forward with x_codes and a1_scale = q_scale, or
  * moe_grouped_gemm_fp8. H % 8 == 0, H <= 32768; eps finite and >= 0; q_scale
- * finite and > 0 where q is given; 16-byte aligned pointers. h must be finite
- * and the sum of its squares below 2^128; a row with others has unspecified
- * outputs (a NaN stays NaN in y).
+ * finite and > 0 where q is given; 16-byte aligned pointers. The sum of
+ * squares is f32, f64 where they would leave f32's range. h must be finite; a
+ * row with others has unspecified outputs (a NaN stays NaN in y), and so has a
+ * row of zeros with eps = 0.
  */
 moe_status_t moe_rms_norm(const void* x, const void* residual, const void* gamma, moe_dtype_t dt,
                           int T, int H, float eps, void* residual_out, void* y, uint8_t* q,

@@ -9,7 +9,7 @@
 // registers from the load to the stores, so the row is read once and both
 // outputs come from the unrounded v. The sum of squares is f32: per thread,
 // then per wave, then over the waves in order, so it does not depend on
-// scheduling.
+// scheduling. A row whose squares leave f32's range is summed again in f64.
 //
 // Bound by the bytes: 8192 rows of 5120 bf16 with residual and codes 71 us,
 // 5.3 TB/s; 16384 of 4096 103 us, 5.9 TB/s. One vector a thread (VPT = 1) is
@@ -20,6 +20,40 @@
 
 namespace moe {
 namespace {
+
+// Below this mean (eps included) squares may have lost bits that count to
+// f32's least number: here the halves of 2^-149 lost are 2^-70 of it at most.
+constexpr float kLeastMean = 0x1p-80f;
+
+// h / sqrt(mean(h^2) + eps) in place, for a block whose squares leave f32's
+// range: the sum and the quotient in f64, where every square of an f32 number
+// is exact.
+template <int VPT>
+__device__ __forceinline__ void normalize_wide(float (&h)[VPT][8], int nvec, int H, float eps) {
+  __shared__ double part[16];
+  double ss = 0.0;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    if ((int)(threadIdx.x + j * blockDim.x) < nvec) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss = fma((double)h[j][i], (double)h[j][i], ss);
+    }
+  }
+#pragma unroll
+  for (int o = kWave / 2; o > 0; o /= 2) ss += __shfl_xor(ss, o, kWave);
+  if (lane_id() == 0) part[threadIdx.x / kWave] = ss;
+  __syncthreads();
+  double total = 0.0;
+  for (int w = 0; w < (int)(blockDim.x / kWave); ++w) total += part[w];
+  const double r = 1.0 / sqrt(total / H + (double)eps);
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    if ((int)(threadIdx.x + j * blockDim.x) < nvec) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[j][i] = (float)((double)h[j][i] * r);
+    }
+  }
+}
 
 template <typename XT, int VPT>
 __global__ __launch_bounds__(1024) void rms_norm_kernel(
@@ -50,12 +84,22 @@ __global__ __launch_bounds__(1024) void rms_norm_kernel(
   __syncthreads();
   float total = 0.f;
   for (int w = 0; w < (int)(blockDim.x / kWave); ++w) total += part[w];
-  const float r = 1.0f / sqrtf(total / (float)H + eps);
+  const float mean = total / (float)H + eps;
+  float r = 1.0f / sqrtf(mean);
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int v = threadIdx.x + j * blockDim.x;
+    if (v < nvec && residual_out != nullptr) store8(residual_out + row + v * 8, h[j]);
+  }
+  // the same for the whole block; false for a NaN too
+  if (!(mean >= kLeastMean && total < INFINITY)) {
+    normalize_wide<VPT>(h, nvec, H, eps);
+    r = 1.0f;
+  }
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     const int v = threadIdx.x + j * blockDim.x;
     if (v < nvec) {
-      if (residual_out != nullptr) store8(residual_out + row + v * 8, h[j]);
       float g[8];
       load8(gamma + v * 8, g);
 #pragma unroll

@@ -151,3 +151,23 @@ def test_norm_feeds_the_fp8_layer():
     assert torch.equal(got, want) and got.abs().sum() > 0
     with pytest.raises(TypeError):
         moe.forward(moe.ForwardConfig(**cfg, x_codes=True), y, wgu, wd, **kw)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("eps", [0.0, 1e-42, 1e-30])
+def test_norm_of_rows_whose_squares_leave_f32(dt, eps):
+    """Rows whose squares are below or above f32's range, against the formula; the tolerance is that of every
+    other row, since the sum is kept in 64 bits there (and h * h is exact in them)."""
+    dev = device()
+    announce(f"rms_norm squares out of range {dt} eps={eps}")
+    g = torch.Generator().manual_seed(3)
+    for H in (8, 264, 8200, 32768):
+        sizes = torch.tensor([1e-19, 1e-21, 1e-23, 1e-25, 1e-30, 1e-37, 1e-39, 1e19, 1e25, 1e37, 1.0])
+        x = torch.randn(len(sizes), H, generator=g).clamp(-8, 8) * sizes[:, None]
+        x[3, 5] = 1e-12                 # one channel carries the norm
+        x[8, 2:] = 1e-25                # squares that overflow beside squares that underflow
+        r = (0.5 * x).to(dt)
+        x, gamma = x.to(dt), (1 + 0.2 * torch.randn(H, generator=g)).to(dt)
+        for res in (None, r):
+            y, ro, q = moe.rms_norm(x.to(dev), gamma.to(dev), eps, None if res is None else res.to(dev), 1 / 56)
+            _check(y, ro, q, x, res, gamma, float(np.float32(eps)), 1 / 56, f"H={H} res={res is not None}")
