@@ -8,6 +8,7 @@
 
 #include <type_traits>
 
+#include "grid.h"
 #include "moe.h"
 
 namespace moe {
@@ -153,6 +154,13 @@ __device__ __forceinline__ void wave_lds_fence() {
 
 // ---------------------------------------------------------------- misc
 __host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// This block's number in a grid of fold_grid().
+__device__ __forceinline__ uint32_t folded_block() { return blockIdx.y * gridDim.x + blockIdx.x; }
+inline dim3 folded(int64_t blocks, int threads, int unit = 1) {
+  const Grid g = fold_grid(blocks, threads, unit);
+  return dim3(g.x, g.y);
+}
 
 // Expert-parallel mask / remap and expert -> slot lookup of one pair p =
 // t * K + k with expert e and routing weight wv (vLLM ep_fused_moe_patch.py,

@@ -57,11 +57,12 @@ __device__ __forceinline__ void normalize_wide(float (&h)[VPT][8], int nvec, int
 
 template <typename XT, int VPT>
 __global__ __launch_bounds__(1024) void rms_norm_kernel(
-    const XT* x, const XT* residual, const XT* __restrict__ gamma, int H, float eps,
+    const XT* x, const XT* residual, const XT* __restrict__ gamma, int T, int H, float eps,
     XT* residual_out, XT* y, uint8_t* __restrict__ q, float inv) {
   __shared__ float part[16];
+  if (folded_block() >= (uint32_t)T) return;
   const int nvec = H / 8;
-  const size_t row = (size_t)blockIdx.x * H;
+  const size_t row = (size_t)folded_block() * H;
   float h[VPT][8];
   float ss = 0.f;
 #pragma unroll
@@ -119,9 +120,9 @@ template <typename XT, int VPT>
 void launch_v(const void* x, const void* residual, const void* gamma, int T, int H, float eps,
               void* residual_out, void* y, uint8_t* q, float inv, hipStream_t stream) {
   const int threads = ceil_div(ceil_div(H / 8, VPT), kWave) * kWave;
-  rms_norm_kernel<XT, VPT><<<T, threads, 0, stream>>>(
+  rms_norm_kernel<XT, VPT><<<folded(T, threads), threads, 0, stream>>>(
       static_cast<const XT*>(x), static_cast<const XT*>(residual),
-      static_cast<const XT*>(gamma), H, eps, static_cast<XT*>(residual_out),
+      static_cast<const XT*>(gamma), T, H, eps, static_cast<XT*>(residual_out),
       static_cast<XT*>(y), q, inv);
 }
 

@@ -171,3 +171,18 @@ def test_norm_of_rows_whose_squares_leave_f32(dt, eps):
         for res in (None, r):
             y, ro, q = moe.rms_norm(x.to(dev), gamma.to(dev), eps, None if res is None else res.to(dev), 1 / 56)
             _check(y, ro, q, x, res, gamma, float(np.float32(eps)), 1 / 56, f"H={H} res={res is not None}")
+
+
+def test_norm_of_more_rows_than_a_grid_line_has_threads_for():
+    """2^26 + 3 rows: with 64 threads a row past the 2^32 threads of one grid dimension."""
+    dev = device()
+    announce("rms_norm 2^26 + 3 rows")
+    T, H = 2 ** 26 + 3, 8
+    x = torch.arange(T * H, device=dev, dtype=torch.int32).remainder_(251).sub_(125).to(torch.bfloat16).view(T, H)
+    gamma = torch.ones(H, dtype=torch.bfloat16, device=dev)
+    y, _, q = moe.rms_norm(x, gamma, 1e-6, q_scale=1 / 56)
+    # the inputs repeat after 251 rows, and so do the outputs, which a small call gives
+    small, _, qs = moe.rms_norm(x[:251].clone(), gamma, 1e-6, q_scale=1 / 56)
+    whole = T // 251
+    assert (y[:whole * 251].view(whole, 251, H) == small).all() and (q[:whole * 251].view(whole, 251, H) == qs).all()
+    assert torch.equal(y[whole * 251:], small[:T - whole * 251]) and torch.equal(q[whole * 251:], qs[:T - whole * 251])
