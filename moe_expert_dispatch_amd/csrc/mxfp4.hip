@@ -43,7 +43,7 @@ template <typename XT>
 __global__ __launch_bounds__(256) void quantize_mxfp4_kernel(const XT* __restrict__ w, int64_t n8,
                                                              uint32_t* __restrict__ codes,
                                                              uint8_t* __restrict__ scale) {
-  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  const int64_t i = (int64_t)folded_block() * blockDim.x + threadIdx.x;
   if (i >= n8) return;  // n8 is a multiple of 4: whole quads leave
   float v[8];
   load8(w + i * 8, v);
@@ -68,7 +68,7 @@ template <typename OT>
 __global__ __launch_bounds__(256) void dequantize_mxfp4_kernel(const uint32_t* __restrict__ codes,
                                                                const uint8_t* __restrict__ scale,
                                                                int64_t n8, OT* __restrict__ w) {
-  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  const int64_t i = (int64_t)folded_block() * blockDim.x + threadIdx.x;
   if (i >= n8) return;
   const uint4 p = cvt8(codes[i], e8m0(scale[i >> 2]));
   if constexpr (sizeof(OT) == 2) {
@@ -1115,7 +1115,7 @@ moe_status_t launch_quantize_mxfp4(const void* w, bool bf16, int64_t n, uint8_t*
                                    uint8_t* scale, hipStream_t stream) {
   if (n == 0) return MOE_OK;
   const int64_t n8 = n / 8;
-  const unsigned blocks = (unsigned)((n8 + 255) / 256);
+  const dim3 blocks = folded((n8 + 255) / 256, 256);
   uint32_t* c = reinterpret_cast<uint32_t*>(codes);
   if (bf16)
     quantize_mxfp4_kernel<uint16_t>
@@ -1130,7 +1130,7 @@ moe_status_t launch_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scale,
                                      void* w, bool bf16, hipStream_t stream) {
   if (n == 0) return MOE_OK;
   const int64_t n8 = n / 8;
-  const unsigned blocks = (unsigned)((n8 + 255) / 256);
+  const dim3 blocks = folded((n8 + 255) / 256, 256);
   const uint32_t* c = reinterpret_cast<const uint32_t*>(codes);
   if (bf16)
     dequantize_mxfp4_kernel<uint16_t>

@@ -93,6 +93,40 @@ def test_quantize_empty_and_refusals():
                              torch.zeros(4, 1, device=dev, dtype=torch.uint8), torch.float16)
 
 
+def test_quantize_more_groups_than_a_grid_line_has_threads_for():
+    """2^35 + 96 weights, four threads a group: past the 2^32 threads of one grid dimension. The weights repeat
+    every 4128 groups, and so have to the codes, the scales and the weights read back."""
+    dev = device()
+    announce("quantize mxfp4 2^35 + 96")
+    n, period = 2 ** 35 + 96, 4128 * 32
+    if torch.cuda.mem_get_info()[0] < 100 * 2 ** 30:
+        pytest.skip("needs 100 GiB of device memory")
+    g = torch.Generator(device=dev).manual_seed(4)
+    part = torch.randn(period, generator=g, device=dev) * torch.randn(period // 32, generator=g, device=dev).exp(
+    ).repeat_interleave(32)
+    part = part.bfloat16()
+    whole = n // period
+    w = torch.empty(n, dtype=torch.bfloat16, device=dev)
+    w[:whole * period].view(whole, period).copy_(part.expand(whole, period))
+    w[whole * period:] = part[:n - whole * period]
+    codes, scale = moe.quantize_mxfp4(w)
+    pc, ps = moe.quantize_mxfp4(part)
+    pw = moe.dequantize_mxfp4(pc, ps)
+
+    def repeats(t, one):
+        m = one.numel()
+        lines, left = t[:whole * m].view(whole, m), t[whole * m:]
+        step = 1 << 14                       # a few GB of truth values at a time
+        return all(bool((lines[i:i + step] == one).all()) for i in range(0, whole, step)) and torch.equal(
+            left, one[:left.numel()])
+    assert repeats(codes, pc) and repeats(scale, ps)
+    w.zero_()
+    moe.dequantize_mxfp4(codes, scale, out=w)
+    assert repeats(w, pw)
+    del w, codes, scale
+    torch.cuda.empty_cache()
+
+
 # ------------------------------------------------------------------ products
 SIZES = [[1], [0, 1, 0], [3, 0, 16, 1], [17, 0, 5, 33], [70, 1, 0, 0, 2], [300, 129], [0, 0],
          [40, 64, 65, 8, 9, 4, 5, 2],
