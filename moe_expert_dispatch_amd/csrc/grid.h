@@ -9,10 +9,10 @@ struct Grid {
   unsigned x, y;
 };
 
-// A grid dimension holds fewer than 2^32 threads. Blocks past half of that go
-// on in further lines of nearly equal length, a multiple of `unit`; block
-// folded_block() of them may lie behind the last of `blocks` (at most
-// y * unit - 1 do, and none where unit is 1 and there is one line).
+// A grid dimension holds fewer than 2^32 threads; a launch of more runs their
+// number modulo 2^32, without an error. Blocks past half of that go on in
+// further lines of nearly equal length, a multiple of `unit`, and some (fewer
+// than y * unit) may lie behind the last of `blocks`, but none with one line.
 inline Grid fold_grid(int64_t blocks, int threads, int unit = 1) {
   const int64_t most = (INT64_C(1) << 31) / threads / unit * unit;
   const int64_t y = (blocks + most - 1) / most;

@@ -451,7 +451,8 @@ moe_status_t moe_forward(const moe_config_t* cfg, const moe_forward_args_t* args
   // more: routing, slot map and permutation in one launch or two
   const bool pairs = mx && !on_input && T > 0 && take_pairs(T, K, H, I);
   const bool plan = mx && !on_input && !pairs && T > 0 && T * K <= kPlanPairs;
-  const int share_rows = (T * K + cfg->ep_size - 1) / cfg->ep_size;  // rows to expect here
+  const int share_rows =  // rows to expect here
+      (int)(((long long)T * K + cfg->ep_size - 1) / cfg->ep_size);
   // the pairs' gate/up blocks route for themselves where lane groups do it
   const PairRouting pair_routing{
       args->logits, cfg->E_global, cfg->renormalize ? 1 : 0,

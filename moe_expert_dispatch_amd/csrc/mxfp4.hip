@@ -639,7 +639,8 @@ __device__ __forceinline__ void tile_product(uint4 (*stage)[kTileRows * 8],
   }
 }
 
-// Blocks b, b + 8, ... run on one XCD (workgroups are dealt round-robin):
+// Blocks b, b + 8, ... run on one XCD (workgroups are dealt round-robin, and the
+// lines of a folded grid are whole eights):
 // it takes whole groups of two row tiles and all their columns, so the two
 // tiles of a slot share its weights in that XCD's L2.
 template <int OP, bool GATHER, typename CT>
@@ -652,8 +653,8 @@ __global__ __launch_bounds__(256, 2) void mxfp4_tile_kernel(
   __shared__ uint4 stage[2][kTileRows * 8];
   const int ncol = ceil_div(N, kTileWeights / M);
   const int group = 2 * ncol;
-  const int in = (int)(blockIdx.x >> 3);
-  const int tile = ((in / group) * 8 + (int)(blockIdx.x & 7)) * 2 + (in % group) % 2;
+  const int in = (int)(folded_block() >> 3);
+  const int tile = ((in / group) * 8 + (int)(folded_block() & 7)) * 2 + (in % group) % 2;
   const int n0 = (in % group) / 2 * (kTileWeights / M);
   int s = 0, r0 = 0, r1 = 0;
   if (!find_tile<kTileRows>(offsets, S, max_rows, tile, &s, &r0, &r1)) return;
@@ -708,8 +709,8 @@ __global__ __launch_bounds__(512, U == 2 ? 2 : 1) void mxfp4_split_kernel(
   static_assert(sizeof(stage) >= 2u * NT * 16 * 4 * 256, "the second half's sums fit");
   const int ncol = ceil_div(N, kTileWeights / M);
   const int group = 2 * ncol;
-  const int bi = (int)(blockIdx.x >> 3);
-  const int tile = ((bi / group) * 8 + (int)(blockIdx.x & 7)) * 2 + (bi % group) % 2;
+  const int bi = (int)(folded_block() >> 3);
+  const int tile = ((bi / group) * 8 + (int)(folded_block() & 7)) * 2 + (bi % group) % 2;
   const int n0 = (bi % group) / 2 * (kTileWeights / M);
   int s = 0, r0 = 0, r1 = 0;
   if (!find_tile<TR>(offsets, S, max_rows, tile, &s, &r0, &r1)) return;
@@ -981,9 +982,9 @@ void launch_product(const void* a, const int32_t* offsets, const int32_t* sorted
   constexpr int M = OP == MOE_GEMM_GATE_UP_SWIGLU ? 2 : 1;
   // Blocks for all tiles of `tr` rows, of which there are at most this many
   // whatever the slots' counts: groups of two row tiles, eight XCDs.
-  auto tile_blocks = [&](int tr) {
+  auto tile_grid = [&](int tr, int threads) {
     const int64_t tiles = (int64_t)max_rows / tr + S;
-    return (unsigned)((tiles + 15) / 16 * 8 * 2 * ceil_div(N, kTileWeights / M));
+    return folded((tiles + 15) / 16 * 8 * 2 * ceil_div(N, kTileWeights / M), threads, 8);
   };
   const uint16_t* a16 = static_cast<const uint16_t*>(a);
   CT* ct = static_cast<CT*>(c);
@@ -996,7 +997,7 @@ void launch_product(const void* a, const int32_t* offsets, const int32_t* sorted
     auto split = [&](auto nt) {
       constexpr int NT = decltype(nt)::value;
       mxfp4_split_kernel<OP, GATHER, CT, NT, NT == 1 ? 2 : 4>
-          <<<tile_blocks(32 * NT), 512, 0, stream>>>(a16, offsets, sorted_pairs, topk, S,
+          <<<tile_grid(32 * NT, 512), 512, 0, stream>>>(a16, offsets, sorted_pairs, topk, S,
                                                      max_rows, w, w_scale, N, Kd, ct);
     };
     if (rows <= kSplitRows1 * S || tiles(32) <= (M == 2 ? want : 2 * want)) {
@@ -1009,7 +1010,7 @@ void launch_product(const void* a, const int32_t* offsets, const int32_t* sorted
         return;
       }
     }
-    mxfp4_tile_kernel<OP, GATHER, CT><<<tile_blocks(kTileRows), 256, 0, stream>>>(
+    mxfp4_tile_kernel<OP, GATHER, CT><<<tile_grid(kTileRows, 256), 256, 0, stream>>>(
         a16, offsets, sorted_pairs, topk, S, max_rows, w, w_scale, N, Kd, ct);
     return;
   }

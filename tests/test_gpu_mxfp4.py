@@ -547,3 +547,35 @@ def test_layer_refusals():
         moe.forward(cfg, a[0], a[2], a[1], **ok)
     with pytest.raises(ValueError):
         moe.forward(cfg, a[0], a[1], a[2], **{**ok, "w_gate_up_scale": a[3][:, :, :1].contiguous()})
+
+
+def test_layer_of_one_rank_of_very_many_pairs():
+    """One of 1024 ranks, all 1024 slots its one expert's, 25 M pairs: the grid for the tiles that they could fill
+    passes the 2^32 threads of one dimension. Half of them are here, so later tiles have rows."""
+    dev = device()
+    announce("mxfp4 layer 25 M pairs, one of 1024 ranks")
+    if torch.cuda.mem_get_info()[0] < 100 * 2 ** 30:
+        pytest.skip("needs 100 GiB of device memory")
+    T, K, H, I, S = 24 * 1024 * 32, 32, 32, 1408, 1024
+    gu, gs = _weights((1, 2 * I, H), 1, H)
+    wd, ds = _weights((1, H, I), 2, I)
+    x = _rows(T, H, 3)
+    ids = torch.full((T, K), 5, dtype=torch.int32)
+    ids[:, ::2] = 0
+    w = torch.rand(T, K, generator=torch.Generator().manual_seed(4))
+    cfg = moe.ForwardConfig(T=T, H=H, I=I, E_global=1024, K=K, renormalize=True, S=S, dtype=moe.MXFP4, ep_size=1024)
+    slots = lambda t: t.to(dev).expand(S, -1, -1).contiguous()  # noqa: E731
+    out = moe.forward(cfg, x.to(dev), slots(gu), slots(wd), topk_ids=ids.to(dev), topk_w=w.to(dev),
+                      rep_off=torch.tensor([0, S], dtype=torch.int32, device=dev),
+                      rep_slots=torch.arange(S, dtype=torch.int32, device=dev),
+                      w_gate_up_scale=slots(gs), w_down_scale=slots(ds))
+    some = torch.arange(0, T, 8191)
+    some[-1] = T - 1
+    n = some.numel()
+    L = dict(gu=gu, gs=gs, wd=wd, ds=ds, x=x[some], El=1, cfg=dict(H=H, I=I))
+    # the same row K / 2 times: once, with the weights' sum (K / 2 - 1 more additions in f32)
+    want, tol = _reference(L, n, np.zeros((n, 1), int), np64(w[some])[:, ::2].sum(1, keepdims=True))
+    got = np64(out[some.to(dev)])
+    assert (np.abs(got - want) <= tol * (1 + K * U) + 2.0 ** -8 * (np.abs(want) + tol) + 1e-38).all()
+    del out
+    torch.cuda.empty_cache()
