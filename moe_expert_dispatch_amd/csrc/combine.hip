@@ -71,12 +71,13 @@ __device__ __forceinline__ void load8(__amdgpu_buffer_rsrc_t r, uint32_t off, co
 template <typename YT, typename OT, int KMAX, int kVec>
 __global__ __launch_bounds__(256) void combine_kernel(const YT* __restrict__ y,
                                                       const int32_t* __restrict__ pair_row,
-                                                      const float* __restrict__ w_masked, int K,
-                                                      int H, OT* __restrict__ out,
+                                                      const float* __restrict__ w_masked, int T,
+                                                      int K, int H, OT* __restrict__ out,
                                                       int accumulate,
                                                       const void* __restrict__ shared,
                                                       int shared_bf16) {
-  const int t = blockIdx.x;
+  const uint32_t t = folded_block();
+  if (t >= (uint32_t)T) return;
   __shared__ int32_t rows[MOE_MAX_TOPK];
   __shared__ float wts[MOE_MAX_TOPK];
   if (threadIdx.x < K) {
@@ -151,8 +152,8 @@ void launch_kv(const void* y, const int32_t* pair_row, const float* w_masked, in
   // at most 256 (wider rows loop), so narrow rows leave no thread idle and
   // more tokens fit on a CU.
   const int threads = std::min(256, std::max(kWave, ceil_div(H / 8, VEC * kWave) * kWave));
-  combine_kernel<YT, OT, KMAX, VEC><<<T, threads, 0, stream>>>(
-      static_cast<const YT*>(y), pair_row, w_masked, K, H, static_cast<OT*>(out), accumulate,
+  combine_kernel<YT, OT, KMAX, VEC><<<folded(T, threads), threads, 0, stream>>>(
+      static_cast<const YT*>(y), pair_row, w_masked, T, K, H, static_cast<OT*>(out), accumulate,
       shared, shared_bf16);
 }
 

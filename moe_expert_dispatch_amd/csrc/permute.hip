@@ -258,7 +258,8 @@ __global__ __launch_bounds__(256) void gather_kernel(const uint4* __restrict__ x
                                                      int nvec, int K,
                                                      const int32_t* __restrict__ pair_row,
                                                      uint4* __restrict__ x_perm) {
-  const int t = blockIdx.x;
+  const uint32_t t = folded_block();
+  if (t >= (uint32_t)T) return;
   __shared__ int32_t rows[MOE_MAX_TOPK];
   if (threadIdx.x < K) rows[threadIdx.x] = pair_row[(size_t)t * K + threadIdx.x];
   __syncthreads();
@@ -271,7 +272,8 @@ __global__ __launch_bounds__(256) void gather_scaled_kernel(const uint4* __restr
                                                             const int32_t* __restrict__ pair_row,
                                                             const float* __restrict__ pair_w,
                                                             uint4* __restrict__ x_perm) {
-  const int t = blockIdx.x;
+  const uint32_t t = folded_block();
+  if (t >= (uint32_t)T) return;
   __shared__ int32_t rows[MOE_MAX_TOPK];
   __shared__ float ws[MOE_MAX_TOPK];
   if (threadIdx.x < K) {
@@ -353,12 +355,13 @@ moe_status_t launch_permute(const void* x, int elem_bytes, int T, int H, int K,
     const uint4* x4 = static_cast<const uint4*>(x);
     uint4* xp4 = static_cast<uint4*>(x_perm);
     if (pair_w == nullptr)
-      gather_kernel<<<T, 256, 0, stream>>>(x4, T, nvec, K, pair_row, xp4);
+      gather_kernel<<<folded(T, 256), 256, 0, stream>>>(x4, T, nvec, K, pair_row, xp4);
     else if (elem_bytes == 2)
-      gather_scaled_kernel<uint16_t><<<T, 256, 0, stream>>>(x4, T, nvec, K, pair_row, pair_w,
-                                                            xp4);
+      gather_scaled_kernel<uint16_t><<<folded(T, 256), 256, 0, stream>>>(x4, T, nvec, K, pair_row,
+                                                                         pair_w, xp4);
     else
-      gather_scaled_kernel<float><<<T, 256, 0, stream>>>(x4, T, nvec, K, pair_row, pair_w, xp4);
+      gather_scaled_kernel<float><<<folded(T, 256), 256, 0, stream>>>(x4, T, nvec, K, pair_row,
+                                                                      pair_w, xp4);
   }
   return launch_status();
 }

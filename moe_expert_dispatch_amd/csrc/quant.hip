@@ -17,7 +17,7 @@ namespace {
 template <typename XT>
 __global__ __launch_bounds__(256) void quantize_kernel(const XT* __restrict__ x, int64_t n,
                                                        float inv, uint8_t* __restrict__ q) {
-  quantize16(x, n, inv, q, (int64_t)blockIdx.x * blockDim.x + threadIdx.x);
+  quantize16(x, n, inv, q, (int64_t)folded_block() * blockDim.x + threadIdx.x);
 }
 
 }  // namespace
@@ -27,7 +27,7 @@ moe_status_t launch_quantize_fp8(const void* x, bool x_bf16, int64_t n, float sc
   if (n == 0) return MOE_OK;
   const float inv = 1.0f / scale;
   const int64_t threads = (n + 15) / 16;
-  const unsigned blocks = (unsigned)((threads + 255) / 256);
+  const dim3 blocks = folded((threads + 255) / 256, 256);
   if (x_bf16)
     quantize_kernel<uint16_t>
         <<<blocks, 256, 0, stream>>>(static_cast<const uint16_t*>(x), n, inv, q);

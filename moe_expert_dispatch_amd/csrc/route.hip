@@ -38,8 +38,8 @@ __global__ __launch_bounds__(256) void route_lanes_kernel(const float* __restric
                                                           int32_t* __restrict__ ids,
                                                           float* __restrict__ w, MapOut mo) {
   const int q = threadIdx.x & (L - 1);
-  const int t = (int)((blockIdx.x * blockDim.x + threadIdx.x) / L);
-  const bool live = t < T;
+  const uint32_t t = folded_block() * (256 / L) + threadIdx.x / L;
+  const bool live = t < (uint32_t)T;
   int id;
   float p;
   route_token<L, EPL>(logits + (size_t)(live ? t : 0) * E, live, E, K, renorm, q, &id, &p);
@@ -148,8 +148,8 @@ __global__ __launch_bounds__(256) void route_kernel(const float* __restrict__ lo
                                                     int E, int K, int renorm, int G, int TG,
                                                     int32_t* __restrict__ ids,
                                                     float* __restrict__ w, MapOut mo) {
-  const int t = blockIdx.x * (blockDim.x / kWave) + threadIdx.x / kWave;
-  if (t >= T) return;  // wave-uniform
+  const uint32_t t = folded_block() * (256 / kWave) + threadIdx.x / kWave;
+  if (t >= (uint32_t)T) return;  // wave-uniform
   const int lane = lane_id();
   const float* row = logits + (size_t)t * E;
 
@@ -244,7 +244,7 @@ template <int L, bool MAP>
 void launch_lanes(const float* logits, int T, int E, int K, int renorm, int32_t* ids, float* w,
                   const MapOut& mo, hipStream_t stream) {
   const int epl = ceil_div(E, L);
-  const dim3 grid((unsigned)ceil_div(T, 256 / L));
+  const dim3 grid = folded((T - 1) / (256 / L) + 1, 256);
   if (epl <= 1)
     route_lanes_kernel<L, 1, MAP><<<grid, 256, 0, stream>>>(logits, T, E, K, renorm, ids, w, mo);
   else if (epl <= 2)
@@ -260,7 +260,7 @@ template <bool MAP>
 void launch_waves(const float* logits, int T, int E, int K, int renorm, int G, int TG,
                   int32_t* ids, float* w, const MapOut& mo, hipStream_t stream) {
   const dim3 block(256);
-  const dim3 grid(ceil_div(T, 256 / kWave));
+  const dim3 grid = folded((T - 1) / (256 / kWave) + 1, 256);
   const int epl = ceil_div(E, kWave);
   if (epl <= 1)
     route_kernel<1, MAP><<<grid, block, 0, stream>>>(logits, T, E, K, renorm, G, TG, ids, w, mo);

@@ -17,8 +17,8 @@ __global__ __launch_bounds__(256) void slot_map_kernel(
     int E_local, const int32_t* __restrict__ rep_off, const int32_t* __restrict__ rep_slots,
     int S, int32_t* __restrict__ slot, float* __restrict__ w_masked,
     uint8_t* __restrict__ mask) {
-  const int p = blockIdx.x * blockDim.x + threadIdx.x;
-  if (p >= P) return;
+  const uint32_t p = blockIdx.x * blockDim.x + threadIdx.x;
+  if (p >= (uint32_t)P) return;
   map_pair(p, p / K, ids[p], w[p], start, E_local, rep_off, rep_slots, S, slot, w_masked, mask);
 }
 
@@ -30,7 +30,7 @@ moe_status_t launch_slot_map(const int32_t* ids, const float* w, int T, int K, i
                              hipStream_t stream) {
   const int P = T * K;
   if (P == 0) return MOE_OK;
-  slot_map_kernel<<<ceil_div(P, 256), 256, 0, stream>>>(ids, w, P, K, start, E_local, rep_off,
+  slot_map_kernel<<<(P - 1) / 256 + 1, 256, 0, stream>>>(ids, w, P, K, start, E_local, rep_off,
                                                        rep_slots, S, slot, w_masked, mask);
   return launch_status();
 }
