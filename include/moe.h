@@ -573,7 +573,7 @@ moe_status_t moe_forward(const moe_config_t* cfg, const moe_forward_args_t* args
  * x, send_x: H * sizeof(dt) a multiple of 16 bytes, 16-byte aligned.
  * ws: at least moe_a2a_dispatch_workspace_size(T, ep_size, cap) bytes.
  * Limits: 1 <= ep_size <= MOE_MAX_A2A_RANKS, E_global % ep_size == 0,
- * 1 <= K <= MOE_MAX_TOPK.
+ * 1 <= K <= MOE_MAX_TOPK, T < 2^24 - 256.
  *
  * moe_a2a_combine gathers the ranks' partial outputs back into token order:
  *   out[t] = round(sum over r = 0..ep_size-1 ascending with

@@ -176,6 +176,9 @@ ForwardLayout forward_layout(const moe_config_t* c) {
   return L;
 }
 
+// A block of 256 threads a token and 256 more blocks, in one grid dimension (2^32 threads).
+constexpr int kMaxA2aTokens = (1 << 24) - 257;
+
 moe_status_t check_a2a_dispatch(const void* x, moe_dtype_t dt, int T, int H, int K,
                                 const int32_t* ids, const float* w, int E_global, int ep_size,
                                 int cap, const int32_t* offsets, const int32_t* token_pos,
@@ -184,7 +187,8 @@ moe_status_t check_a2a_dispatch(const void* x, moe_dtype_t dt, int T, int H, int
   if (T < 0 || K < 1 || E_global < 1 || ep_size < 1 || cap < T) return MOE_ERR_INVALID_ARG;
   if (E_global % ep_size != 0) return MOE_ERR_INVALID_ARG;
   if (!dtype_ok(dt)) return MOE_ERR_UNSUPPORTED;
-  if (ep_size > MOE_MAX_A2A_RANKS || K > MOE_MAX_TOPK || E_global > MOE_MAX_EXPERTS)
+  if (ep_size > MOE_MAX_A2A_RANKS || K > MOE_MAX_TOPK || E_global > MOE_MAX_EXPERTS ||
+      T > kMaxA2aTokens)
     return MOE_ERR_UNSUPPORTED;
   if (H < 1 || (H * dtype_bytes(dt)) % 16 != 0) return MOE_ERR_UNSUPPORTED;
   if (!pairs_fit(T, ep_size) || !pairs_fit(cap, ep_size) || !pairs_fit(cap * ep_size, K))
@@ -638,7 +642,7 @@ moe_status_t moe_route_backward(const float* logits, const int32_t* ids, const f
 }
 
 size_t moe_a2a_dispatch_workspace_size(int T, int ep_size, int cap) {
-  if (T < 0 || ep_size < 1 || ep_size > MOE_MAX_A2A_RANKS || cap < T ||
+  if (T < 0 || T > kMaxA2aTokens || ep_size < 1 || ep_size > MOE_MAX_A2A_RANKS || cap < T ||
       !pairs_fit(T, ep_size) || !pairs_fit(cap, ep_size))
     return 0;
   return a2a_layout(T, ep_size, cap).total;

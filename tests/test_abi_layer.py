@@ -138,3 +138,16 @@ def test_python_layer_refuses(so):
         moe.balance_loss(x.float(), torch.zeros(4, 2, dtype=torch.int32), 1.0)
     with pytest.raises(ValueError):
         moe.route_backward(x.float(), torch.zeros(4, 2, dtype=torch.int32), None, True)
+
+
+def test_a2a_dispatch_refuses_more_tokens_than_its_grid_holds(so):
+    """A block of 256 threads a token, and up to 256 more: 2^32 threads from 2^24 - 256 tokens on."""
+    most = (1 << 24) - 257
+    ws = so.moe_a2a_dispatch_workspace_size
+    assert ws(most, 1, most) > 0 and ws(most + 1, 1, most + 1) == 0
+
+    def call(T, n):
+        return so.moe_a2a_dispatch(fake, 1, T, 64, 1, fake, fake, 8, 1, T, fake, fake, fake, fake, fake, fake, fake,
+                                   ctypes.c_size_t(n), None)
+    assert call(most, 0) == WORKSPACE
+    assert call(most + 1, 0) == UNSUPPORTED and call(1 << 24, 1 << 40) == UNSUPPORTED
