@@ -461,8 +461,11 @@ void with_lanes(int E, int K, bool aligned, F&& f) {
   }
 }
 
+// Blocks of `per` tokens each; T is up to 2^31 - 1, where T + per - 1 would overflow.
+int token_blocks(int T, int per) { return T > 0 ? (T - 1) / per + 1 : 0; }
+
 int balance_blocks(int T, int E, int K) {
-  const int rounds = ceil_div(T, kLossThreads / lanes_for(E, K));
+  const int rounds = token_blocks(T, kLossThreads / lanes_for(E, K));
   return rounds <= kLossRounds ? 1 : std::min(kMaxBlocks, ceil_div(rounds, 2));
 }
 
@@ -513,7 +516,7 @@ moe_status_t launch_route_backward(const float* logits, const int32_t* ids, cons
   if (T == 0) return MOE_OK;
   with_lanes(E, K, aligned16(logits) && aligned16(dlogits), [&](auto l, auto epl, auto vec) {
     constexpr int L = decltype(l)::value;
-    const int blocks = std::min(ceil_div(T, kGradThreads / L), kGradBlocks);
+    const int blocks = std::min(token_blocks(T, kGradThreads / L), kGradBlocks);
     route_backward_kernel<L, decltype(epl)::value, decltype(vec)::value>
         <<<blocks, kGradThreads, 0, stream>>>(logits, ids, dw, token_mask, counts, dloss, T, E,
                                               K, renorm, coef, dlogits);

@@ -140,6 +140,13 @@ def test_python_layer_refuses(so):
         moe.route_backward(x.float(), torch.zeros(4, 2, dtype=torch.int32), None, True)
 
 
+def test_balance_loss_workspace_at_the_most_tokens(so):
+    """T * K < 2^31: the largest T takes the blocks, and with them the workspace, of every large T."""
+    ws = so.moe_balance_loss_workspace_size
+    for E, K in ((1, 1), (8, 1), (64, 1)):
+        assert ws(2 ** 31 - 1, E, K) == ws(2 ** 30, E, K) > ws(64, E, K)
+
+
 def test_a2a_dispatch_refuses_more_tokens_than_its_grid_holds(so):
     """A block of 256 threads a token, and up to 256 more: 2^32 threads from 2^24 - 256 tokens on."""
     most = (1 << 24) - 257

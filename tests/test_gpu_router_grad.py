@@ -285,3 +285,24 @@ def test_refusals():
         moe.route_backward(l, ids, None, True)
     with pytest.raises(RuntimeError):
         moe.balance_loss(l, ids, 1.0, ws=torch.empty(8, dtype=torch.uint8, device=dev))
+
+
+def test_most_tokens():
+    """2^31 - 1 tokens of one expert, the most that T * K < 2^31 allows: the loss, its counts and an exactly
+    zero gradient (a softmax of one is constant)."""
+    dev = device()
+    announce("router 2^31 - 1 tokens")
+    if torch.cuda.mem_get_info()[0] < 45 * 2 ** 30:
+        pytest.skip("needs 45 GiB of device memory")
+    T = 2 ** 31 - 1
+    l = torch.full((T, 1), 0.5, device=dev)
+    ids = torch.zeros(T, 1, dtype=torch.int32, device=dev)
+    d = torch.full((T, 1), 7.0, device=dev)
+    loss, counts, prob = moe.balance_loss(l, ids, 0.25)
+    assert counts.tolist() == [T, T] and float(prob) == 1.0 and float(loss) == 0.25
+    for renorm in (False, True):
+        d.fill_(7.0)
+        moe.route_backward(l, ids, l, renorm, counts=counts, coef=0.25, dlogits=d)
+        assert float(d.abs().max()) == 0.0
+    del l, ids, d
+    torch.cuda.empty_cache()
