@@ -481,7 +481,14 @@ typedef struct {
                            of moe_rms_norm) instead of bf16; 0 for every other dtype */
 } moe_config_t;
 
-/* Stage boundaries at which moe_forward records the caller's events. */
+/*
+ * Stage boundaries at which moe_forward records the caller's events: each
+ * behind the last launch of its stage. Stages that share a launch (MXFP4 with
+ * few tokens: route, slot map and permute, with up to two tokens or few narrow
+ * pairs in the gate/up product, the combine in the down product) have theirs
+ * together behind it, in this order, so the time of the whole launch stands at
+ * the first of them and none at the others.
+ */
 enum {
   MOE_EV_START = 0,     /* before routing */
   MOE_EV_ROUTED = 1,    /* after route and slot map */

@@ -431,14 +431,17 @@ moe_status_t launch_gemm_mxfp4(moe_gemm_op_t op, const void* a, const int32_t* s
 constexpr int mxfp4_pair_columns(int H) { return H > 2048 ? 16 : 32; }
 
 // The layer of a few tokens, pair by pair (no permutation): the pairs' slots
-// (routed here, or from the slot map), act [T * topk, I] = the SwiGLU rows,
+// (routed here, or from the slot map) and act [T * topk, I] = the SwiGLU rows,
 // then out = the weighted sum of the down products, with shared and
 // accumulate as in launch_combine.
-moe_status_t launch_mxfp4_pairs(const void* x, const PairRouting& routing, int T, int topk,
-                                const uint8_t* w_gate_up, const uint8_t* gate_up_scale,
-                                const uint8_t* w_down, const uint8_t* down_scale, int H, int I,
-                                void* act, void* out, bool out_bf16, int accumulate,
-                                const void* shared, hipStream_t stream);
+moe_status_t launch_mxfp4_pairs_gate_up(const void* x, const PairRouting& routing, int T,
+                                        int topk, const uint8_t* w_gate_up,
+                                        const uint8_t* gate_up_scale, int H, int I, void* act,
+                                        hipStream_t stream);
+moe_status_t launch_mxfp4_pairs_down(const void* act, const MapOut& map, int T, int topk,
+                                     const uint8_t* w_down, const uint8_t* down_scale, int H,
+                                     int I, void* out, bool out_bf16, int accumulate,
+                                     const void* shared, hipStream_t stream);
 
 constexpr int kMaxNormWidth = 32768;
 // h = x + residual (null: x), the norm of h times gamma as y (dtype of x)

@@ -462,7 +462,8 @@ moe_status_t moe_forward(const moe_config_t* cfg, const moe_forward_args_t* args
       args->logits, cfg->E_global, cfg->renormalize ? 1 : 0,
       args->logits ? route_lanes(cfg->E_global, K, cfg->num_expert_group) : 0,
       {cfg->ep_rank * E_local, E_local, S, args->rep_off, args->rep_slots, slot, w_masked, mask}};
-  if (pairs && pair_routing.lanes > 0) {
+  const bool routed_by_gate_up = pairs && pair_routing.lanes > 0;
+  if (routed_by_gate_up) {
     // nothing to launch
   } else if (plan) {
     MOE_TRY(launch_plan(args->logits, T, cfg->E_global, K, cfg->renormalize ? 1 : 0,
@@ -480,7 +481,7 @@ moe_status_t moe_forward(const moe_config_t* cfg, const moe_forward_args_t* args
     MOE_TRY(launch_slot_map(ids_in, w_in, T, K, cfg->ep_rank * E_local, E_local, args->rep_off,
                             args->rep_slots, S, slot, w_masked, mask, stream));
   }
-  MOE_TRY(mark(MOE_EV_ROUTED));
+  if (!routed_by_gate_up) MOE_TRY(mark(MOE_EV_ROUTED));
   // bf16 with a direct-to-LDS shape: the gate/up GEMM fetches token rows of x
   // itself, so the permutation only orders the pairs (no x_perm copy).
   // Input-side routing gathers rows scaled by the pair weight instead.
@@ -495,14 +496,21 @@ moe_status_t moe_forward(const moe_config_t* cfg, const moe_forward_args_t* args
                            offsets, sorted_pairs, pair_row, fused_gather ? nullptr : x_perm,
                            perm_ws, stream, on_input ? w_masked : nullptr,
                            quant ? &fq : nullptr));
-  MOE_TRY(mark(MOE_EV_PERMUTED));
+  if (!routed_by_gate_up) MOE_TRY(mark(MOE_EV_PERMUTED));
   if (pairs) {
-    MOE_TRY(launch_mxfp4_pairs(args->x, pair_routing, T, K,
-                               static_cast<const uint8_t*>(args->w_gate_up), args->w_gate_up_e8m0,
-                               static_cast<const uint8_t*>(args->w_down), args->w_down_e8m0, H, I,
-                               act, args->out, cfg->out_dtype == MOE_DTYPE_BF16, cfg->accumulate,
-                               args->shared_out, stream));
+    MOE_TRY(launch_mxfp4_pairs_gate_up(args->x, pair_routing, T, K,
+                                       static_cast<const uint8_t*>(args->w_gate_up),
+                                       args->w_gate_up_e8m0, H, I, act, stream));
+    if (routed_by_gate_up) {  // an event follows the launch that ends its stage
+      MOE_TRY(mark(MOE_EV_ROUTED));
+      MOE_TRY(mark(MOE_EV_PERMUTED));
+    }
     MOE_TRY(mark(MOE_EV_GATE_UP));
+    MOE_TRY(launch_mxfp4_pairs_down(act, pair_routing.map, T, K,
+                                    static_cast<const uint8_t*>(args->w_down),
+                                    args->w_down_e8m0, H, I, args->out,
+                                    cfg->out_dtype == MOE_DTYPE_BF16, cfg->accumulate,
+                                    args->shared_out, stream));
     MOE_TRY(mark(MOE_EV_DOWN));
     return mark(MOE_EV_COMBINED);
   }

@@ -1164,11 +1164,10 @@ moe_status_t launch_gemm_mxfp4(moe_gemm_op_t op, const void* a, const int32_t* s
   return launch_status();
 }
 
-moe_status_t launch_mxfp4_pairs(const void* x, const PairRouting& routing, int T, int topk,
-                                const uint8_t* w_gate_up, const uint8_t* gate_up_scale,
-                                const uint8_t* w_down, const uint8_t* down_scale, int H, int I,
-                                void* act, void* out, bool out_bf16, int accumulate,
-                                const void* shared, hipStream_t stream) {
+moe_status_t launch_mxfp4_pairs_gate_up(const void* x, const PairRouting& routing, int T,
+                                        int topk, const uint8_t* w_gate_up,
+                                        const uint8_t* gate_up_scale, int H, int I, void* act,
+                                        hipStream_t stream) {
   using std::integral_constant;
   const int P = T * topk;
   const int S = routing.map.S;
@@ -1193,12 +1192,17 @@ moe_status_t launch_mxfp4_pairs(const void* x, const PairRouting& routing, int T
     gate_up(integral_constant<int, 8>{}, std::false_type{});
   else
     gate_up(integral_constant<int, 4>{}, std::false_type{});
-  const moe_status_t st = launch_status();
-  if (st != MOE_OK) return st;
+  return launch_status();
+}
+
+moe_status_t launch_mxfp4_pairs_down(const void* act, const MapOut& map, int T, int topk,
+                                     const uint8_t* w_down, const uint8_t* down_scale, int H,
+                                     int I, void* out, bool out_bf16, int accumulate,
+                                     const void* shared, hipStream_t stream) {
   auto down = [&](auto o) {
     using OT = decltype(o);
     mxfp4_pair_down_kernel<OT><<<dim3(H / 16, T), 512, 0, stream>>>(
-        act16, routing.map.slot, routing.map.mask, routing.map.w_masked, topk, S, w_down,
+        static_cast<const uint16_t*>(act), map.slot, map.mask, map.w_masked, topk, map.S, w_down,
         down_scale, H, I, static_cast<OT*>(out), accumulate,
         static_cast<const uint16_t*>(shared));
   };

@@ -579,3 +579,40 @@ def test_layer_of_one_rank_of_very_many_pairs():
     assert (np.abs(got - want) <= tol * (1 + K * U) + 2.0 ** -8 * (np.abs(want) + tol) + 1e-38).all()
     del out
     torch.cuda.empty_cache()
+
+
+# ------------------------------------------------------------------ stage events
+@pytest.mark.parametrize("T", [1, 2, 16])
+@pytest.mark.parametrize("given", [False, True])
+def test_stage_events_follow_their_stages(T, given):
+    """An event is recorded behind the launch that ends its stage: the weights that a product has to read, at
+    25 TB/s (three times what the memory gives; they pass every L2), are a time that has to lie between the
+    events around it."""
+    dev = device()
+    announce(f"mxfp4 events T={T} given={given}")
+    H, I, K, E = 8192, 16384, 4, 8
+    g = torch.Generator(device=dev).manual_seed(T)
+    byte = lambda *s: torch.randint(0, 256, s, generator=g, device=dev, dtype=torch.uint8)  # noqa: E731
+    sc = lambda *s: torch.randint(118, 121, s, generator=g, device=dev, dtype=torch.uint8)  # noqa: E731
+    w = (byte(E, 2 * I, H // 2), byte(E, H, I // 2))
+    kw = dict(w_gate_up_scale=sc(E, 2 * I, H // 32), w_down_scale=sc(E, H, I // 32))
+    x = torch.randn(T, H, generator=g, device=dev).bfloat16()
+    logits = torch.randn(T, E, generator=g, device=dev)
+    if given:
+        kw["topk_ids"], kw["topk_w"] = moe.route(logits, K, True)
+    else:
+        kw["logits"] = logits
+    cfg = moe.ForwardConfig(T=T, H=H, I=I, E_global=E, K=K, renormalize=True, S=E, dtype=moe.MXFP4)
+    ev = [torch.cuda.Event(enable_timing=True) for _ in range(moe.NUM_EVENTS)]
+    for e in ev:
+        e.record()
+    for _ in range(3):
+        moe.forward(cfg, x, *w, events=[e.cuda_event for e in ev], **kw)
+    torch.cuda.synchronize()
+    us = [1e3 * a.elapsed_time(b) for a, b in zip(ev, ev[1:])]
+    assert all(t >= 0 for t in us)
+    down = K * H * I * 17 / 32 / 25e6       # at least K slots of one matrix: 11 us
+    # routing and permutation stand before GATE_UP, in the gate/up launch or before it
+    assert sum(us[:3]) >= 2 * down and us[3] + us[4] >= down and us[3] >= down, us
+    if T <= 2 and not given:                # routed by the gate/up product: those stages end with it
+        assert us[0] >= 2 * down, us
