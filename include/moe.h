@@ -358,7 +358,8 @@ moe_status_t moe_grouped_gemm_mxfp4(moe_gemm_op_t op, const void* a, const int32
  *   q = quantize(v, q_scale) as moe_quantize_fp8 does, from the unrounded v.
  * x, residual, residual_out, y [T, H] and gamma [H] of dt (f32 or bf16); q
  * codes [T, H]. residual_out, y and q may be NULL, but not all three of them.
- * residual_out may be x or residual itself, and y may be x; no other overlap.
+ * residual_out may be x or residual itself, and y may be x, but not both x
+ * (y == residual_out is MOE_ERR_INVALID_ARG); no other overlap.
  * q's consumer is moe_forward with x_codes and a1_scale = q_scale, or
  * moe_grouped_gemm_fp8. H % 8 == 0, H <= 32768; eps finite and >= 0; q_scale
  * finite and > 0 where q is given; 16-byte aligned pointers. The sum of

@@ -612,6 +612,7 @@ moe_status_t moe_rms_norm(const void* x, const void* residual, const void* gamma
   if (!dtype_ok(dt) || H % 8 != 0 || H > kMaxNormWidth) return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
   if (!x || !gamma || (!residual_out && !y && !q)) return MOE_ERR_INVALID_ARG;
+  if (y && y == residual_out) return MOE_ERR_INVALID_ARG;
   if (q && !scale_ok(q_scale)) return MOE_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(residual) || !aligned16(gamma) || !aligned16(residual_out) ||
       !aligned16(y) || !aligned16(q))

@@ -38,6 +38,15 @@ def test_rms_norm_validation(so):
     assert call(T=0, x=None, gamma=None, scale=0.0) == 0
 
 
+def test_rms_norm_refuses_one_place_for_two_outputs(so):
+    """residual_out may be x and y may be x, but not both at once."""
+    other = ctypes.c_void_p(1 << 20)
+
+    def call(ro, y):
+        return so.moe_rms_norm(fake, other, other, 1, 4, 64, 1e-6, ro, y, None, 0.0, None)
+    assert call(fake, fake) == INVALID and call(other, other) == INVALID
+
+
 def test_balance_loss_validation(so):
     ws = so.moe_balance_loss_workspace_size
     assert ws(0, 8, 2) > 0 and ws(1 << 20, 1024, 32) > 0

@@ -186,3 +186,14 @@ def test_norm_of_more_rows_than_a_grid_line_has_threads_for():
     whole = T // 251
     assert (y[:whole * 251].view(whole, 251, H) == small).all() and (q[:whole * 251].view(whole, 251, H) == qs).all()
     assert torch.equal(y[whole * 251:], small[:T - whole * 251]) and torch.equal(q[whole * 251:], qs[:T - whole * 251])
+
+
+def test_norm_refuses_one_place_for_two_outputs():
+    dev = device()
+    x, r, gamma = (t.to(dev) for t in _inputs(4, 64, torch.bfloat16, 1))
+    for both in (x, r, torch.empty_like(x)):
+        with pytest.raises(RuntimeError):
+            moe.rms_norm(x, gamma, residual=r, y=both, residual_out=both)
+    y, ro, _ = moe.rms_norm(x.clone(), gamma, residual=r.clone())
+    got = moe.rms_norm(x, gamma, residual=r, y=x, residual_out=r)     # each in place of its own
+    assert torch.equal(got[0], y) and torch.equal(got[1], ro)
