@@ -45,9 +45,10 @@ MAX_EXPERTS = 1024
 MAX_TOPK = 32
 MAX_SLOTS = 1024
 
+# ForwardConfig dtype of the 4-bit expert path (a name for it where torch has no such type)
+MXFP4 = getattr(torch, "float4_e2m1fn_x2", "float4_e2m1fn_x2")
 _DT = {torch.float32: MOE_DTYPE_F32, torch.bfloat16: MOE_DTYPE_BF16,
-       torch.float8_e4m3fn: MOE_DTYPE_FP8_E4M3, torch.float4_e2m1fn_x2: MOE_DTYPE_MXFP4}
-MXFP4 = torch.float4_e2m1fn_x2  # ForwardConfig dtype of the 4-bit expert path
+       torch.float8_e4m3fn: MOE_DTYPE_FP8_E4M3, MXFP4: MOE_DTYPE_MXFP4}
 MX_GROUP = 32  # weights that share one scale byte
 FP8 = torch.float8_e4m3fn  # ForwardConfig dtype of the FP8 expert path
 _CODES = (torch.uint8, torch.float8_e4m3fn)  # tensors holding E4M3 codes

@@ -3,6 +3,9 @@ entry points: every call here fails its checks, has no work, or asks a
 workspace size, so nothing reaches a device.
 """
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -167,3 +170,23 @@ def test_a2a_dispatch_refuses_more_tokens_than_its_grid_holds(so):
                                    ctypes.c_size_t(n), None)
     assert call(most, 0) == WORKSPACE
     assert call(most + 1, 0) == UNSUPPORTED and call(1 << 24, 1 << 40) == UNSUPPORTED
+
+
+def test_package_needs_no_torch_type_of_four_bits():
+    """A torch without float4_e2m1fn_x2: the package imports, and MXFP4 still names its layers."""
+    code = """
+import torch
+del torch.float4_e2m1fn_x2
+import ctypes, moe_expert_dispatch_amd as moe
+size = lambda dt: moe.lib().moe_forward_workspace_size(ctypes.byref(moe.ForwardConfig(
+    T=16, H=64, I=64, E_global=8, K=2, renormalize=True, S=8, dtype=dt).c_struct()))
+assert moe.ForwardConfig(16, 64, 64, 8, 2, True, 8, moe.MXFP4).out_dtype == torch.bfloat16
+print(size(moe.MXFP4), size(torch.bfloat16), size(torch.float32))
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    run = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=100)
+    assert run.returncode == 0, run.stderr
+    sizes = [int(v) for v in run.stdout.split()]
+    here = [moe.lib().moe_forward_workspace_size(ctypes.byref(_cfg(dtype=dt).c_struct()))
+            for dt in (moe.MXFP4, torch.bfloat16, torch.float32)]
+    assert sizes == here and all(sizes)
