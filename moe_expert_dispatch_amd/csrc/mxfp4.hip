@@ -1085,10 +1085,8 @@ void launch_product(const void* a, const int32_t* offsets, const int32_t* sorted
         go(i1{}, rb, i4{}, std::false_type{});
       else if (split == 2)
         go(i2{}, rb, i4{}, std::false_type{});
-      else if (split == 4)
+      else  // 4: eight waves split more than 2048 k's, of which 16 rows are two windows
         go(i4{}, rb, i4{}, std::false_type{});
-      else
-        go(i8{}, rb, i4{}, std::false_type{});
     } else if (split > 1) {
       go(i8{}, rb, i2{}, std::true_type{});
     } else if constexpr (M == 1) {
