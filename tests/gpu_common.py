@@ -43,6 +43,18 @@ def assert_close(got, ref, tol, what="", extra=None):
             f"worst at {i}: got {got[i]!r}, ref {ref[i]!r}")
 
 
+def assert_within(got, ref, allow, what=""):
+    """|got - ref| <= allow for every element, all three finite: a comparison with a NaN is false both
+    ways, so the elements that hold are what is asked for, not those that do not."""
+    got, ref, allow = np.broadcast_arrays(*(np.asarray(a, dtype=np.float64) for a in (got, ref, allow)))
+    with np.errstate(invalid="ignore"):
+        good = np.isfinite(got) & np.isfinite(ref) & np.isfinite(allow) & (np.abs(got - ref) <= allow)
+    if not good.all():
+        i = np.unravel_index(np.argmin(good), good.shape)
+        raise AssertionError(f"{what}: {int((~good).sum())} of {good.size} elements; first at {i}: "
+                             f"got {got[i]!r}, ref {ref[i]!r}, allowed {allow[i]!r}")
+
+
 def rel_fro(got, ref):
     got = np.asarray(got, dtype=np.float64)
     ref = np.asarray(ref, dtype=np.float64)

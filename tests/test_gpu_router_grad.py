@@ -14,7 +14,7 @@ import torch
 
 import moe_expert_dispatch_amd as moe
 import oracle
-from gpu_common import announce, device, np64
+from gpu_common import announce, assert_within, device, np64
 
 pytestmark = pytest.mark.gpu
 
@@ -285,6 +285,90 @@ def test_refusals():
         moe.route_backward(l, ids, None, True)
     with pytest.raises(RuntimeError):
         moe.balance_loss(l, ids, 1.0, ws=torch.empty(8, dtype=torch.uint8, device=dev))
+
+
+# ------------------------------------------------------------------ every element a number
+def _grad_within(dev, l, ids, dw, mask, renorm, counts, coef, what):
+    """As _check_grad, in a form that no NaN passes, for finite or -inf logits and finite dw."""
+    T, E = l.shape
+    K = ids.shape[1]
+    got = np64(moe.route_backward(*_dev(dev, l, ids, dw), renorm, counts=counts, coef=coef,
+                                  token_mask=_dev(dev, mask)[0]))
+    c = None if counts is None else counts.cpu().numpy().astype(np.int64)
+    ok = np.ones(T, bool) if mask is None else mask.numpy() != 0
+    keep = torch.from_numpy(ok)
+    want, size = np.zeros((T, E)), np.zeros((T, E))
+    l, ids, dw = l[keep], ids[keep], None if dw is None else dw[keep]
+    want[ok] = oracle.route_backward(l, ids, dw, renorm, c, coef, 1.0)
+    p = oracle.layer_oracle.probabilities(l)
+    s = np.zeros_like(p)
+    if dw is not None:
+        w = oracle.routing_weights(l, ids, renorm)
+        a = w * np.abs(np64(dw))
+        dot = a.sum(1, keepdims=True)
+        # what the 64 bits of the reference leave where its terms cancel (see _check_grad)
+        s += (2 * E * 2.0 ** -53 / (34 * U)) * p * 2 * dot
+        if not renorm:
+            s += p * dot
+        i = ids.numpy()
+        for t, k in zip(*np.nonzero((i >= 0) & (i < E))):
+            s[t, i[t, k]] += a[t, k] + (w[t, k] * dot[t, 0] if renorm else 0.0)
+    if c is not None and c[E] > 0:
+        f = c[:E] / (c[E] * K)
+        s += abs(coef) * E / c[E] * p * (f + (p * f).sum(1, keepdims=True))
+    size[ok] = s
+    eps = (2 * (2 * _range(l, None) + 32) + K + 22 + 12) * U
+    assert_within(got, want, eps * size + ok[:, None] * 1e-38, what)
+
+
+@pytest.mark.parametrize("T,E,K", CASES)
+@pytest.mark.parametrize("pad", [0.0, 0.3])
+def test_gradient_is_a_number_everywhere(T, E, K, pad):
+    dev = device()
+    announce(f"router grad numbers T={T} E={E} K={K} pad={pad}")
+    l, ids, dw, mask = _case(T, E, K, 7 * T + E + K, pad)
+    counts = moe.balance_loss(*_dev(dev, l, ids), 0.02, token_mask=_dev(dev, mask)[0])[1]
+    for renorm in (False, True):
+        _grad_within(dev, l, ids, dw, mask, renorm, counts, 0.02, f"both renorm={renorm}")
+        _grad_within(dev, l, ids, dw, mask, renorm, None, 0.0, f"weights renorm={renorm}")
+    _grad_within(dev, l, ids, None, mask, False, counts, 0.02, "loss only")
+
+
+@pytest.mark.parametrize("E,K", [(8, 2), (60, 4), (256, 8), (1000, 8)])
+def test_gradient_is_a_number_beside_forbidden_and_foreign(E, K):
+    """Experts at -inf, whole rows of them, selected ones among them, foreign and repeated ids."""
+    dev = device()
+    announce(f"router grad numbers forbidden E={E} K={K}")
+    T = 64
+    l, ids, dw, _ = _case(T, E, K, E)
+    l[:, ::2] = float("-inf")
+    l[5] = float("-inf")
+    l[6, 1:] = float("-inf")
+    l[6, 0] = 0.25
+    ids = torch.sort(l, dim=1, descending=True, stable=True)[1][:, :K].int()
+    ids[8] = 0                                   # a forbidden expert alone, K times
+    ids[9, 0] = 2                                # and one beside others
+    ids[10] = -1
+    ids[11, -1] = E
+    ids[12] = ids[12, 0]
+    for coef, loss in ((1.0, True), (0.0, False)):
+        counts = moe.balance_loss(*_dev(dev, l, ids), 1.0)[1] if loss else None
+        for renorm in (False, True):
+            _grad_within(dev, l, ids, dw, None, renorm, counts, coef, f"loss={loss} renorm={renorm}")
+
+
+def test_gradient_repeats_with_an_expert_held_many_times():
+    """Terms of one expert held up to 32 times are added in LDS: the same bits every time."""
+    dev = device()
+    announce("router grad repeated ids")
+    g = torch.Generator(device=dev).manual_seed(9)
+    for E, K in ((8, 8), (64, 16), (256, 32), (700, 32)):
+        l = torch.randn(500, E, generator=g, device=dev)
+        dw = torch.randn(500, K, generator=g, device=dev)
+        ids = torch.randint(0, 3, (500, K), generator=g, device=dev, dtype=torch.int32)
+        first = moe.route_backward(l, ids, dw, False)
+        for _ in range(20):
+            assert torch.equal(moe.route_backward(l, ids, dw, False), first)
 
 
 def test_most_tokens():
