@@ -230,6 +230,24 @@ def test_products_with_nan_scale_and_capacity():
     assert (c[6:] == 3.0).all() and torch.equal(c[:4].cpu(), y[:4])
 
 
+@pytest.mark.parametrize("low", [0, 246])
+@pytest.mark.parametrize("rows", [1, 3, 9, 20, 60, 200])
+def test_products_at_the_ends_of_the_scales(low, rows):
+    """The least scales (weights below bf16's normal numbers) with large activations, and the largest with small
+    ones: products are exact there too."""
+    dev = device()
+    announce(f"mxfp4 products scales from {low} rows={rows}")
+    H, I, S = 256, 160, 2
+    g = torch.Generator().manual_seed(low + rows)
+    wd = torch.randint(0, 256, (S, H, I // 2), generator=g, dtype=torch.uint8)
+    ds = torch.randint(low, low + 7, (S, H, I // 32), generator=g, dtype=torch.uint8)
+    a = (torch.randn(S * rows, I, generator=g) * (2.0 ** 110 if low == 0 else 2.0 ** -110)).bfloat16()
+    off = _offsets([rows] * S)
+    y = moe.grouped_gemm_mxfp4(moe.DOWN, a.to(dev), off.to(dev), wd.to(dev), ds.to(dev), c_dtype=torch.float32)
+    want, m = oracle.mxfp4_grouped_down(a, off, wd, ds)
+    assert (np.abs(np64(y) - want) <= (2 * I * U * m + 2 * U * np.abs(want)) * 1.01).all()
+
+
 def test_products_refusals():
     dev = device()
     w, s = _weights((2, 64, 64), 1, 64)
@@ -579,6 +597,55 @@ def test_layer_of_one_rank_of_very_many_pairs():
     assert (np.abs(got - want) <= tol * (1 + K * U) + 2.0 ** -8 * (np.abs(want) + tol) + 1e-38).all()
     del out
     torch.cuda.empty_cache()
+
+
+# ------------------------------------------------------------------ pair by pair
+def _taken_pair_by_pair(dev, L, T, **kw):
+    """Whether a call goes pair by pair, by what it writes into its workspace: routing and activations, but no
+    expert output of each pair ([T * K, H] f32)."""
+    P, H, I = T * L["cfg"]["K"], L["cfg"]["H"], L["cfg"]["I"]
+    assert 7 * H // 2 > 17 + 2 * I
+    cfg = moe.ForwardConfig(T=T, **L["cfg"])
+    ws = torch.full((moe.forward_workspace_size(cfg),), 0xA5, dtype=torch.uint8, device=dev)
+    out = _run(dev, L, T, ws=ws, **kw)
+    return out, int((ws != 0xA5).sum()) <= P * (17 + 2 * I)
+
+
+# H in each form of the gate/up product (up to 2048, 4096, more), over whole and broken steps of 128, 256 and 512
+@pytest.mark.parametrize("H", [608, 1184, 2048, 2080, 2560, 3968, 4096, 4128, 6176])
+@pytest.mark.parametrize("T,K,I", [(1, 3, 608), (2, 2, 32), (1, 1, 928), (2, 4, 352)])
+def test_pairs_of_wide_rows(H, T, K, I):
+    dev = device()
+    announce(f"mxfp4 pairs T={T} K={K} H={H} I={I}")
+    L = _layer(T, H, I, K + 1, K, H + I)
+    got, pairs = _taken_pair_by_pair(dev, L, T, logits=L["logits"])
+    assert pairs
+    ids, w = oracle.route(L["logits"], K, True)
+    want, tol = _reference(L, T, ids, w)
+    assert (np.abs(np64(got) - want) <= tol + 2.0 ** -8 * (np.abs(want) + tol)).all()
+
+
+# (T, K, H, I, pair by pair): at and just past 64 pairs, 16 M weights of one matrix over all pairs and
+# 768 blocks of 32 or 16 columns
+BOUNDS = [(16, 4, 256, 64, True), (13, 5, 256, 64, False), (64, 1, 320, 32, True), (65, 1, 320, 32, False),
+          (16, 4, 1024, 256, True), (16, 4, 1024, 288, False), (16, 4, 672, 384, True), (16, 4, 608, 416, False),
+          (5, 4, 2080, 384, True), (5, 4, 2080, 416, False), (4, 5, 4096, 192, True), (5, 4, 4128, 192, True),
+          (3, 2, 5216, 512, True), (3, 2, 5216, 544, False), (24, 2, 2080, 160, True), (10, 6, 2048, 128, True)]
+
+
+@pytest.mark.parametrize("T,K,H,I,pairs", BOUNDS)
+def test_pairs_at_their_bounds(T, K, H, I, pairs):
+    """Both sides of each bound, routed here and with given ids, with replicated slots, against the oracle."""
+    dev = device()
+    announce(f"mxfp4 pair bounds T={T} K={K} H={H} I={I}")
+    L = _layer(T, H, I, 8, K, T + K + H + I, extra=2)
+    ids, w = oracle.route(L["logits"], K, True)
+    want, tol = _reference(L, T, ids, w)
+    for kw in (dict(logits=L["logits"]),
+               dict(topk_ids=torch.from_numpy(ids.astype(np.int32)), topk_w=torch.from_numpy(w.astype(np.float32)))):
+        got, taken = _taken_pair_by_pair(dev, L, T, **kw)
+        assert taken == pairs
+        assert (np.abs(np64(got) - want) <= tol + 2.0 ** -8 * (np.abs(want) + tol)).all()
 
 
 # ------------------------------------------------------------------ stage events
