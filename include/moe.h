@@ -284,7 +284,8 @@ moe_status_t moe_grouped_gemm(moe_gemm_op_t op, moe_dtype_t dt, const void* a,
 /*
  * moe_quantize_fp8 -- q[i] = quantize(x[i], scale) for i < n.
  * x of x_dt (MOE_DTYPE_BF16 or MOE_DTYPE_F32) and q (bytes) are device
- * buffers, 16-byte aligned; scale must be finite and > 0. x must hold
+ * buffers, 16-byte aligned; scale must be finite and > 2^-128 (as
+ * every scale that codes are made with). x must hold
  * finite values (a NaN input gives an unspecified code).
  */
 moe_status_t moe_quantize_fp8(const void* x, moe_dtype_t x_dt, int64_t n, float scale,
@@ -362,7 +363,7 @@ moe_status_t moe_grouped_gemm_mxfp4(moe_gemm_op_t op, const void* a, const int32
  * (y == residual_out is MOE_ERR_INVALID_ARG); no other overlap.
  * q's consumer is moe_forward with x_codes and a1_scale = q_scale, or
  * moe_grouped_gemm_fp8. H % 8 == 0, H <= 32768; eps finite and >= 0; q_scale
- * finite and > 0 where q is given; 16-byte aligned pointers. The sum of
+ * finite and > 2^-128 where q is given; 16-byte aligned pointers. The sum of
  * squares is f32, f64 where they would leave f32's range. h must be finite; a
  * row with others has unspecified outputs (a NaN stays NaN in y), and so has a
  * row of zeros with eps = 0.

@@ -34,6 +34,8 @@ int dtype_bytes(moe_dtype_t dt) {
 // Bytes of a weight for the weight-panel limit (MXFP4: rounded up).
 int weight_bytes(moe_dtype_t dt) { return dt == MOE_DTYPE_MXFP4 ? 1 : dtype_bytes(dt); }
 bool scale_ok(float s) { return s > 0.0f && s <= 3.4e38f; }  // finite, positive (false for NaN)
+// A scale that codes are made with: they are of v * (1 / s), in f32.
+bool code_scale_ok(float s) { return scale_ok(s) && 1.0f / s <= 3.4e38f; }
 
 // T * K and T * K * max(H, I) must stay addressable with 32-bit row indices.
 bool pairs_fit(int T, int K) { return (long long)T * K < (1LL << 31); }
@@ -242,7 +244,8 @@ moe_status_t check_config(const moe_config_t* c) {
   if ((!dtype_ok(c->dtype) && !fp8 && !mx) || !dtype_ok(c->out_dtype)) return MOE_ERR_UNSUPPORTED;
   if (c->x_codes && !fp8) return MOE_ERR_INVALID_ARG;
   if (mx && (c->H % 32 != 0 || c->I % 32 != 0)) return MOE_ERR_UNSUPPORTED;
-  if (fp8 && (!scale_ok(c->a1_scale) || !scale_ok(c->a2_scale))) return MOE_ERR_INVALID_ARG;
+  if (fp8 && (!code_scale_ok(c->a1_scale) || !code_scale_ok(c->a2_scale)))
+    return MOE_ERR_INVALID_ARG;
   if (fp8 && (c->routing_on_input || !gemm_fp8_ok(c->H) || !gemm_fp8_ok(c->I) ||
               !gemm_fp8_gather_ok(c->T_max, c->H)))
     return MOE_ERR_UNSUPPORTED;
@@ -553,7 +556,7 @@ moe_status_t moe_forward(const moe_config_t* cfg, const moe_forward_args_t* args
 
 moe_status_t moe_quantize_fp8(const void* x, moe_dtype_t x_dt, int64_t n, float scale,
                               uint8_t* q, hipStream_t stream) {
-  if (n < 0 || !scale_ok(scale)) return MOE_ERR_INVALID_ARG;
+  if (n < 0 || !code_scale_ok(scale)) return MOE_ERR_INVALID_ARG;
   if (x_dt != MOE_DTYPE_BF16 && x_dt != MOE_DTYPE_F32) return MOE_ERR_UNSUPPORTED;
   if (n == 0) return MOE_OK;
   if (!x || !q || !aligned16(x) || !aligned16(q)) return MOE_ERR_INVALID_ARG;
@@ -569,7 +572,7 @@ moe_status_t moe_grouped_gemm_fp8(moe_gemm_op_t op, const uint8_t* a, float a_sc
   const moe_status_t st =
       check_gemm(op, MOE_DTYPE_BF16, a, offsets, S, max_rows, w, H, I, c, 1);
   if (st != MOE_OK) return st;
-  if (!scale_ok(a_scale) || (op == MOE_GEMM_GATE_UP_SWIGLU && !scale_ok(c_scale)))
+  if (!scale_ok(a_scale) || (op == MOE_GEMM_GATE_UP_SWIGLU && !code_scale_ok(c_scale)))
     return MOE_ERR_INVALID_ARG;
   if (max_rows > 0 && !w_scale) return MOE_ERR_INVALID_ARG;
   if (!gemm_fp8_ok(op == MOE_GEMM_GATE_UP_SWIGLU ? H : I)) return MOE_ERR_UNSUPPORTED;
@@ -613,7 +616,7 @@ moe_status_t moe_rms_norm(const void* x, const void* residual, const void* gamma
   if (T == 0) return MOE_OK;
   if (!x || !gamma || (!residual_out && !y && !q)) return MOE_ERR_INVALID_ARG;
   if (y && y == residual_out) return MOE_ERR_INVALID_ARG;
-  if (q && !scale_ok(q_scale)) return MOE_ERR_INVALID_ARG;
+  if (q && !code_scale_ok(q_scale)) return MOE_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(residual) || !aligned16(gamma) || !aligned16(residual_out) ||
       !aligned16(y) || !aligned16(q))
     return MOE_ERR_INVALID_ARG;

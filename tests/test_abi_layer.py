@@ -41,6 +41,19 @@ def test_rms_norm_validation(so):
     assert call(T=0, x=None, gamma=None, scale=0.0) == 0
 
 
+def test_scales_need_a_finite_reciprocal(so):
+    """Codes are of v * (1 / scale): a scale below 2^-128 has no reciprocal in f32 (0 would get the code of NaN)."""
+    other = ctypes.c_void_p(1 << 20)
+    for s in (1e-39, 2.0 ** -128, 1e-45):
+        assert so.moe_rms_norm(fake, None, other, 1, 4, 64, 1e-6, None, None, fake, s, None) == INVALID
+        assert so.moe_quantize_fp8(fake, 1, 4, s, fake, None) == INVALID
+        cfg = _cfg(H=256, I=256, dtype=moe.FP8, a2_scale=s)
+        assert so.moe_forward_workspace_size(ctypes.byref(cfg.c_struct())) == 0
+    for s in (2.0 ** -127, 2.0 ** -126, 3.0e38):
+        cfg = _cfg(H=256, I=256, dtype=moe.FP8, a2_scale=s)
+        assert so.moe_forward_workspace_size(ctypes.byref(cfg.c_struct())) > 0
+
+
 def test_rms_norm_refuses_one_place_for_two_outputs(so):
     """residual_out may be x and y may be x, but not both at once."""
     other = ctypes.c_void_p(1 << 20)
