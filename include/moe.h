@@ -341,8 +341,9 @@ moe_status_t moe_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scale, in
  * [S, H, I/2]; w_scale: [S, 2I, H/32] or [S, H, I/32]. c: bf16, or f32 for
  * the down product (c_dt). H % 32 == 0 and I % 32 == 0. Products are exact
  * (a code times its scale is a bf16 value), sums f32, one rounding to c_dt;
- * the order of the sums depends on max_rows, S and the shape, not on the
- * scheduling. A weight whose scale byte is 255 makes its outputs NaN, one past
+ * the order of the sums depends on max_rows, S, the shape and the device's
+ * number of compute units, not on the scheduling (in moe_forward on T * K,
+ * ep_size and E_global in place of max_rows). A weight whose scale byte is 255 makes its outputs NaN, one past
  * bf16's range (scale bytes 253 and 254 with large codes) not finite. The
  * other rules are those of moe_grouped_gemm; w_scale is 16-byte aligned.
  */
@@ -387,7 +388,8 @@ moe_status_t moe_rms_norm(const void* x, const void* residual, const void* gamma
  * have no influence whatever they hold). counts [E + 1] int32, counts[E] = n;
  * prob [E] f32; loss one f32. With no valid token counts, prob and loss are 0.
  * Logits of -inf have probability 0 (a row of only -inf: all 0); NaN and +inf
- * in a valid row give NaN. Sums are f32 in a fixed order, f64 over blocks.
+ * in a valid row give NaN. Sums are f32 in a fixed order, f64 over blocks
+ * (of many blocks sixteen partial sums, rounded to f32 in between).
  * Limits as moe_route. ws: 16-byte aligned, at least
  * moe_balance_loss_workspace_size(T, E, K) bytes, contents ignored.
  *
@@ -548,7 +550,8 @@ typedef struct {
  * w_down are codes [S, 2I, H/2] and [S, H, I/2] with the scales
  * args->w_gate_up_e8m0 and args->w_down_e8m0; the products are
  * moe_grouped_gemm_mxfp4 with the SwiGLU output in bf16 and the expert
- * outputs in f32. H % 32 == 0 and I % 32 == 0; cfg->gemm_blocks has no effect.
+ * outputs in f32. H % 32 == 0 and I % 32 == 0, and a slot's gate/up panel,
+ * 2 * I * H weights, is under 2^31; cfg->gemm_blocks has no effect.
  */
 size_t moe_forward_workspace_size(const moe_config_t* cfg);
 moe_status_t moe_forward(const moe_config_t* cfg, const moe_forward_args_t* args, void* ws,

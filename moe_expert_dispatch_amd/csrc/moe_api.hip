@@ -124,7 +124,9 @@ moe_status_t launch_gemm(moe_gemm_op_t op, moe_dtype_t dt, const void* a, const 
 }
 
 // An MXFP4 layer takes its pairs one by one, each reading its slot's weights
-// itself, for up to two tokens, whose pairs share no slot or few, and where so
+// itself, for up to two tokens (also where they share slots: two tokens, all 8 of
+// 8 experts of 2048 x 1408 25.6 us, three tokens, by slots, 26.7; 4096 x 1024
+// 31.8 and 30.9; 8 of 64 experts 34.7), and where so
 // few and small pairs leave less work than the two launches cost that this
 // saves: 64 pairs, 16 M weights of one matrix over all pairs (26 MB of codes and
 // scales), and 768 gate/up blocks (one and a half rounds; each routes its

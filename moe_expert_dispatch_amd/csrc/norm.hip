@@ -14,7 +14,10 @@
 // Bound by the bytes: 8192 rows of 5120 bf16 with residual and codes 71 us,
 // 5.3 TB/s; 16384 of 4096 103 us, 5.9 TB/s. One vector a thread (VPT = 1) is
 // the fastest wherever 1024 threads hold a row: with two a thread 72 and 111
-// us, with four 79 and 121. A single row of 4096 takes 2.4 us.
+// us, with four 79 and 121. A single row of 4096 takes 2.4 us. Rows of 512 and
+// 1024 run at 6.5 TB/s and more (134 and 268 MB, in part in the memory-side
+// cache); shorter ones leave lanes of their one wave idle: 524288 rows of 128
+// (the norm of heads) 115 us, 2.3 TB/s.
 #include "common.h"
 #include "vec8.h"
 

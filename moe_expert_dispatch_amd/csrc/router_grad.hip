@@ -230,6 +230,8 @@ __global__ __launch_bounds__(kLossThreads) void balance_partial_kernel(
 }
 
 // Many blocks' sums to kFold of them: line y adds blocks y, y + kFold, ...
+// They go on as f32, half a step of 2^-24 each, as the blocks' own sums are:
+// the last kernel reads one format whether they were folded or not.
 constexpr int kFold = 16;
 __global__ __launch_bounds__(kWave) void balance_fold_kernel(const float2* __restrict__ part,
                                                              int nblk, int E,
@@ -312,8 +314,10 @@ __global__ __launch_bounds__(kGradThreads) void route_backward_kernel(
   constexpr int kGroups = kGradThreads / L;
   // The selected experts' terms of each lane group's token, else zeros. Only
   // the group's own wave uses its row, and a wave's LDS accesses run in
-  // order; an expert that a token holds twice is added to twice by one
-  // instruction, lane after lane, so the order is fixed.
+  // order. An expert that a token holds twice is added to twice by one
+  // instruction: the sum is the same either way round. Three times and more
+  // the lanes' order counts, which the hardware keeps from run to run (seen
+  // with experts held up to 32 times, not promised by a document).
   __shared__ __align__(16) float picked[kGroups][L * EPL];
   const int q = threadIdx.x & (L - 1);
   const int grp = threadIdx.x / L;
