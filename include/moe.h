@@ -190,6 +190,8 @@ moe_status_t moe_slot_map(const int32_t* ids, const float* w, int T, int K, int 
  * moe_permute_workspace_size() bytes (per-chunk slot histograms; contents on
  * entry are ignored).
  * x_perm may be NULL to compute only the index arrays.
+ * T * K and the pairs of one chunk (T * K * S / 65536, and at least 512)
+ * together stay under 2^31 - 1024 (MOE_ERR_UNSUPPORTED otherwise).
  */
 size_t moe_permute_workspace_size(int T, int K, int S);
 

@@ -358,6 +358,8 @@ struct PermutePlan {
   size_t ws_bytes;
 };
 PermutePlan permute_plan(int T, int K, int S);
+// Whether the permutation's 32-bit pair indices hold T * K pairs.
+bool permute_fits(int T, int K, int S);
 // Entries of the static histogram array behind moe_permute_noalloc (256 KiB
 // per device): permute_plan never needs more than 65536 / S chunks of S.
 constexpr int kPermuteScratchInts = 65536;

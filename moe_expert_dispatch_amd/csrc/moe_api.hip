@@ -73,7 +73,7 @@ moe_status_t check_permute(const void* x, moe_dtype_t dt, int T, int H, int K,
                            size_t ws_bytes) {
   if (T < 0 || K < 1 || S < 1 || H < 1) return MOE_ERR_INVALID_ARG;
   if (!dtype_ok(dt)) return MOE_ERR_UNSUPPORTED;
-  if (S > MOE_MAX_SLOTS || K > MOE_MAX_TOPK || H % 8 != 0 || !pairs_fit(T, K))
+  if (S > MOE_MAX_SLOTS || K > MOE_MAX_TOPK || H % 8 != 0 || !permute_fits(T, K, S))
     return MOE_ERR_UNSUPPORTED;
   if (!offsets) return MOE_ERR_INVALID_ARG;
   if (T > 0 && (!slot || !mask || !sorted_pairs || !pair_row)) return MOE_ERR_INVALID_ARG;
@@ -253,7 +253,8 @@ moe_status_t check_config(const moe_config_t* c) {
     return MOE_ERR_UNSUPPORTED;
   if (c->E_global > MOE_MAX_EXPERTS || c->K > MOE_MAX_TOPK || c->S > MOE_MAX_SLOTS)
     return MOE_ERR_UNSUPPORTED;
-  if (c->H % 8 != 0 || c->I % 8 != 0 || !pairs_fit(c->T_max, c->K)) return MOE_ERR_UNSUPPORTED;
+  if (c->H % 8 != 0 || c->I % 8 != 0 || !permute_fits(c->T_max, c->K, c->S))
+    return MOE_ERR_UNSUPPORTED;
   if (!weight_panel_ok(c->H, c->I, weight_bytes(c->dtype))) return MOE_ERR_UNSUPPORTED;
   if (c->gemm_blocks < 0) return MOE_ERR_INVALID_ARG;
   const long long P = (long long)c->T_max * c->K;
@@ -315,7 +316,7 @@ moe_status_t moe_slot_map(const int32_t* ids, const float* w, int T, int K, int 
 }
 
 size_t moe_permute_workspace_size(int T, int K, int S) {
-  if (T < 0 || K < 1 || S < 1 || !pairs_fit(T, K)) return 0;
+  if (T < 0 || K < 1 || S < 1 || !permute_fits(T, K, S)) return 0;
   return permute_plan(T, K, S).ws_bytes;
 }
 
@@ -336,6 +337,7 @@ moe_status_t moe_permute_noalloc(const void* x, moe_dtype_t dt, int T, int H, in
                                  void* x_perm, hipStream_t stream) {
   constexpr size_t kScratchBytes = (size_t)kPermuteScratchInts * sizeof(int32_t);
   if (T < 0 || K < 1 || S < 1 || !pairs_fit(T, K)) return MOE_ERR_INVALID_ARG;
+  if (!permute_fits(T, K, S)) return MOE_ERR_UNSUPPORTED;
   if (permute_plan(T, K, S).ws_bytes > kScratchBytes) return MOE_ERR_UNSUPPORTED;
   int32_t* hist = nullptr;
   moe_status_t st = permute_scratch(&hist);

@@ -293,15 +293,23 @@ PermutePlan permute_plan(int T, int K, int S) {
   // histograms stay small: each ranking block reads all of them); a chunk is
   // a run of whole tokens, so the block that ranks it can also gather them.
   const int cap = S > 0 ? (65536 / S > 0 ? 65536 / S : 1) : 1;
-  const int units = ceil_div(pl.P, kSub);
+  // (written so that nothing passes 31 bits for any T * K < 2^31)
+  const int units = pl.P > 0 ? (pl.P - 1) / kSub + 1 : 0;
   const int n = units < cap ? units : cap;
-  const int tokens = n > 0 ? ceil_div(T, n) : 1;  // tokens per chunk
+  const int tokens = n > 0 ? (T - 1) / n + 1 : 1;  // tokens per chunk
   pl.chunk = tokens * K;
-  pl.nchunks = pl.P > 0 ? ceil_div(T, tokens) : 0;  // <= n
+  pl.nchunks = pl.P > 0 ? (T - 1) / tokens + 1 : 0;  // <= n
   const int bound = n > 0 ? n : 1;  // min(units, cap), monotone in P
   // histograms, padded to whole 16-byte vectors
   pl.ws_bytes = ((size_t)S * (size_t)bound * sizeof(int32_t) + 15) / 16 * 16;
   return pl;
+}
+
+bool permute_fits(int T, int K, int S) {
+  const int64_t P = (int64_t)T * K;
+  if (P >= (INT64_C(1) << 31)) return false;
+  // the kernels' first pair + chunk, and the steps behind it, in 31 bits
+  return P + permute_plan(T, K, S).chunk + 2 * kSub < (INT64_C(1) << 31);
 }
 
 namespace {

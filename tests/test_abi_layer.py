@@ -172,6 +172,26 @@ def test_balance_loss_workspace_at_the_most_tokens(so):
         assert ws(2 ** 31 - 1, E, K) == ws(2 ** 30, E, K) > ws(64, E, K)
 
 
+@pytest.mark.parametrize("S", [1, 80, 1024])
+def test_permute_refuses_pairs_whose_chunks_pass_31_bits(so, S):
+    """A chunk's end, first pair + chunk, is a 32-bit index: the last chunk of 2^31 - 1 pairs ends behind it."""
+    ws = so.moe_permute_workspace_size
+    small = ws(1 << 30, 1, S)
+    assert small >= 4 * S
+
+    def call(T, K=1, n=0):
+        return so.moe_permute(None, 1, T, 64, K, fake, fake, S, fake, fake, fake, None, fake, ctypes.c_size_t(n), None)
+    for T, K in ((2 ** 31 - 1, 1), (2 ** 31 - 600, 1), ((2 ** 31 - 1) // 7, 7), (2 ** 26 - 1, 32)):
+        assert ws(T, K, S) == 0 and call(T, K, 1 << 40) == UNSUPPORTED
+        assert so.moe_permute_noalloc(None, 1, T, 64, K, fake, fake, S, fake, fake, fake, None, None) != 0
+        cfg = moe.ForwardConfig(T=T, H=32, I=32, E_global=max(K, 1), K=K, renormalize=True, S=max(S, K), dtype=moe.MXFP4)
+        assert so.moe_forward_workspace_size(ctypes.byref(cfg.c_struct())) == 0
+    # the most that is taken: chunks of T / n tokens, n = 65536 / S, and the steps past the end of one
+    n = 65536 // S
+    most = max(T for T in range(2 ** 31 - 2 ** 26, 2 ** 31, 1 << 12) if T + -(-T // n) + 1024 < 2 ** 31)
+    assert ws(most, 1, S) == small and call(most) == WORKSPACE
+
+
 def test_a2a_dispatch_refuses_more_tokens_than_its_grid_holds(so):
     """A block of 256 threads a token, and up to 256 more: 2^32 threads from 2^24 - 256 tokens on."""
     most = (1 << 24) - 257
