@@ -346,8 +346,9 @@ moe_status_t moe_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scale, in
  * the order of the sums depends on max_rows, S, the shape and the device's
  * number of compute units, not on the scheduling (in moe_forward on T * K,
  * ep_size and E_global in place of max_rows). A weight whose scale byte is 255 makes its outputs NaN, one past
- * bf16's range (scale bytes 253 and 254 with large codes) not finite. The
- * other rules are those of moe_grouped_gemm; w_scale is 16-byte aligned.
+ * bf16's range (scale bytes 253 and 254 with large codes) not finite.
+ * max_rows < 2^31 - 1024. The other rules are those of moe_grouped_gemm;
+ * w_scale is 16-byte aligned.
  */
 moe_status_t moe_grouped_gemm_mxfp4(moe_gemm_op_t op, const void* a, const int32_t* offsets,
                                     int S, int max_rows, const uint8_t* w,

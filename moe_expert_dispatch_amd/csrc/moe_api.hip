@@ -606,6 +606,8 @@ moe_status_t moe_grouped_gemm_mxfp4(moe_gemm_op_t op, const void* a, const int32
       check_gemm(op, MOE_DTYPE_BF16, a, offsets, S, max_rows, w, H, I, c, 1);
   if (st != MOE_OK) return st;
   if (H % 32 != 0 || I % 32 != 0 || !dtype_ok(c_dt)) return MOE_ERR_UNSUPPORTED;
+  // tiles step up to 160 rows past a slot's last one, in 32-bit indices
+  if (max_rows >= 0x7fffffff - 1023) return MOE_ERR_UNSUPPORTED;
   if (op == MOE_GEMM_GATE_UP_SWIGLU && c_dt != MOE_DTYPE_BF16) return MOE_ERR_UNSUPPORTED;
   if (max_rows > 0 && (!w_scale || !aligned16(w_scale))) return MOE_ERR_INVALID_ARG;
   return launch_gemm_mxfp4(op, a, nullptr, 1, offsets, S, max_rows, max_rows, w, w_scale, H, I, c,

@@ -121,6 +121,16 @@ def test_grouped_gemm_mxfp4_validation(so):
     assert call(rows=0, H=32768, I=32768) == UNSUPPORTED  # the weight-panel limit, one byte a weight
 
 
+def test_grouped_gemm_mxfp4_refuses_rows_whose_tiles_pass_31_bits(so):
+    """Tiles step past a slot's last row by up to 160 rows, in 32-bit indices. The check behind this one (no scales)
+    refuses the rest without a launch."""
+    def call(rows):
+        return so.moe_grouped_gemm_mxfp4(1, fake, fake, 4, rows, fake, None, 64, 64, fake, 1, None)
+    for rows in (2 ** 31 - 1, 2 ** 31 - 1024):
+        assert call(rows) == UNSUPPORTED
+    assert call(2 ** 31 - 1025) == INVALID
+
+
 def _cfg(**kw):
     base = dict(T=16, H=64, I=64, E_global=8, K=2, renormalize=True, S=8, dtype=moe.MXFP4)
     base.update(kw)
