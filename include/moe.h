@@ -286,9 +286,9 @@ moe_status_t moe_grouped_gemm(moe_gemm_op_t op, moe_dtype_t dt, const void* a,
 /*
  * moe_quantize_fp8 -- q[i] = quantize(x[i], scale) for i < n.
  * x of x_dt (MOE_DTYPE_BF16 or MOE_DTYPE_F32) and q (bytes) are device
- * buffers, 16-byte aligned; scale must be finite and > 2^-128 (as
- * every scale that codes are made with). x must hold
- * finite values (a NaN input gives an unspecified code).
+ * buffers, 16-byte aligned; scale must be finite and > 2^-128, where f32 holds
+ * its reciprocal (as every scale that codes are made with). x must hold finite
+ * values (a NaN input gives an unspecified code).
  */
 moe_status_t moe_quantize_fp8(const void* x, moe_dtype_t x_dt, int64_t n, float scale,
                               uint8_t* q, hipStream_t stream);
@@ -345,10 +345,10 @@ moe_status_t moe_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scale, in
  * (a code times its scale is a bf16 value), sums f32, one rounding to c_dt;
  * the order of the sums depends on max_rows, S, the shape and the device's
  * number of compute units, not on the scheduling (in moe_forward on T * K,
- * ep_size and E_global in place of max_rows). A weight whose scale byte is 255 makes its outputs NaN, one past
- * bf16's range (scale bytes 253 and 254 with large codes) not finite.
- * max_rows < 2^31 - 1024. The other rules are those of moe_grouped_gemm;
- * w_scale is 16-byte aligned.
+ * ep_size, and for up to 64 pairs E_global, in place of max_rows). A weight
+ * whose scale byte is 255 makes its outputs NaN, one past bf16's range (scale
+ * bytes 253 and 254 with large codes) not finite. max_rows < 2^31 - 1024. The
+ * other rules are those of moe_grouped_gemm; w_scale is 16-byte aligned.
  */
 moe_status_t moe_grouped_gemm_mxfp4(moe_gemm_op_t op, const void* a, const int32_t* offsets,
                                     int S, int max_rows, const uint8_t* w,

@@ -967,8 +967,9 @@ __global__ __launch_bounds__(512) void mxfp4_pair_down_kernel(
 // more, and max_rows bounds them all: a caller's capacity far over the rows
 // there are takes the kernel of the capacity). Slots far over the average are
 // right in every kernel, but in the streaming ones a block reads its codes
-// again for every RB rows. Measured with rows drawn evenly. Both sides in us at 64 slots, Kd = 4096 / N = 1024
-// gate/up and Kd = 1024 / N = 4096 down: 16 rows a slot 71 and 42 streamed
+// again for every RB rows. Measured with rows drawn evenly. Both sides in us at
+// 64 slots, Kd = 4096 / N = 1024 gate/up and Kd = 1024 / N = 4096 down: 16 rows a
+// slot 71 and 42 streamed
 // (16 rows at a time), 88 and 45 split, but a slot past 16 streams its codes
 // twice (12 rows a slot on the average already have one in six past it); at 31
 // 88 and 46 split, but past 32 twice; at 64 113 split by 64 rows, 137 in tiles.

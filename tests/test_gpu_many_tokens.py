@@ -54,6 +54,24 @@ def test_route(T, E, groups):
     _free()
 
 
+def test_route_and_slot_map_of_the_most_pairs():
+    """2^31 - 1 pairs: the last index is the last that 31 bits hold."""
+    dev = device()
+    _need(60)
+    T = 2 ** 31 - 1
+    announce(f"route and slot map T={T}")
+    part = torch.randn(PERIOD, 1, generator=torch.Generator().manual_seed(6)).to(dev)
+    logits = _repeat(part, T)
+    ids, w = moe.route(logits, 1, False)
+    del logits
+    assert not ids.any() and bool((w == 1).all())
+    w.view(-1)[-1] = 0.5
+    slot, wm, mask = moe.slot_map(ids, w, 1)
+    assert not slot.any() and torch.equal(wm, w) and bool((mask == 1).all())
+    del ids, w, slot, wm, mask
+    _free()
+
+
 def test_combine():
     dev = device()
     _need(16)
