@@ -377,6 +377,48 @@ moe_status_t moe_rms_norm(const void* x, const void* residual, const void* gamma
                           float q_scale, hipStream_t stream);
 
 /*
+ * moe_layer_norm -- layer norm, with moe_rms_norm's options.
+ *   h = x + residual in f32 (residual NULL: h = x); residual_out = round(h);
+ *   v = (h - mean(h)) / sqrt(mean((h - mean(h))^2) + eps) * gamma + beta;
+ *   y = round(v);  q = quantize(v, q_scale).
+ * beta [H] of dt, or NULL: 0. Everything else as moe_rms_norm: the limits, what
+ * may be NULL, the overlaps allowed, rows whose squares leave f32's range. The
+ * mean is corrected by the deviations' own, so that rows far from 0 beside
+ * their deviation keep f32's accuracy. A row of equal values with eps = 0 has
+ * unspecified outputs.
+ *
+ * moe_rms_norm_backward, moe_layer_norm_backward -- their gradients.
+ *   n = the normalised row (v without gamma and beta), r = 1 / its root,
+ *   g = dy * gamma;
+ *   RMS:   dx = round(r (g - n mean(g n)) + dresidual)
+ *   layer: dx = round(r (g - mean(g) - n mean(g n)) + dresidual)
+ *   dgamma = sum over rows of dy * n,  dbeta = sum over rows of dy.
+ * x [T, H]: the row that was normalised: the forward pass's x, or its
+ * residual_out where it added a residual (dx is then the gradient of both
+ * addends). dy, dresidual [T, H]: gradients that arrive through y and through
+ * residual_out (dresidual NULL: 0). All of dt; dgamma, dbeta [H] f32, written
+ * whole (zeros for T = 0). dx, dgamma and dbeta may be NULL, but not all. dx
+ * may be dy, x or dresidual itself; no other overlap. The order of the sums
+ * depends on T and H alone. dy, gamma and their product must be finite and
+ * leave room in f32 for a row's sum; the rows as for the norm.
+ * ws: 16-byte aligned, at least moe_norm_backward_workspace_size(T, H) bytes,
+ * contents ignored (may be NULL where that is 0 or dgamma and dbeta are).
+ */
+moe_status_t moe_layer_norm(const void* x, const void* residual, const void* gamma,
+                            const void* beta, moe_dtype_t dt, int T, int H, float eps,
+                            void* residual_out, void* y, uint8_t* q, float q_scale,
+                            hipStream_t stream);
+size_t moe_norm_backward_workspace_size(int T, int H);
+moe_status_t moe_rms_norm_backward(const void* dy, const void* x, const void* gamma,
+                                   const void* dresidual, moe_dtype_t dt, int T, int H, float eps,
+                                   void* dx, float* dgamma, void* ws, size_t ws_bytes,
+                                   hipStream_t stream);
+moe_status_t moe_layer_norm_backward(const void* dy, const void* x, const void* gamma,
+                                     const void* dresidual, moe_dtype_t dt, int T, int H,
+                                     float eps, void* dx, float* dgamma, float* dbeta, void* ws,
+                                     size_t ws_bytes, hipStream_t stream);
+
+/*
  * moe_balance_loss -- the router's balance loss with its per-expert counts.
  *   Source: [EPMASK] module docstring (the global top-k ids every rank
  *   computes are what the counts count); [SLOTS] Description (per-expert load
@@ -449,6 +491,86 @@ moe_status_t moe_combine_shared(const void* y, moe_dtype_t y_dt, const int32_t* 
                                 const float* w_masked, int T, int K, int H, const void* shared,
                                 moe_dtype_t shared_dt, void* out, moe_dtype_t out_dt,
                                 int accumulate, hipStream_t stream);
+
+/*
+ * moe_combine_backward -- gradient of moe_combine (and of moe_combine_shared,
+ * whose shared input has dout itself as its gradient).
+ *   dy[pair_row[p]] = round(w_masked[p] * dout[t]),  p = t*K + k
+ *   dw[p] = <dout[t], y[pair_row[p]]>, 0 for a pair without a row
+ * dout [T, H] of dout_dt; y and dy [rows, H] of y_dt; w_masked [T, K] or NULL
+ * (weight 1); dw [T, K] f32. The products and sums are f32, in an order that
+ * depends on H and K alone. dy or dw may be NULL, but not both; y is read for
+ * dw only (may be NULL without it). Rows that no pair has stay as they are. No
+ * row may belong to two pairs (moe_permute gives none to two); dy must not
+ * overlap an input. dw with -1 rows dropped is what moe_route_backward takes.
+ * K <= MOE_MAX_TOPK, H % 8 == 0, H < 2^24; dout, y and dy 16-byte aligned.
+ *
+ * moe_permute_backward -- gradient of moe_permute (pair_w NULL) and of
+ * moe_permute_scaled.
+ *   dx[t] = round(sum over k with pair_row[p] >= 0 of pair_w[p] * dx_perm[pair_row[p]])
+ *   dpair_w[p] = <dx_perm[pair_row[p]], x[t]>, 0 for a pair without a row
+ * dx_perm [rows, H] and x [T, H] of dt; dx [T, H] of dx_dt; accumulate as in
+ * moe_combine; dpair_w [T, K] f32, or NULL (x is then not read). dpair_w needs
+ * pair_w. dx must not overlap an input. Limits as moe_combine_backward.
+ */
+moe_status_t moe_combine_backward(const void* dout, moe_dtype_t dout_dt, const void* y,
+                                  moe_dtype_t y_dt, const int32_t* pair_row,
+                                  const float* w_masked, int T, int K, int H, void* dy, float* dw,
+                                  hipStream_t stream);
+moe_status_t moe_permute_backward(const void* dx_perm, moe_dtype_t dt, const int32_t* pair_row,
+                                  const float* pair_w, const void* x, int T, int K, int H,
+                                  void* dx, moe_dtype_t dx_dt, int accumulate, float* dpair_w,
+                                  hipStream_t stream);
+
+/*
+ * The experts' training pass. A forward pass that is to be differentiated
+ * keeps the gate/up product h [rows, 2I] before its SwiGLU:
+ *   h   = moe_grouped_gemm(MOE_GEMM_DOWN, .., w_gate_up, H = 2I, I = H)
+ *   act = moe_swiglu(h),  y = moe_grouped_gemm(MOE_GEMM_DOWN, act, .., w_down)
+ * and from dy (moe_combine_backward):
+ *   dh       = moe_grouped_gemm_backward(MOE_GEMM_DOWN, dy, w_down, h)
+ *   dx_perm  = moe_grouped_gemm_backward(MOE_GEMM_GATE_UP_SWIGLU, dh, w_gate_up)
+ *   dw_down  = moe_grouped_gemm_weight_grad(dy, act)
+ *   dw_gate_up = moe_grouped_gemm_weight_grad(dh, x_perm)
+ * Rows of slot s are offsets[s] .. offsets[s+1], as in moe_grouped_gemm;
+ * rows behind the last slot's are neither read nor written. max_rows < 2^31 -
+ * 1024. Products of bf16 values are exact, sums f32, one rounding at the end
+ * (dt MOE_DTYPE_F32: f32 products and sums on the matrix cores). The orders of
+ * the sums depend on shapes alone, not on the scheduling. Buffers 16-byte
+ * aligned, H % 8 == 0, I % 8 == 0; no output may overlap an input.
+ *
+ * moe_swiglu -- act[r, j] = silu(h[r, j]) * h[r, I + j], one rounding.
+ *
+ * moe_grouped_gemm_backward -- the rows' gradient of a grouped product.
+ * op == MOE_GEMM_GATE_UP_SWIGLU: dc [rows, 2I] (gradient of h, before the
+ *   SwiGLU), w [S, 2I, H]: out [rows, H], out[r] = dc[r] w[s].
+ * op == MOE_GEMM_DOWN: dc [rows, H], w [S, H, I]: da[r] = dc[r] w[s]; h NULL:
+ *   out = da [rows, I]; else h [rows, 2I] = [g, u] and out [rows, 2I] is the
+ *   gradient of h: [da u s(g) (1 + g (1 - s(g))), da g s(g)], s the sigmoid, da
+ *   not rounded in between. h with MOE_GEMM_GATE_UP_SWIGLU: MOE_ERR_INVALID_ARG.
+ * A slot's w is under 2^31 bytes.
+ *
+ * moe_grouped_gemm_weight_grad -- the weights' gradient of a grouped product.
+ *   dw[s] = sum over the rows r of slot s of dc[r]^T a[r]     (dw [S, N, Kd])
+ * dc [rows, N], a [rows, Kd] of dt; dw of dw_dt (f32 or bf16). Slots without
+ * rows get zeros. accumulate != 0: dw += in f32, then the rounding. N and Kd
+ * are multiples of 8 under 2^20. With few tiles and many rows a slot's rows are
+ * split, the parts' f32 sums held in ws: 16-byte aligned, at least
+ * moe_grouped_gemm_weight_grad_workspace_size(..) bytes (often 0; then ws may
+ * be NULL), contents ignored.
+ */
+moe_status_t moe_swiglu(const void* h, moe_dtype_t dt, const int32_t* offsets, int S,
+                        int max_rows, int I, void* act, hipStream_t stream);
+moe_status_t moe_grouped_gemm_backward(moe_gemm_op_t op, moe_dtype_t dt, const void* dc,
+                                       const int32_t* offsets, int S, int max_rows, const void* w,
+                                       int H, int I, const void* h, void* out,
+                                       hipStream_t stream);
+size_t moe_grouped_gemm_weight_grad_workspace_size(moe_dtype_t dt, int S, int max_rows, int N,
+                                                   int Kd);
+moe_status_t moe_grouped_gemm_weight_grad(moe_dtype_t dt, const void* dc, const void* a,
+                                          const int32_t* offsets, int S, int max_rows, int N,
+                                          int Kd, void* dw, moe_dtype_t dw_dt, int accumulate,
+                                          void* ws, size_t ws_bytes, hipStream_t stream);
 
 /*
  * Fused forward: one call enqueues every stage in order on one stream.

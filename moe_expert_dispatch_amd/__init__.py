@@ -27,6 +27,9 @@ __all__ = [
     "a2a_dispatch", "a2a_dispatch_workspace_size", "a2a_combine",
     "rms_norm", "balance_loss", "balance_loss_workspace_size", "route_backward",
     "MXFP4", "quantize_mxfp4", "dequantize_mxfp4", "grouped_gemm_mxfp4",
+    "layer_norm", "layer_norm_backward", "rms_norm_backward", "norm_backward_workspace_size",
+    "combine_backward", "permute_backward", "swiglu", "grouped_gemm_backward",
+    "grouped_gemm_weight_grad", "grouped_gemm_weight_grad_workspace_size",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -104,6 +107,20 @@ _SIGS = {
     "moe_rms_norm": (_i, [_p, _p, _p, _i, _i, _i, ctypes.c_float, _p, _p, _p, ctypes.c_float, _p]),
     "moe_balance_loss_workspace_size": (_sz, [_i, _i, _i]),
     "moe_balance_loss": (_i, [_p, _p, _p, _i, _i, _i, ctypes.c_float, _p, _p, _p, _p, _sz, _p]),
+    "moe_layer_norm": (_i, [_p, _p, _p, _p, _i, _i, _i, ctypes.c_float, _p, _p, _p,
+                            ctypes.c_float, _p]),
+    "moe_norm_backward_workspace_size": (_sz, [_i, _i]),
+    "moe_rms_norm_backward": (_i, [_p, _p, _p, _p, _i, _i, _i, ctypes.c_float, _p, _p, _p, _sz,
+                                   _p]),
+    "moe_layer_norm_backward": (_i, [_p, _p, _p, _p, _i, _i, _i, ctypes.c_float, _p, _p, _p, _p,
+                                     _sz, _p]),
+    "moe_combine_backward": (_i, [_p, _i, _p, _i, _p, _p, _i, _i, _i, _p, _p, _p]),
+    "moe_permute_backward": (_i, [_p, _i, _p, _p, _p, _i, _i, _i, _p, _i, _i, _p, _p]),
+    "moe_swiglu": (_i, [_p, _i, _p, _i, _i, _i, _p, _p]),
+    "moe_grouped_gemm_backward": (_i, [_i, _i, _p, _p, _i, _i, _p, _i, _i, _p, _p, _p]),
+    "moe_grouped_gemm_weight_grad_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
+    "moe_grouped_gemm_weight_grad": (_i, [_i, _p, _p, _p, _i, _i, _i, _i, _p, _i, _i, _p, _sz,
+                                          _p]),
     "moe_route_backward": (_i, [_p, _p, _p, _p, _p, _p, _i, _i, _i, _i, ctypes.c_float, _p, _p]),
 }
 EXPORTED_SYMBOLS = tuple(_SIGS)
@@ -504,6 +521,95 @@ def rms_norm(x: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-6,
     return y, residual_out, q
 
 
+def layer_norm(x: torch.Tensor, gamma: torch.Tensor, beta: Optional[torch.Tensor] = None,
+               eps: float = 1e-5, residual: Optional[torch.Tensor] = None,
+               q_scale: Optional[float] = None, y: Optional[torch.Tensor] = None,
+               residual_out: Optional[torch.Tensor] = None, q: Optional[torch.Tensor] = None
+               ) -> Tuple[torch.Tensor, Optional[torch.Tensor], Optional[torch.Tensor]]:
+    """moe_layer_norm -> (y [T, H], residual_out [T, H] or None, q codes [T, H] uint8 or None).
+
+    As rms_norm, with the mean taken out and beta [H] (None: 0) added."""
+    _dev(x, "x", (torch.float32, torch.bfloat16))
+    if x.dim() != 2:
+        raise ValueError("x must be [T, H]")
+    T, H = x.shape
+    _dev(gamma, "gamma", x.dtype, (H,))
+    if beta is not None:
+        _dev(beta, "beta", x.dtype, (H,))
+    if residual is not None:
+        _dev(residual, "residual", x.dtype, (T, H))
+        residual_out = (torch.empty_like(x) if residual_out is None
+                        else _dev(residual_out, "residual_out", x.dtype, (T, H)))
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    if q_scale is not None:
+        q = (torch.empty_like(x, dtype=torch.uint8) if q is None else _dev(q, "q", _CODES, (T, H)))
+    elif q is not None:
+        raise ValueError("q needs a q_scale")
+    y = torch.empty_like(x) if y is None else _dev(y, "y", x.dtype, (T, H))
+    _launch("moe_layer_norm", x, (gamma, beta, residual, residual_out, y, q), x.data_ptr(),
+            _ptr(residual), gamma.data_ptr(), _ptr(beta), _DT[x.dtype], T, H, eps,
+            _ptr(residual_out), y.data_ptr(), _ptr(q), 0.0 if q_scale is None else q_scale)
+    return y, residual_out, q
+
+
+def norm_backward_workspace_size(T: int, H: int) -> int:
+    return int(lib().moe_norm_backward_workspace_size(T, H))
+
+
+def _norm_backward(what, dy, x, gamma, eps, dresidual, dx, outs, ws):
+    _dev(x, "x", (torch.float32, torch.bfloat16))
+    if x.dim() != 2:
+        raise ValueError("x must be [T, H]")
+    T, H = x.shape
+    _dev(dy, "dy", x.dtype, (T, H))
+    _dev(gamma, "gamma", x.dtype, (H,))
+    if dresidual is not None:
+        _dev(dresidual, "dresidual", x.dtype, (T, H))
+    dx = torch.empty_like(x) if dx is None else _dev(dx, "dx", x.dtype, (T, H))
+    if ws is None:
+        ws = _empty((norm_backward_workspace_size(T, H),), torch.uint8, x)
+    _launch(what, x, (dy, gamma, dresidual, dx, *outs, ws), dy.data_ptr(), x.data_ptr(),
+            gamma.data_ptr(), _ptr(dresidual), _DT[x.dtype], T, H, eps, dx.data_ptr(),
+            *(o.data_ptr() for o in outs), ws.data_ptr(), ws.numel() * ws.element_size())
+    return dx
+
+
+def _column_sums(x: torch.Tensor, t: Optional[torch.Tensor], name: str) -> torch.Tensor:
+    H = x.shape[-1]
+    return _empty((H,), torch.float32, x) if t is None else _dev(t, name, torch.float32, (H,))
+
+
+def rms_norm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-6,
+                      dresidual: Optional[torch.Tensor] = None,
+                      dx: Optional[torch.Tensor] = None, dgamma: Optional[torch.Tensor] = None,
+                      ws: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """moe_rms_norm_backward -> (dx [T, H], dgamma [H] f32).
+
+    dy is the gradient of rms_norm's y; x its input, or its residual_out where it added a
+    residual, whose gradient dresidual is then added (dx is the gradient of both addends). dx may
+    be dy, x or dresidual itself."""
+    _dev(x, "x", (torch.float32, torch.bfloat16))
+    dgamma = _column_sums(x, dgamma, "dgamma")
+    dx = _norm_backward("moe_rms_norm_backward", dy, x, gamma, eps, dresidual, dx, (dgamma,), ws)
+    return dx, dgamma
+
+
+def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-5,
+                        dresidual: Optional[torch.Tensor] = None,
+                        dx: Optional[torch.Tensor] = None, dgamma: Optional[torch.Tensor] = None,
+                        dbeta: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None
+                        ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """moe_layer_norm_backward -> (dx [T, H], dgamma [H] f32, dbeta [H] f32); arguments as
+    rms_norm_backward."""
+    _dev(x, "x", (torch.float32, torch.bfloat16))
+    dgamma = _column_sums(x, dgamma, "dgamma")
+    dbeta = _column_sums(x, dbeta, "dbeta")
+    dx = _norm_backward("moe_layer_norm_backward", dy, x, gamma, eps, dresidual, dx,
+                        (dgamma, dbeta), ws)
+    return dx, dgamma, dbeta
+
+
 # ---------------------------------------------------------------- the router's training step
 def _router_inputs(logits, ids, token_mask) -> Tuple[int, int, int]:
     _dev(logits, "logits", torch.float32)
@@ -599,6 +705,188 @@ def combine(y: torch.Tensor, pair_row: torch.Tensor, w_masked: Optional[torch.Te
                                  H, _ptr(out), _DT[out.dtype], int(bool(accumulate)),
                                  _stream()), "moe_combine")
     return out
+
+
+# ---------------------------------------------------------------- the layer's training step
+def _pair_rows(pair_row, K: int) -> int:
+    _dev(pair_row, "pair_row", torch.int32)
+    if K < 1 or pair_row.numel() % K != 0:
+        raise ValueError("pair_row must hold T*K entries")
+    return pair_row.numel() // K
+
+
+def combine_backward(dout: torch.Tensor, y: Optional[torch.Tensor], pair_row: torch.Tensor,
+                     w_masked: Optional[torch.Tensor], K: int,
+                     dy: Optional[torch.Tensor] = None, dw: Optional[torch.Tensor] = None
+                     ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """moe_combine_backward -> (dy [rows, H] of y's dtype, dw [T, K] f32).
+
+    dout [T, H] is the gradient of combine's out, y [rows, H] the rows that it summed. dw is None
+    without weights, where y may be None too (a dy is needed then). Rows of dy that no pair has
+    are not written."""
+    T = _pair_rows(pair_row, K)
+    _dev(dout, "dout", (torch.float32, torch.bfloat16))
+    if dout.dim() != 2 or dout.shape[0] != T:
+        raise ValueError("dout must be [T, H] with T*K entries in pair_row")
+    H = dout.shape[1]
+    for t, name in ((y, "y"), (dy, "dy")):
+        if t is not None:
+            _dev(t, name, (torch.float32, torch.bfloat16))
+            if t.dim() != 2 or t.shape[1] != H:
+                raise ValueError(f"{name} must be [rows, H]")
+    if y is not None:
+        dy = torch.empty_like(y) if dy is None else _dev(dy, "dy", y.dtype, tuple(y.shape))
+    elif dy is None:
+        raise ValueError("dy is needed where there is no y")
+    if w_masked is not None:
+        _dev(w_masked, "w_masked", torch.float32)
+        if w_masked.numel() != T * K:
+            raise ValueError("w_masked must hold T*K entries")
+        if y is None:
+            raise ValueError("the weights' gradient needs y")
+        dw = (_empty((T, K), torch.float32, dout) if dw is None
+              else _dev(dw, "dw", torch.float32, (T, K)))
+    elif dw is not None:
+        raise ValueError("dw needs w_masked")
+    if dy.shape[0] == 0:  # a share without pairs: an empty tensor has no address to pass
+        return dy, None if dw is None else dw.zero_()
+    _launch("moe_combine_backward", dout, (y, pair_row, w_masked, dy, dw), dout.data_ptr(),
+            _DT[dout.dtype], _ptr(y), _DT[dy.dtype], pair_row.data_ptr(), _ptr(w_masked), T, K, H,
+            dy.data_ptr(), _ptr(dw))
+    return dy, dw
+
+
+def permute_backward(dx_perm: torch.Tensor, pair_row: torch.Tensor, K: int,
+                     pair_w: Optional[torch.Tensor] = None, x: Optional[torch.Tensor] = None,
+                     dx: Optional[torch.Tensor] = None, dx_dtype: Optional[torch.dtype] = None,
+                     accumulate: bool = False, dpair_w: Optional[torch.Tensor] = None
+                     ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """moe_permute_backward -> (dx [T, H], dpair_w [T, K] f32 or None).
+
+    dx_perm [rows, H] is the gradient of permute's rows. With pair_w [T, K] (rows that carry
+    their weight) and x [T, H] dpair_w is the weights' gradient; without x it is None. accumulate
+    adds to dx, which must be given."""
+    T = _pair_rows(pair_row, K)
+    _dev(dx_perm, "dx_perm", (torch.float32, torch.bfloat16))
+    if dx_perm.dim() != 2:
+        raise ValueError("dx_perm must be [rows, H]")
+    H = dx_perm.shape[1]
+    if pair_w is not None:
+        _dev(pair_w, "pair_w", torch.float32)
+        if pair_w.numel() != T * K:
+            raise ValueError("pair_w must hold T*K entries")
+    if x is not None:
+        if pair_w is None:
+            raise ValueError("the weights' gradient needs pair_w")
+        _dev(x, "x", dx_perm.dtype, (T, H))
+        dpair_w = (_empty((T, K), torch.float32, dx_perm) if dpair_w is None
+                   else _dev(dpair_w, "dpair_w", torch.float32, (T, K)))
+    elif dpair_w is not None:
+        raise ValueError("dpair_w needs x")
+    if dx is None:
+        if accumulate:
+            raise ValueError("accumulate needs dx")
+        dx = _empty((T, H), dx_dtype or dx_perm.dtype, dx_perm)
+    else:
+        _dev(dx, "dx", (torch.float32, torch.bfloat16), (T, H))
+    if dx_perm.shape[0] == 0:
+        return dx if accumulate else dx.zero_(), None if dpair_w is None else dpair_w.zero_()
+    _launch("moe_permute_backward", dx_perm, (pair_row, pair_w, x, dx, dpair_w),
+            dx_perm.data_ptr(), _DT[dx_perm.dtype], pair_row.data_ptr(), _ptr(pair_w), _ptr(x), T,
+            K, H, dx.data_ptr(), _DT[dx.dtype], 1 if accumulate else 0, _ptr(dpair_w))
+    return dx, dpair_w
+
+
+def _slots(offsets) -> int:
+    _dev(offsets, "offsets", torch.int32)
+    if offsets.dim() != 1 or offsets.numel() < 2:
+        raise ValueError("offsets must have S + 1 entries")
+    return offsets.numel() - 1
+
+
+def swiglu(h: torch.Tensor, offsets: torch.Tensor, act: Optional[torch.Tensor] = None
+           ) -> torch.Tensor:
+    """moe_swiglu: h [rows, 2I] (gate, up) -> act [rows, I]; rows behind offsets[S] are not
+    written. h is grouped_gemm(DOWN, x_perm, offsets, w_gate_up)."""
+    _dev(h, "h", (torch.float32, torch.bfloat16))
+    S = _slots(offsets)
+    if h.dim() != 2 or h.shape[1] % 2:
+        raise ValueError("h must be [rows, 2I]")
+    rows, I = h.shape[0], h.shape[1] // 2
+    act = (_empty((rows, I), h.dtype, h) if act is None
+           else _dev(act, "act", h.dtype, (rows, I)))
+    _launch("moe_swiglu", h, (offsets, act), h.data_ptr(), _DT[h.dtype], offsets.data_ptr(), S,
+            rows, I, act.data_ptr())
+    return act
+
+
+def grouped_gemm_backward(op: int, dc: torch.Tensor, offsets: torch.Tensor, w: torch.Tensor,
+                          h: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None
+                          ) -> torch.Tensor:
+    """moe_grouped_gemm_backward, the rows' gradient. GATE_UP_SWIGLU: dc [rows, 2I] (gradient of
+    h), w [S, 2I, H] -> [rows, H]. DOWN: dc [rows, H], w [S, H, I] -> [rows, I], or with h
+    [rows, 2I] (swiglu's input) -> its gradient [rows, 2I]. Rows behind offsets[S] are not
+    written."""
+    _dev(dc, "dc", (torch.float32, torch.bfloat16))
+    _dev(w, "w", dc.dtype)
+    S = _slots(offsets)
+    if dc.dim() != 2 or w.dim() != 3 or w.shape[0] != S or w.shape[1] != dc.shape[1]:
+        raise ValueError("dc must be [rows, N] and w [S, N, K] with S + 1 offsets")
+    rows = dc.shape[0]
+    if op == GATE_UP_SWIGLU:
+        if w.shape[1] % 2:
+            raise ValueError("w must be [S, 2I, H]")
+        if h is not None:
+            raise ValueError("h belongs to DOWN")
+        H, I, cols = w.shape[2], w.shape[1] // 2, w.shape[2]
+    elif op == DOWN:
+        H, I = w.shape[1], w.shape[2]
+        cols = I if h is None else 2 * I
+    else:
+        raise ValueError("op must be GATE_UP_SWIGLU or DOWN")
+    if h is not None:
+        _dev(h, "h", dc.dtype, (rows, cols))
+    out = (_empty((rows, cols), dc.dtype, dc) if out is None
+           else _dev(out, "out", dc.dtype, (rows, cols)))
+    _launch("moe_grouped_gemm_backward", dc, (offsets, w, h, out), op, _DT[dc.dtype],
+            dc.data_ptr(), offsets.data_ptr(), S, rows, w.data_ptr(), H, I, _ptr(h),
+            out.data_ptr())
+    return out
+
+
+def grouped_gemm_weight_grad_workspace_size(dtype: torch.dtype, S: int, rows: int, N: int, K: int
+                                            ) -> int:
+    return int(lib().moe_grouped_gemm_weight_grad_workspace_size(_DT[dtype], S, rows, N, K))
+
+
+def grouped_gemm_weight_grad(dc: torch.Tensor, a: torch.Tensor, offsets: torch.Tensor,
+                             dw: Optional[torch.Tensor] = None,
+                             dw_dtype: torch.dtype = torch.float32, accumulate: bool = False,
+                             ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """moe_grouped_gemm_weight_grad: dw [S, N, K] (f32 or bf16) of dc [rows, N] and a [rows, K],
+    zeros for slots without rows. accumulate adds to dw, which must be given."""
+    _dev(dc, "dc", (torch.float32, torch.bfloat16))
+    _dev(a, "a", dc.dtype)
+    S = _slots(offsets)
+    if dc.dim() != 2 or a.dim() != 2 or a.shape[0] != dc.shape[0]:
+        raise ValueError("dc must be [rows, N] and a [rows, K]")
+    rows, N, Kd = dc.shape[0], dc.shape[1], a.shape[1]
+    if dw is None:
+        if accumulate:
+            raise ValueError("accumulate needs dw")
+        if dw_dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError(f"dw_dtype {dw_dtype}, expected torch.float32 or torch.bfloat16")
+        dw = _empty((S, N, Kd), dw_dtype, dc)
+    else:
+        _dev(dw, "dw", (torch.float32, torch.bfloat16), (S, N, Kd))
+    if ws is None:
+        need = grouped_gemm_weight_grad_workspace_size(dc.dtype, S, rows, N, Kd)
+        ws = _empty((need,), torch.uint8, dc) if need else None
+    _launch("moe_grouped_gemm_weight_grad", dc, (a, offsets, dw, ws), _DT[dc.dtype],
+            dc.data_ptr(), a.data_ptr(), offsets.data_ptr(), S, rows, N, Kd, dw.data_ptr(),
+            _DT[dw.dtype], 1 if accumulate else 0, _ptr(ws),
+            0 if ws is None else ws.numel() * ws.element_size())
+    return dw
 
 
 # ---------------------------------------------------------------- fused

@@ -452,6 +452,55 @@ moe_status_t launch_rms_norm(const void* x, const void* residual, const void* ga
                              int T, int H, float eps, void* residual_out, void* y, uint8_t* q,
                              float scale, hipStream_t stream);
 
+// Layer norm, with launch_rms_norm's options; beta may be null.
+moe_status_t launch_layer_norm(const void* x, const void* residual, const void* gamma,
+                               const void* beta, bool bf16, int T, int H, float eps,
+                               void* residual_out, void* y, uint8_t* q, float scale,
+                               hipStream_t stream);
+// Gradient of the layer norm (centred) or of the RMS norm. Null dresidual, dx,
+// dgamma and dbeta are left out.
+size_t norm_backward_workspace_bytes(int T, int H);
+moe_status_t launch_norm_backward(bool centred, const void* dy, const void* x, const void* gamma,
+                                  const void* dresidual, bool bf16, int T, int H, float eps,
+                                  void* dx, float* dgamma, float* dbeta, void* ws,
+                                  hipStream_t stream);
+
+// Gradients of launch_combine and of the permutation's rows (null dpair_w: of
+// the rows alone).
+moe_status_t launch_combine_backward(const void* dout, moe_dtype_t dout_dt, const void* y,
+                                     moe_dtype_t y_dt, const int32_t* pair_row,
+                                     const float* w_masked, int T, int K, int H, void* dy,
+                                     float* dw, hipStream_t stream);
+moe_status_t launch_permute_backward(const void* dx_perm, moe_dtype_t dt, const int32_t* pair_row,
+                                     const float* pair_w, const void* x, int T, int K, int H,
+                                     void* dx, moe_dtype_t dx_dt, int accumulate, float* dpair_w,
+                                     hipStream_t stream);
+
+moe_status_t launch_swiglu(const void* h, bool bf16, const int32_t* offsets, int S, int max_rows,
+                           int I, void* act, hipStream_t stream);
+// Rows' gradient of a grouped product with weights w [S, Kd, N]; h non-null:
+// of the SwiGLU's input as well (out [rows, 2N]).
+moe_status_t launch_gemm_backward_bf16(const void* dc, const int32_t* offsets, int S, int max_rows,
+                                       const void* w, int Kd, int N, const void* h, void* out,
+                                       hipStream_t stream);
+moe_status_t launch_gemm_backward_f32(const void* dc, const int32_t* offsets, int S, int max_rows,
+                                      const void* w, int Kd, int N, const void* h, void* out,
+                                      hipStream_t stream);
+// Weights' gradient dw [S, M, N]. Where there are few tiles and many rows, a
+// slot's rows are split in grad_splits() parts that ws [splits, S, M, N] f32
+// holds until they are added up.
+constexpr int kGradTileBf16 = 256, kGradTileF32 = 64;  // rows and columns of a tile
+constexpr int kSplitBlocks = 256, kMaxSplits = 16;
+int grad_splits(int S, int max_rows, int M, int N, int tile);
+moe_status_t launch_gemm_weight_grad_bf16(const void* dc, const void* a, const int32_t* offsets,
+                                          int S, int max_rows, int M, int N, void* dw, bool dw_f32,
+                                          int accumulate, void* ws, hipStream_t stream);
+moe_status_t launch_gemm_weight_grad_f32(const void* dc, const void* a, const int32_t* offsets,
+                                         int S, int max_rows, int M, int N, void* dw, bool dw_f32,
+                                         int accumulate, void* ws, hipStream_t stream);
+moe_status_t launch_fold_splits(const float* part, int splits, size_t n, void* out, bool out_f32,
+                                int accumulate, hipStream_t stream);
+
 // Balance loss with counts [E + 1] and mean probabilities [E]; the gradient
 // of routing weights and loss. Null token_mask: every token is valid.
 size_t balance_workspace_bytes(int T, int E, int K);

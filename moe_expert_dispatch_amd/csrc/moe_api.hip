@@ -266,6 +266,57 @@ moe_status_t check_config(const moe_config_t* c) {
   return MOE_OK;
 }
 
+moe_status_t check_norm(const void* x, const void* gamma, moe_dtype_t dt, int T, int H, float eps) {
+  if (T < 0 || H < 1 || !(eps >= 0.0f && eps <= 3.4e38f)) return MOE_ERR_INVALID_ARG;
+  if (!dtype_ok(dt) || H % 8 != 0 || H > kMaxNormWidth) return MOE_ERR_UNSUPPORTED;
+  if (T > 0 && (!x || !gamma || !aligned16(x) || !aligned16(gamma))) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+moe_status_t norm_backward(bool centred, const void* dy, const void* x, const void* gamma,
+                           const void* dresidual, moe_dtype_t dt, int T, int H, float eps,
+                           void* dx, float* dgamma, float* dbeta, void* ws, size_t ws_bytes,
+                           hipStream_t stream) {
+  const moe_status_t st = check_norm(x, gamma, dt, T, H, eps);
+  if (st != MOE_OK) return st;
+  if ((!dx && !dgamma && !dbeta) || (T > 0 && !dy)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(dy) || !aligned16(dresidual) || !aligned16(dx) || !aligned16(dgamma) ||
+      !aligned16(dbeta))
+    return MOE_ERR_INVALID_ARG;
+  if (dgamma && dgamma == dbeta) return MOE_ERR_INVALID_ARG;
+  if (dgamma || dbeta) {
+    const size_t need = norm_backward_workspace_bytes(T, H);
+    if (need > 0 && (!ws || ws_bytes < need)) return MOE_ERR_WORKSPACE;
+    if (!aligned16(ws)) return MOE_ERR_INVALID_ARG;
+  }
+  return launch_norm_backward(centred, dy, x, gamma, dresidual, dt == MOE_DTYPE_BF16, T, H, eps,
+                              dx, dgamma, dbeta, ws, stream);
+}
+
+// Rows of the dispatch's gradients: their byte offsets and resources are 32 bits.
+constexpr int kMaxRowWidth = (1 << 24) - 1;
+
+// Widths of the experts' gradients (rows of 2 * width values, tiles of 256 rows).
+constexpr int kMaxGradWidth = (1 << 20) - 1;
+
+moe_status_t check_grad(moe_dtype_t dt, const int32_t* offsets, int S, int max_rows, int N, int Kd) {
+  if (S < 1 || max_rows < 0 || N < 1 || Kd < 1) return MOE_ERR_INVALID_ARG;
+  if (!dtype_ok(dt)) return MOE_ERR_UNSUPPORTED;
+  if (S > MOE_MAX_SLOTS || N % 8 != 0 || Kd % 8 != 0 || N > kMaxGradWidth || Kd > kMaxGradWidth ||
+      (long long)max_rows >= (1LL << 31) - 1024)
+    return MOE_ERR_UNSUPPORTED;
+  if (!offsets) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+int grad_tile(moe_dtype_t dt) { return dt == MOE_DTYPE_BF16 ? kGradTileBf16 : kGradTileF32; }
+
+// Tiles of [M, N] in 31 bits, `times` of them.
+bool tiles_fit(int64_t times, int M, int N, int tile) {
+  const int64_t most = (int64_t{1} << 31) - 1 - (1 << 20);  // a block's step past the last
+  return times * ceil_div(M, tile) <= most / ceil_div(N, tile);
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -693,6 +744,137 @@ moe_status_t moe_a2a_combine(const void* partial, moe_dtype_t partial_dt,
   if (T > 0 && (!aligned16(partial) || !aligned16(out))) return MOE_ERR_INVALID_ARG;
   return launch_combine(partial, partial_dt, token_pos, nullptr, T, ep_size, H, out, out_dt, 0,
                         stream);
+}
+
+moe_status_t moe_layer_norm(const void* x, const void* residual, const void* gamma,
+                            const void* beta, moe_dtype_t dt, int T, int H, float eps,
+                            void* residual_out, void* y, uint8_t* q, float q_scale,
+                            hipStream_t stream) {
+  const moe_status_t st = check_norm(x, gamma, dt, T, H, eps);
+  if (st != MOE_OK || T == 0) return st;
+  if (!residual_out && !y && !q) return MOE_ERR_INVALID_ARG;
+  if (y && y == residual_out) return MOE_ERR_INVALID_ARG;
+  if (q && !code_scale_ok(q_scale)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(residual) || !aligned16(beta) || !aligned16(residual_out) || !aligned16(y) ||
+      !aligned16(q))
+    return MOE_ERR_INVALID_ARG;
+  return launch_layer_norm(x, residual, gamma, beta, dt == MOE_DTYPE_BF16, T, H, eps, residual_out,
+                           y, q, q_scale, stream);
+}
+
+size_t moe_norm_backward_workspace_size(int T, int H) {
+  if (T < 0 || H < 1 || H % 8 != 0 || H > kMaxNormWidth) return 0;
+  return norm_backward_workspace_bytes(T, H);
+}
+
+moe_status_t moe_rms_norm_backward(const void* dy, const void* x, const void* gamma,
+                                   const void* dresidual, moe_dtype_t dt, int T, int H, float eps,
+                                   void* dx, float* dgamma, void* ws, size_t ws_bytes,
+                                   hipStream_t stream) {
+  return norm_backward(false, dy, x, gamma, dresidual, dt, T, H, eps, dx, dgamma, nullptr, ws,
+                       ws_bytes, stream);
+}
+
+moe_status_t moe_layer_norm_backward(const void* dy, const void* x, const void* gamma,
+                                     const void* dresidual, moe_dtype_t dt, int T, int H,
+                                     float eps, void* dx, float* dgamma, float* dbeta, void* ws,
+                                     size_t ws_bytes, hipStream_t stream) {
+  return norm_backward(true, dy, x, gamma, dresidual, dt, T, H, eps, dx, dgamma, dbeta, ws,
+                       ws_bytes, stream);
+}
+
+moe_status_t moe_combine_backward(const void* dout, moe_dtype_t dout_dt, const void* y,
+                                  moe_dtype_t y_dt, const int32_t* pair_row,
+                                  const float* w_masked, int T, int K, int H, void* dy, float* dw,
+                                  hipStream_t stream) {
+  if (T < 0 || K < 1 || H < 1) return MOE_ERR_INVALID_ARG;
+  if (!dtype_ok(dout_dt) || !dtype_ok(y_dt)) return MOE_ERR_UNSUPPORTED;
+  if (K > MOE_MAX_TOPK || H % 8 != 0 || H > kMaxRowWidth || !pairs_fit(T, K))
+    return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!dout || !pair_row || (!dy && !dw) || (dw && !y)) return MOE_ERR_INVALID_ARG;
+  if (dy && (dy == y || dy == dout)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(dout) || !aligned16(y) || !aligned16(dy)) return MOE_ERR_INVALID_ARG;
+  return launch_combine_backward(dout, dout_dt, y, y_dt, pair_row, w_masked, T, K, H, dy, dw,
+                                 stream);
+}
+
+moe_status_t moe_permute_backward(const void* dx_perm, moe_dtype_t dt, const int32_t* pair_row,
+                                  const float* pair_w, const void* x, int T, int K, int H,
+                                  void* dx, moe_dtype_t dx_dt, int accumulate, float* dpair_w,
+                                  hipStream_t stream) {
+  const moe_status_t st = check_combine(dx_perm, dt, pair_row, pair_w, T, K, H, dx, dx_dt, false);
+  if (st != MOE_OK) return st;
+  if (H > kMaxRowWidth) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (dpair_w && (!pair_w || !x || !aligned16(x))) return MOE_ERR_INVALID_ARG;
+  if (dx == dx_perm || (dpair_w && dx == x)) return MOE_ERR_INVALID_ARG;
+  return launch_permute_backward(dx_perm, dt, pair_row, pair_w, x, T, K, H, dx, dx_dt, accumulate,
+                                 dpair_w, stream);
+}
+
+moe_status_t moe_swiglu(const void* h, moe_dtype_t dt, const int32_t* offsets, int S,
+                        int max_rows, int I, void* act, hipStream_t stream) {
+  const moe_status_t st = check_grad(dt, offsets, S, max_rows, I, I);
+  if (st != MOE_OK || max_rows == 0) return st;
+  if (!h || !act || h == act || !aligned16(h) || !aligned16(act)) return MOE_ERR_INVALID_ARG;
+  return launch_swiglu(h, dt == MOE_DTYPE_BF16, offsets, S, max_rows, I, act, stream);
+}
+
+moe_status_t moe_grouped_gemm_backward(moe_gemm_op_t op, moe_dtype_t dt, const void* dc,
+                                       const int32_t* offsets, int S, int max_rows, const void* w,
+                                       int H, int I, const void* h, void* out,
+                                       hipStream_t stream) {
+  if (op != MOE_GEMM_GATE_UP_SWIGLU && op != MOE_GEMM_DOWN) return MOE_ERR_INVALID_ARG;
+  const moe_status_t st = check_grad(dt, offsets, S, max_rows, H, I);
+  if (st != MOE_OK) return st;
+  const bool down = op == MOE_GEMM_DOWN;
+  if (h && !down) return MOE_ERR_INVALID_ARG;
+  if (!down && I > kMaxGradWidth / 2) return MOE_ERR_UNSUPPORTED;
+  const int Kd = down ? H : 2 * I, N = down ? I : H;
+  if ((unsigned long long)Kd * N * dtype_bytes(dt) >= (1ull << 31)) return MOE_ERR_UNSUPPORTED;
+  const int tile = grad_tile(dt);
+  if (!tiles_fit(max_rows / tile + 1 + (int64_t)(S < max_rows ? S : max_rows), 1, N, tile))
+    return MOE_ERR_UNSUPPORTED;
+  if (max_rows == 0) return MOE_OK;
+  if (!dc || !w || !out || out == dc || out == w || out == h) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(dc) || !aligned16(w) || !aligned16(h) || !aligned16(out))
+    return MOE_ERR_INVALID_ARG;
+  return dt == MOE_DTYPE_BF16
+             ? launch_gemm_backward_bf16(dc, offsets, S, max_rows, w, Kd, N, h, out, stream)
+             : launch_gemm_backward_f32(dc, offsets, S, max_rows, w, Kd, N, h, out, stream);
+}
+
+size_t moe_grouped_gemm_weight_grad_workspace_size(moe_dtype_t dt, int S, int max_rows, int N,
+                                                   int Kd) {
+  const int32_t some = 0;
+  if (check_grad(dt, &some, S, max_rows, N, Kd) != MOE_OK) return 0;
+  const int splits = grad_splits(S, max_rows, N, Kd, grad_tile(dt));
+  return splits > 1 ? (size_t)splits * S * N * Kd * sizeof(float) : 0;
+}
+
+moe_status_t moe_grouped_gemm_weight_grad(moe_dtype_t dt, const void* dc, const void* a,
+                                          const int32_t* offsets, int S, int max_rows, int N,
+                                          int Kd, void* dw, moe_dtype_t dw_dt, int accumulate,
+                                          void* ws, size_t ws_bytes, hipStream_t stream) {
+  const moe_status_t st = check_grad(dt, offsets, S, max_rows, N, Kd);
+  if (st != MOE_OK) return st;
+  if (!dtype_ok(dw_dt)) return MOE_ERR_UNSUPPORTED;
+  const int tile = grad_tile(dt);
+  if (!tiles_fit((int64_t)S * grad_splits(S, max_rows, N, Kd, tile), N, Kd, tile))
+    return MOE_ERR_UNSUPPORTED;
+  if (!dw || !aligned16(dw)) return MOE_ERR_INVALID_ARG;
+  if (max_rows > 0 && (!dc || !a || dw == dc || dw == a || !aligned16(dc) || !aligned16(a)))
+    return MOE_ERR_INVALID_ARG;
+  const size_t need = moe_grouped_gemm_weight_grad_workspace_size(dt, S, max_rows, N, Kd);
+  if (need > 0 && (!ws || ws_bytes < need)) return MOE_ERR_WORKSPACE;
+  if (need > 0 && !aligned16(ws)) return MOE_ERR_INVALID_ARG;
+  const bool f32 = dw_dt == MOE_DTYPE_F32;
+  return dt == MOE_DTYPE_BF16
+             ? launch_gemm_weight_grad_bf16(dc, a, offsets, S, max_rows, N, Kd, dw, f32, accumulate,
+                                            ws, stream)
+             : launch_gemm_weight_grad_f32(dc, a, offsets, S, max_rows, N, Kd, dw, f32, accumulate,
+                                           ws, stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,217 @@
+// Gradient of the root-mean-square norm and of the layer norm.
+//
+//   n = (x - m) r   (RMS: m = 0), r = 1 / sqrt(mean (x - m)^2 + eps)
+//   g = dy * gamma
+//   dx = r (g - mean g - n mean(g n)) + dresidual   (RMS: without mean g)
+//   dgamma = sum over rows of dy * n,  dbeta = sum over rows of dy
+//
+// The row's mean and deviation are formed again from x, which is read anyway,
+// so nothing has to be kept from the forward pass. A block goes from row to
+// row with its columns' sums for dgamma and dbeta in registers; each block
+// writes one row of partial sums, and a second kernel adds those in order.
+// Every sum's order depends on T and H alone.
+#include <algorithm>
+
+#include "norm_row.h"
+
+namespace moe {
+namespace {
+
+template <typename XT, bool CENTRED, int VPT, int L>
+__global__ __launch_bounds__(L == 0 ? 1024 : kNormGroupThreads) void norm_backward_kernel(
+    const XT* dy, const XT* x, const XT* __restrict__ gamma, const XT* dresidual, int T, int H,
+    float eps, XT* dx, float* __restrict__ pg, float* __restrict__ pb, int part_stride) {
+  __shared__ float part[5][16];
+  constexpr int kRows = L == 0 ? 1 : kNormGroupThreads / (L == 0 ? 1 : L);
+  const int group = L == 0 ? 0 : threadIdx.x / (L == 0 ? 1 : L);
+  const int first = L == 0 ? threadIdx.x : threadIdx.x % (L == 0 ? 1 : L);
+  const int stride = L == 0 ? blockDim.x : L;
+  const int nvec = H / 8;
+  const float over = 1.0f / (float)H;
+  float ag[VPT][8] = {}, ab[VPT][8] = {};
+  for (int64_t t = (int64_t)blockIdx.x * kRows + group; t < T; t += (int64_t)gridDim.x * kRows) {
+    const size_t row = (size_t)t * H;
+    float h[VPT][8] = {}, d[VPT][8] = {};
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int v = first + j * stride;
+      if (v < nvec) {
+        load8(x + row + v * 8, h[j]);
+        load8(dy + row + v * 8, d[j]);
+      }
+    }
+    const double r = normalize_row<CENTRED, VPT, L>(h, first, stride, nvec, H, eps, part);
+    float sg = 0.f, sn = 0.f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int v = first + j * stride;
+      if (v < nvec) {
+        float w[8];
+        load8(gamma + v * 8, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          ag[j][i] = fmaf(d[j][i], h[j][i], ag[j][i]);
+          if constexpr (CENTRED) ab[j][i] += d[j][i];
+          d[j][i] *= w[i];
+          sn = fmaf(d[j][i], h[j][i], sn);
+          if constexpr (CENTRED) sg += d[j][i];
+        }
+      }
+    }
+    sn = lanes_sum<L>(sn, part[3]) * over;
+    if constexpr (CENTRED) sg = lanes_sum<L>(sg, part[4]) * over;
+    if (dx != nullptr) {
+      const float rf = (float)r;
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        const int v = first + j * stride;
+        if (v < nvec) {
+          float o[8] = {};
+          if (dresidual != nullptr) load8(dresidual + row + v * 8, o);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float c = CENTRED ? fmaf(-h[j][i], sn, d[j][i] - sg) : fmaf(-h[j][i], sn, d[j][i]);
+            o[i] = fmaf(c, rf, o[i]);
+          }
+          store8(dx + row + v * 8, o);
+        }
+      }
+    }
+  }
+  if (pg == nullptr && pb == nullptr) return;
+  const size_t at = (size_t)blockIdx.x * part_stride;
+  if constexpr (L == 0) {
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int v = first + j * stride;
+      if (v < nvec) {
+        if (pg != nullptr) store8(pg + at + v * 8, ag[j]);
+        if (CENTRED && pb != nullptr) store8(pb + at + v * 8, ab[j]);
+      }
+    }
+  } else {  // the block's groups in order
+    constexpr int W = L * 8;
+    __shared__ float both[2][kRows][W];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      both[0][group][first * 8 + i] = ag[0][i];
+      both[1][group][first * 8 + i] = ab[0][i];
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < H; c += kNormGroupThreads) {
+      float a = 0.f, b = 0.f;
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) {
+        a += both[0][k][c];
+        b += both[1][k][c];
+      }
+      if (pg != nullptr) pg[at + c] = a;
+      if (CENTRED && pb != nullptr) pb[at + c] = b;
+    }
+  }
+}
+
+// out[c] = the sum over n rows of part [n, H], or zero for none: 16 lines of
+// a block add every 16th row, then the lines are added in order.
+__global__ __launch_bounds__(256) void fold_columns_kernel(const float* __restrict__ pg,
+                                                           const float* __restrict__ pb, int n,
+                                                           int H, float* __restrict__ dgamma,
+                                                           float* __restrict__ dbeta) {
+  const float* part = blockIdx.y == 0 ? pg : pb;
+  float* out = blockIdx.y == 0 ? dgamma : dbeta;
+  if (out == nullptr) return;
+  __shared__ float4 lines[16][16];
+  const int line = threadIdx.x / 16, at = threadIdx.x % 16;
+  const int c = (blockIdx.x * 16 + at) * 4;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (c < H) {
+#pragma unroll 4
+    for (int k = line; k < n; k += 16) {
+      const float4 v = *reinterpret_cast<const float4*>(part + (size_t)k * H + c);
+      s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+    }
+  }
+  lines[line][at] = s;
+  __syncthreads();
+  if (line != 0 || c >= H) return;
+#pragma unroll
+  for (int k = 1; k < 16; ++k) {
+    const float4 v = lines[k][at];
+    s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+  }
+  *reinterpret_cast<float4*>(out + c) = s;
+}
+
+// Blocks that share the rows: about 4096 waves, 16 a compute unit, at most 1024.
+int norm_blocks(int T, int H) {
+  if (T == 0) return 0;
+  const int L = norm_lanes(H / 8);
+  const int waves = L == 0 ? std::min(16, ceil_div(H / 8, kWave)) : kNormGroupThreads / kWave;
+  const int64_t rows = L == 0 ? 1 : kNormGroupThreads / L;
+  return (int)std::min<int64_t>((T + rows - 1) / rows, std::min(1024, 4096 / waves));
+}
+
+template <typename XT, bool CENTRED>
+void launch_typed(const void* dy, const void* x, const void* gamma, const void* dresidual, int T,
+                  int H, float eps, void* dx, float* pg, float* pb, int part_stride, int blocks,
+                  hipStream_t stream) {
+  const int nvec = H / 8;
+  auto go = [&](auto vpt, auto lanes) {
+    constexpr int VPT = decltype(vpt)::value, L = decltype(lanes)::value;
+    const int threads = L == 0 ? ceil_div(ceil_div(nvec, VPT), kWave) * kWave : kNormGroupThreads;
+    norm_backward_kernel<XT, CENTRED, VPT, L><<<blocks, threads, 0, stream>>>(
+        static_cast<const XT*>(dy), static_cast<const XT*>(x), static_cast<const XT*>(gamma),
+        static_cast<const XT*>(dresidual), T, H, eps, static_cast<XT*>(dx), pg, pb, part_stride);
+  };
+  const std::integral_constant<int, 1> one;
+  const std::integral_constant<int, 0> block;
+  switch (norm_lanes(nvec)) {
+    case 16: return go(one, std::integral_constant<int, 16>{});
+    case 32: return go(one, std::integral_constant<int, 32>{});
+    case 64: return go(one, std::integral_constant<int, 64>{});
+  }
+  if (nvec <= 1024)
+    go(one, block);
+  else if (nvec <= 2048)
+    go(std::integral_constant<int, 2>{}, block);
+  else
+    go(std::integral_constant<int, 4>{}, block);
+}
+
+}  // namespace
+
+size_t norm_backward_workspace_bytes(int T, int H) {
+  const int blocks = norm_blocks(T, H);
+  return blocks > 1 ? (size_t)blocks * H * 2 * sizeof(float) : 0;
+}
+
+moe_status_t launch_norm_backward(bool centred, const void* dy, const void* x, const void* gamma,
+                                  const void* dresidual, bool bf16, int T, int H, float eps,
+                                  void* dx, float* dgamma, float* dbeta, void* ws,
+                                  hipStream_t stream) {
+  const bool sums = dgamma != nullptr || dbeta != nullptr;
+  if (T == 0 && !sums) return MOE_OK;
+  const int blocks = norm_blocks(T, H);
+  float* pg = blocks == 1 ? dgamma : static_cast<float*>(ws);
+  float* pb = blocks == 1 ? dbeta : static_cast<float*>(ws) + (size_t)blocks * H;  // of no rows: unread
+  if (T > 0) {
+    float* kg = dgamma != nullptr ? pg : nullptr;
+    float* kb = dbeta != nullptr ? pb : nullptr;
+    auto go = [&](auto kind, auto c) {
+      launch_typed<typename decltype(kind)::type, decltype(c)::value>(
+          dy, x, gamma, dresidual, T, H, eps, dx, kg, kb, H, blocks, stream);
+    };
+    struct B16 { typedef uint16_t type; };
+    struct F32 { typedef float type; };
+    if (bf16 && centred) go(B16{}, std::true_type{});
+    else if (bf16) go(B16{}, std::false_type{});
+    else if (centred) go(F32{}, std::true_type{});
+    else go(F32{}, std::false_type{});
+  }
+  if (sums && blocks != 1)
+    fold_columns_kernel<<<dim3(ceil_div(H, 64), dbeta != nullptr ? 2 : 1), 256, 0, stream>>>(
+        pg, pb, blocks, H, dgamma, dbeta);
+  return launch_status();
+}
+
+}  // namespace moe

@@ -46,3 +46,4 @@ from .layer_oracle import (  # noqa: F401
     route_backward,
     routing_weights,
 )
+from . import training_oracle as training  # noqa: F401
