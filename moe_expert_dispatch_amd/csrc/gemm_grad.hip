@@ -11,6 +11,8 @@
 // 256 columns, and reach the matrix cores through transposing LDS reads
 // (ds_read_b64_tr_b16: 16 lanes read 4 rows of 16 columns, each lane gets the
 // 4 rows of its column).
+#include <algorithm>
+
 #include "grouped_tiles.h"
 
 namespace moe {
@@ -24,52 +26,75 @@ typedef int int32x4_t __attribute__((ext_vector_type(4)));
 typedef int int32x2_t __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
-constexpr int kTile = kGradTileBf16;  // rows and columns of an output tile
-constexpr int kSlice = 64;        // of the contraction at a time
-constexpr int kThreads = 512;     // 8 waves, 2 x 4 of 128 x 64
-constexpr int kPartVec = kTile * kSlice / 8;  // 16-byte vectors of one operand's slice (32 KB)
-constexpr uint32_t kOOB = 0x80000000u;        // past every resource here
+constexpr int kSlice = 64;              // of the contraction at a time
+constexpr uint32_t kOOB = 0x80000000u;  // past every resource here
 constexpr int kXcdItems = 32, kGroupCols = 4;
+
+// An output tile: WM x WN waves of NI x NJ fragments of 32 rows by 32 columns.
+// A wave's columns are consecutive. Its fragments of rows lie WM fragments
+// apart, so that the rows that a slot's last tile has are shared out among the
+// waves, 32 at a time.
+template <int WM_, int NI_, int WN_, int NJ_>
+struct Shape {
+  static constexpr int WM = WM_, NI = NI_, WN = WN_, NJ = NJ_;
+  static constexpr int kRowsM = WM * NI * 32, kColsN = WN * NJ * 32;
+  static constexpr int kWaves = WM * WN, kThreads = kWaves * kWave;
+  static constexpr int kVecM = kRowsM * kSlice / 8, kVecN = kColsN * kSlice / 8;  // of a slice
+  static constexpr int kCopiesM = kVecM / kThreads, kCopiesN = kVecN / kThreads;  // a wave, 1 KB each
+  static_assert(kVecM % kThreads == 0 && kVecN % kThreads == 0, "whole copies");
+};
+typedef Shape<2, 4, 4, 2> Large;  // 256 x 256: 64 KB a slice, one block a compute unit
+typedef Shape<1, 2, 4, 1> Small;  // 64 x 128: 24 KB a slice, three blocks a compute unit
+static_assert(Large::kRowsM == kGradTileBf16 && Large::kColsN == kGradTileBf16, "the host's tile");
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, uint32_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes,
                                            0x00020000);
 }
 
+// The same of values that every lane holds alike: said with readfirstlane, without
+// which the compiler may keep them in vector registers and loop over the lanes at
+// each copy (the weights' gradient of 131072 rows of 2048 x 4096 took 2.66 ms so).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_rsrc(const void* base, uint32_t bytes) {
+  const uint64_t a = reinterpret_cast<uint64_t>(base);
+  const uint32_t lo = (uint32_t)uniform_i32((int)(uint32_t)a);
+  const uint32_t hi = (uint32_t)uniform_i32((int)(uint32_t)(a >> 32));
+  return make_rsrc(reinterpret_cast<const void*>(((uint64_t)hi << 32) | lo),
+                   (uint32_t)uniform_i32((int)bytes));
+}
+
+// 16 bytes a lane from byte offset `off` to LDS, 1 KB in a row from `to`; out of
+// range, zeros. (A function of its own, not a template: the host's pass drops a
+// kernel's stub without a word where it looks at this size inside one.)
+__device__ __forceinline__ void copy16(__amdgpu_buffer_rsrc_t from, uint4* to, uint32_t off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (lds_ptr_t)to, 16, off, 0, 0, 0);
+}
+
 // LDS place, in vectors, of 16-byte chunk ch of row r: of a tile whose rows are
-// 64 contracted values (128 bytes), and of one whose rows are 256 columns (512
-// bytes). Both spread the reads of a half wave over all banks.
+// 64 contracted values (128 bytes), and of one whose rows are COLS columns.
+// Both spread the reads of a half wave over all banks.
 __device__ __forceinline__ int swz_k(int r, int ch) { return r * 8 + (ch ^ ((r >> 1) & 7)); }
-__device__ __forceinline__ int swz_t(int r, int ch) { return r * 32 + (ch ^ ((r & 3) << 2)); }
+template <int COLS>
+__device__ __forceinline__ int swz_t(int r, int ch) {
+  return r * (COLS / 8) + (ch ^ ((r & 3) << 2));
+}
 
 // 8 contracted values of this lane's column from a tile of the second kind;
 // `at` is the byte offset of the first four, the others lie 4 rows below.
+template <int COLS>
 __device__ __forceinline__ bf16x8_t read_tr(const uint4* part, int at) {
   typedef short s16x8_t __attribute__((ext_vector_type(8)));
   typedef __attribute__((address_space(3))) s16x4_t* lds_s16x4_t;
   typedef __attribute__((address_space(3))) char* lds_char_t;
   const lds_char_t p = (lds_char_t)(lds_ptr_t)const_cast<uint4*>(part) + at;
   const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t)p);
-  const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t)(p + 4 * 512));
+  const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t)(p + 4 * COLS * 2));
   return __builtin_bit_cast(bf16x8_t,
                             (s16x8_t)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
 __device__ __forceinline__ bf16x8_t read_k(const uint4* part, int at) {
   return *reinterpret_cast<const bf16x8_t*>(reinterpret_cast<const char*>(part) + at);
-}
-
-// Two runs of 4 consecutive columns a lane (accumulator groups g and g + 1 of
-// the lane halves) become 8 consecutive columns: group g for lanes 0..31,
-// g + 1 for the others.
-__device__ __forceinline__ void join8(const float* lo, const float* hi, float* o) {
-#pragma unroll
-  for (int v = 0; v < 4; ++v) {
-    const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(lo[v]), __float_as_uint(hi[v]),
-                                                    false, false);
-    o[v] = __uint_as_float(s[0]);
-    o[4 + v] = __uint_as_float(s[1]);
-  }
 }
 
 __device__ __forceinline__ int32x4_t pack8(const float* o) {
@@ -102,24 +127,45 @@ struct Args {
   int accumulate, splits;  // weights'; splits > 1: out is [splits, S, M, N]
 };
 
+// A tile: its slot, output rows and columns, and what is contracted.
+template <typename SH>
+struct Item {
+  int s, split, m0, n0, row0, rows, nd;
+  const uint16_t *m_next, *n_next;  // weights' gradient: of the next slice to ask for
+  int left;                         // and the rows from there on
+  uint32_t m_off[SH::kCopiesM], n_off[SH::kCopiesN];  // of the lane's chunks in a slice
+};
+
+// Waits until at most N vector memory operations of the wave are outstanding.
+template <int N>
+__device__ __forceinline__ void vm_wait() {
+  static_assert(N < 16, "one field of the count");
+  __builtin_amdgcn_s_waitcnt(0x0f70 | N);
+}
+
 // A persistent block takes items (output tiles) in turn. LDS holds two slices
 // of both operands, each in an array of its own, so that the compiler sees
-// that the reads of one do not wait for the copies into the other.
-template <int KIND>
-__global__ __launch_bounds__(kThreads, 1) void grouped_grad_kernel(Args p) {
+// that the reads of one need not wait for the copies into the other. The copy
+// of slice d + 1 runs while slice d is multiplied. The next item's first slice
+// is asked for before an item's results are stored, its second one behind the
+// stores: no more outstanding operations than that second slice's then mean
+// that the first has arrived (loads arrive in order), whatever the stores do.
+template <int KIND, typename SH>
+__global__ __launch_bounds__(SH::kThreads, SH::kWaves == 8 ? 2 : 3) void grouped_grad_kernel(Args p) {
   constexpr bool WEIGHTS = KIND >= kWeights;
-  __shared__ uint4 stage0[2 * kPartVec], stage1[2 * kPartVec];
+  constexpr int BM = SH::kRowsM, BN = SH::kColsN, NI = SH::NI, NJ = SH::NJ;
+  __shared__ uint4 stage0[SH::kVecM + SH::kVecN], stage1[SH::kVecM + SH::kVecN];
   __shared__ int32_t tp[WEIGHTS ? 1 : MOE_MAX_SLOTS + 1];
-  __shared__ int32_t scratch[WEIGHTS ? 1 : kThreads];
+  __shared__ int32_t scratch[WEIGHTS ? 1 : SH::kThreads];
   const int lane = lane_id();
   const int wave = uniform_i32(threadIdx.x / kWave);
-  const int wm = wave >> 2, wn = wave & 3;
+  const int wm = wave / SH::WN, wn = wave % SH::WN;
 
-  const int NT = ceil_div(p.N, kTile);
-  const int MT = WEIGHTS ? ceil_div(p.M, kTile) : 0;
+  const int NT = ceil_div(p.N, BN);
+  const int MT = WEIGHTS ? ceil_div(p.M, BM) : 0;
   int RT = 0;
   if constexpr (!WEIGHTS) {
-    tile_prefix<kThreads, kTile>(p.offsets, p.S, p.max_rows, tp, scratch);
+    tile_prefix<SH::kThreads, BM>(p.offsets, p.S, p.max_rows, tp, scratch);
     RT = uniform_i32(tp[p.S]);
   }
   const int GN = NT < kGroupCols ? NT : kGroupCols;
@@ -127,255 +173,282 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_grad_kernel(Args p) {
   const int total = WEIGHTS ? p.S * p.splits * MT * NT : RT * NT;  // the host keeps it in 31 bits
 
   // Byte offsets of this lane's fragments in a stage.
-  int m_at[4], n_at[2];  // M side: 32 rows i; N side: 32 columns j
+  int m_at[4], n_at[NJ];
   const int tr_row = (lane >> 5) * 8 + ((lane & 15) >> 2);
+  const int tr_ch = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if constexpr (WEIGHTS) {
-      const int ch = wm * 16 + i * 4 + ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
-      m_at[i] = swz_t(tr_row, ch) * 16 + (lane & 1) * 8;
-    } else {  // i: the chunk of contracted block kb; rows 32 further lie 4 KB further
-      m_at[i] = swz_k(wm * 128 + (lane & 31), 2 * i + (lane >> 5)) * 16;
-    }
+    if constexpr (WEIGHTS)
+      m_at[i] = swz_t<BM>(tr_row, (i * SH::WM + wm) * 4 + tr_ch) * 16 + (lane & 1) * 8;
+    else  // i: the chunk of contracted block i of the slice; fragments of rows lie 4 KB apart
+      m_at[i] = swz_k(wm * 32 + (lane & 31), 2 * i + (lane >> 5)) * 16;
   }
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int ch = wn * 8 + j * 4 + ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
-    n_at[j] = swz_t(tr_row, ch) * 16 + (lane & 1) * 8;
-  }
+  for (int j = 0; j < NJ; ++j)
+    n_at[j] = swz_t<BN>(tr_row, (wn * NJ + j) * 4 + tr_ch) * 16 + (lane & 1) * 8;
 
-  for (int item = first_item(blockIdx.x, gridDim.x); item < total; item += gridDim.x) {
-    // the tile: its slot, output rows and columns, and what is contracted
-    int s, m0, n0, rows, row0, nd, split = 0;
+  Item<SH> it;
+  const uint32_t m_row = (uint32_t)(WEIGHTS ? p.M : p.Kd) * 2u, n_row = (uint32_t)p.N * 2u;
+
+  auto setup = [&](int item) {
+    int lo, hi;
     if constexpr (WEIGHTS) {
       const int z = item / (MT * NT);
       int mt, nt;
       item_tile(item - z * MT * NT, MT, NT, GM, GN, &mt, &nt);
-      s = z / p.splits;
-      split = z - s * p.splits;
-      int lo, hi;
-      slot_rows(p.offsets, s, p.max_rows, &lo, &hi);
+      it.s = z / p.splits;
+      it.split = z - it.s * p.splits;
+      slot_rows(p.offsets, it.s, p.max_rows, &lo, &hi);
       const int whole = ceil_div(hi - lo, kSlice);
       const int each = ceil_div(whole, p.splits) * kSlice;  // rows of a split
-      row0 = uniform_i32(min(lo + split * each, hi));
-      rows = uniform_i32(min(hi - row0, each));
-      nd = ceil_div(rows, kSlice);
-      m0 = mt * kTile;
-      n0 = nt * kTile;
+      it.row0 = uniform_i32(min(lo + it.split * each, hi));
+      it.rows = uniform_i32(min(hi - it.row0, each));
+      it.nd = ceil_div(it.rows, kSlice);
+      it.m0 = mt * BM;
+      it.n0 = nt * BN;
+      it.m_next = p.m_side + (size_t)it.row0 * p.M;
+      it.n_next = p.n_side + (size_t)it.row0 * p.N;
+      it.left = it.rows;
     } else {
       int rt, nt;
       item_tile(item, RT, NT, GM, GN, &rt, &nt);
-      s = uniform_i32(tile_slot(tp, p.S, rt));
-      int lo, hi;
-      slot_rows(p.offsets, s, p.max_rows, &lo, &hi);
-      row0 = uniform_i32(lo + (rt - tp[s]) * kTile);
-      rows = uniform_i32(min(kTile, hi - row0));
-      nd = ceil_div(p.Kd, kSlice);
-      m0 = 0;
-      n0 = nt * kTile;
+      it.s = uniform_i32(tile_slot(tp, p.S, rt));
+      slot_rows(p.offsets, it.s, p.max_rows, &lo, &hi);
+      it.row0 = uniform_i32(lo + (rt - tp[it.s]) * BM);
+      it.rows = uniform_i32(min(BM, hi - it.row0));
+      it.nd = ceil_div(p.Kd, kSlice);
+      it.m0 = 0;
+      it.n0 = nt * BN;
     }
-    const uint32_t m_row = (uint32_t)(WEIGHTS ? p.M : p.Kd) * 2u, n_row = (uint32_t)p.N * 2u;
-
-    // offsets of the lane's chunks in a slice
-    uint32_t m_off[4], n_off[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int q = wave * 4 + i;  // KB of the part
-      const int r = q * 2 + (lane >> 5);
-      const int c = (lane & 31) ^ ((r & 3) << 2);
-      n_off[i] = n0 + c * 8 < p.N ? (uint32_t)r * n_row + (uint32_t)(n0 + c * 8) * 2u : kOOB;
+    for (int i = 0; i < SH::kCopiesM; ++i) {
+      const int v = (wave * SH::kCopiesM + i) * kWave + lane;  // vector of the slice
       if constexpr (WEIGHTS) {
-        m_off[i] = m0 + c * 8 < p.M ? (uint32_t)r * m_row + (uint32_t)(m0 + c * 8) * 2u : kOOB;
+        const int r = v / (BM / 8), c = it.m0 + ((v % (BM / 8)) ^ ((r & 3) << 2)) * 8;
+        it.m_off[i] = c < p.M ? (uint32_t)r * m_row + (uint32_t)c * 2u : kOOB;
       } else {
-        const int rr = q * 8 + (lane >> 3);
-        const int ch = (lane & 7) ^ ((rr >> 1) & 7);
-        m_off[i] = (uint32_t)rr * m_row + (uint32_t)ch * 16u;
+        const int r = v / 8, ch = (v % 8) ^ ((r >> 1) & 7);
+        it.m_off[i] = (uint32_t)r * m_row + (uint32_t)ch * 16u;
       }
     }
-
-    auto fetch = [&](uint4* stage, int d) {
-      if constexpr (WEIGHTS) {
-        const int left = rows - d * kSlice < kSlice ? rows - d * kSlice : kSlice;
-        const size_t r = (size_t)row0 + (size_t)d * kSlice;
-        const __amdgpu_buffer_rsrc_t rm = make_rsrc(p.m_side + r * p.M, (uint32_t)left * m_row);
-        const __amdgpu_buffer_rsrc_t rn = make_rsrc(p.n_side + r * p.N, (uint32_t)left * n_row);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(rm, (lds_ptr_t)(stage + (wave * 4 + i) * 64), 16,
-                                                   m_off[i], 0, 0, 0);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(
-              rn, (lds_ptr_t)(stage + kPartVec + (wave * 4 + i) * 64), 16, n_off[i], 0, 0, 0);
-      } else {
-        const __amdgpu_buffer_rsrc_t rm =
-            make_rsrc(p.m_side + (size_t)row0 * p.Kd, (uint32_t)rows * m_row);
-        const __amdgpu_buffer_rsrc_t rn =
-            make_rsrc(p.n_side + (size_t)s * p.Kd * p.N, (uint32_t)p.Kd * n_row);
-        const bool tail = (d + 1) * kSlice > p.Kd;  // the chunks past Kd belong to the next row
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int rr = (wave * 4 + i) * 8 + (lane >> 3);
-          const int ch = (lane & 7) ^ ((rr >> 1) & 7);
-          const uint32_t o = m_off[i] + (uint32_t)d * (kSlice * 2);
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(
-              rm, (lds_ptr_t)(stage + (wave * 4 + i) * 64), 16,
-              tail && d * kSlice + ch * 8 >= p.Kd ? kOOB : o, 0, 0, 0);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(
-              rn, (lds_ptr_t)(stage + kPartVec + (wave * 4 + i) * 64), 16,
-              n_off[i] == kOOB ? kOOB : n_off[i] + (uint32_t)d * kSlice * n_row, 0, 0, 0);
-      }
-    };
-
-    floatx16 acc[2][4];
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[j][i] = floatx16{};
-
-    // a wave whose part of the tile is empty only copies
-    const bool live = WEIGHTS ? m0 + wm * 128 < p.M && n0 + wn * 64 < p.N
-                              : wm * 128 < rows && n0 + wn * 64 < p.N;
-    auto compute = [&](const uint4* stage) {
-      if (!live) return;
-#pragma unroll
-      for (int kb = 0; kb < kSlice / 16; ++kb) {
-        bf16x8_t fm[4], fn[2];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if constexpr (WEIGHTS) fm[i] = read_tr(stage, m_at[i] + kb * (16 * 512));
-          else fm[i] = read_k(stage, m_at[kb] + i * 4096);
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) fn[j] = read_tr(stage + kPartVec, n_at[j] + kb * (16 * 512));
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            acc[j][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fn[j], fm[i], acc[j][i], 0, 0, 0);
-      }
-    };
-    // this wave's copies are done; with the barrier everyone's are, and nobody
-    // reads the other stage
-    auto arrive = [&]() {
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      __syncthreads();
-    };
-
-    __syncthreads();  // the previous item's reads are done
-    if (nd > 0) fetch(stage0, 0);
-    for (int d = 0; d < nd; d += 2) {
-      arrive();
-      if (d + 1 < nd) fetch(stage1, d + 1);
-      compute(stage0);
-      if (d + 1 >= nd) break;
-      arrive();
-      if (d + 2 < nd) fetch(stage0, d + 2);
-      compute(stage1);
+    for (int i = 0; i < SH::kCopiesN; ++i) {
+      const int v = (wave * SH::kCopiesN + i) * kWave + lane;
+      const int r = v / (BN / 8), c = it.n0 + ((v % (BN / 8)) ^ ((r & 3) << 2)) * 8;
+      it.n_off[i] = c < p.N ? (uint32_t)r * n_row + (uint32_t)c * 2u : kOOB;
     }
-    if (!live) continue;
+  };
 
-    // register v of acc[j][i]: column 8 (v / 4) + 4 (lane / 32) + v % 4 of the 32
-    // of j, row lane % 32 of the 32 of i
-    const int ch8 = 8 * (lane >> 5);
-    if constexpr (KIND == kRows || KIND == kRowsSwiglu) {
-      const uint32_t cols = KIND == kRowsSwiglu ? 2u * (uint32_t)p.N : (uint32_t)p.N;
-      const uint32_t bytes = (uint32_t)rows * cols * 2u;
-      const __amdgpu_buffer_rsrc_t rc =
-          make_rsrc(static_cast<uint16_t*>(p.out) + (size_t)row0 * cols, bytes);
-      const __amdgpu_buffer_rsrc_t rh =
-          make_rsrc(KIND == kRowsSwiglu ? p.h + (size_t)row0 * cols : nullptr,
-                    KIND == kRowsSwiglu ? bytes : 0u);
+  // Asks for slice d, each in turn (past the last one: for nothing, LDS gets
+  // zeros). What lies outside of the tile's rows, columns and contraction
+  // arrives as zeros.
+  auto fetch = [&](uint4* stage, int d) {
+    uint4* to_m = stage + wave * SH::kCopiesM * kWave;
+    uint4* to_n = stage + SH::kVecM + wave * SH::kCopiesN * kWave;
+    if constexpr (WEIGHTS) {
+      const uint32_t have = (uint32_t)max(0, min(it.left, kSlice));
+      const __amdgpu_buffer_rsrc_t rm = uniform_rsrc(it.m_next, have * m_row);
+      const __amdgpu_buffer_rsrc_t rn = uniform_rsrc(it.n_next, have * n_row);
+      it.m_next += (size_t)kSlice * p.M;
+      it.n_next += (size_t)kSlice * p.N;
+      it.left -= kSlice;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t r = (uint32_t)(wm * 128 + i * 32 + (lane & 31));
+      for (int i = 0; i < SH::kCopiesM; ++i)
+        copy16(rm, to_m + i * kWave, it.m_off[i]);
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int g = 0; g < 4; g += 2) {
-            const int col = n0 + wn * 64 + j * 32 + 8 * g + ch8;
-            float lo[4], hi[4], o[8];
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-              lo[v] = acc[j][i][4 * g + v];
-              hi[v] = acc[j][i][4 * g + 4 + v];
-            }
-            join8(lo, hi, o);
-            const uint32_t at = col < p.N ? (r * cols + (uint32_t)col) * 2u : kOOB;
-            if constexpr (KIND == kRows) {
-              __builtin_amdgcn_raw_buffer_store_b128(pack8(o), rc, at, 0, 0);
-            } else {
-              const uint32_t up = col < p.N ? at + (uint32_t)p.N * 2u : kOOB;
-              float gt[8], u[8];
-              unpack8(__builtin_amdgcn_raw_buffer_load_b128(rh, at, 0, 0), gt);
-              unpack8(__builtin_amdgcn_raw_buffer_load_b128(rh, up, 0, 0), u);
-#pragma unroll
-              for (int v = 0; v < 8; ++v) {
-                const float sg = 1.0f / (1.0f + __expf(-gt[v]));
-                const float silu = gt[v] * sg;
-                gt[v] = o[v] * u[v] * (sg + silu * (1.0f - sg));
-                u[v] = o[v] * silu;
-              }
-              __builtin_amdgcn_raw_buffer_store_b128(pack8(gt), rc, at, 0, 0);
-              __builtin_amdgcn_raw_buffer_store_b128(pack8(u), rc, up, 0, 0);
-            }
-          }
-      }
+      for (int i = 0; i < SH::kCopiesN; ++i)
+        copy16(rn, to_n + i * kWave, it.n_off[i]);
     } else {
-      constexpr uint32_t OB = KIND == kWeightsF32 ? 4u : 2u;
-      const size_t first = (((size_t)split * p.S + s) * p.M + m0) * p.N;
-      const int high = p.M - m0 < kTile ? p.M - m0 : kTile;
-      const __amdgpu_buffer_rsrc_t rc = make_rsrc(static_cast<char*>(p.out) + first * OB,
-                                                  (uint32_t)high * (uint32_t)p.N * OB);
+      const bool live = d < it.nd;
+      const __amdgpu_buffer_rsrc_t rm =
+          uniform_rsrc(p.m_side + (size_t)it.row0 * p.Kd, live ? (uint32_t)it.rows * m_row : 0u);
+      const __amdgpu_buffer_rsrc_t rn =
+          uniform_rsrc(p.n_side + (size_t)it.s * p.Kd * p.N, live ? (uint32_t)p.Kd * n_row : 0u);
+      const bool tail = (d + 1) * kSlice > p.Kd;  // chunks past Kd belong to the next row
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t r = (uint32_t)(wm * 128 + i * 32 + (lane & 31));
+      for (int i = 0; i < SH::kCopiesM; ++i) {
+        const int v = (wave * SH::kCopiesM + i) * kWave + lane;
+        const int ch = (v % 8) ^ ((v / 8 >> 1) & 7);
+        copy16(rm, to_m + i * kWave,
+               tail && d * kSlice + ch * 8 >= p.Kd ? kOOB : it.m_off[i] + (uint32_t)d * (kSlice * 2));
+      }
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          if constexpr (KIND == kWeightsF32) {
+      for (int i = 0; i < SH::kCopiesN; ++i)
+        copy16(rn, to_n + i * kWave,
+               it.n_off[i] == kOOB ? kOOB : it.n_off[i] + (uint32_t)d * kSlice * n_row);
+    }
+  };
+
+  // Multiplies a slice: the wave's first ni fragments of rows.
+  auto multiply = [&](const uint4* stage, auto& acc) {
+    constexpr int ni = sizeof(acc[0]) / sizeof(floatx16);
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              const int col = n0 + wn * 64 + j * 32 + 8 * g + 4 * (lane >> 5);
-              const uint32_t at = col < p.N ? (r * (uint32_t)p.N + (uint32_t)col) * 4u : kOOB;
-              int32x4_t o;
-              if (p.accumulate) {
-                const int32x4_t prev = __builtin_amdgcn_raw_buffer_load_b128(rc, at, 0, 0);
+    for (int kb = 0; kb < kSlice / 16; ++kb) {
+      bf16x8_t fm[ni], fn[NJ];
 #pragma unroll
-                for (int v = 0; v < 4; ++v)
-                  o[v] = __float_as_int(__int_as_float(prev[v]) + acc[j][i][4 * g + v]);
-              } else {
+      for (int i = 0; i < ni; ++i) {
+        if constexpr (WEIGHTS) fm[i] = read_tr<BM>(stage, m_at[i] + kb * (16 * BM * 2));
+        else fm[i] = read_k(stage, m_at[kb] + i * (SH::WM * 4096));
+      }
 #pragma unroll
-                for (int v = 0; v < 4; ++v) o[v] = __float_as_int(acc[j][i][4 * g + v]);
-              }
-              __builtin_amdgcn_raw_buffer_store_b128(o, rc, at, 0, 0);
-            }
-          } else {
+      for (int j = 0; j < NJ; ++j)
+        fn[j] = read_tr<BN>(stage + SH::kVecM, n_at[j] + kb * (16 * BN * 2));
 #pragma unroll
-            for (int g = 0; g < 4; g += 2) {
-              const int col = n0 + wn * 64 + j * 32 + 8 * g + ch8;
-              const uint32_t at = col < p.N ? (r * (uint32_t)p.N + (uint32_t)col) * 2u : kOOB;
-              float lo[4], hi[4], o[8];
+      for (int j = 0; j < NJ; ++j)
 #pragma unroll
-              for (int v = 0; v < 4; ++v) {
-                lo[v] = acc[j][i][4 * g + v];
-                hi[v] = acc[j][i][4 * g + 4 + v];
-              }
-              join8(lo, hi, o);
-              if (p.accumulate) {
-                float prev[8];
-                unpack8(__builtin_amdgcn_raw_buffer_load_b128(rc, at, 0, 0), prev);
+        for (int i = 0; i < ni; ++i)
+          acc[j][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fn[j], fm[i], acc[j][i], 0, 0, 0);
+    }
+  };
+  // All slices of the item; `use` multiplies the one in a stage.
+  auto contract = [&](auto use) {
+    vm_wait<SH::kCopiesM + SH::kCopiesN>();
+    __syncthreads();
+    use(stage0);
+    for (int d = 1; d < it.nd; d += 2) {
+      vm_wait<0>();
+      __syncthreads();
+      if (d + 1 < it.nd) fetch(stage0, d + 1);
+      use(stage1);
+      if (d + 1 >= it.nd) break;
+      vm_wait<0>();
+      __syncthreads();
+      if (d + 2 < it.nd) fetch(stage1, d + 2);
+      use(stage0);
+    }
+    __syncthreads();  // both stages have been read
+  };
+  // Stores the wave's first ni fragments of rows of tile t, 32 rows at a time
+  // through the wave's own part of stage 1 (nobody else copies or reads there),
+  // so that whole lines are written. Register v of acc[j][i] is column 8 (v / 4) +
+  // 4 (lane / 32) + v % 4 of the 32 of j, row lane % 32 of the 32 of i; what is read
+  // back are 4 or 8 consecutive columns a lane, kLanes lanes to a row.
+  auto store = [&](const Item<SH>& t, auto& acc) {
+    constexpr int ni = sizeof(acc[0]) / sizeof(floatx16);
+    constexpr int kCols = KIND == kWeightsF32 ? 4 : 8;
+    constexpr int kLanes = NJ * 32 / kCols, kLines = kWave / kLanes;  // rows a step
+    auto place = [&](int r, int ch) {
+      if constexpr (NJ == 2)
+        return stage1 + (r < 16 ? 0 : SH::kVecM) + wave * 256 + (r & 15) * 16 + (ch ^ (r & 15));
+      else
+        return stage1 + SH::kVecM + wave * 256 + r * 8 + (ch ^ ((r >> 1) & 7));
+    };
+    constexpr uint32_t OB = KIND == kWeightsF32 ? 4u : 2u;
+    const uint32_t cols = KIND == kRowsSwiglu ? 2u * (uint32_t)p.N : (uint32_t)p.N;
+    const size_t first = WEIGHTS ? (((size_t)t.split * p.S + t.s) * p.M + t.m0) * p.N
+                                 : (size_t)t.row0 * cols;
+    const uint32_t bytes = (uint32_t)(WEIGHTS ? min(p.M - t.m0, BM) : t.rows) * cols * OB;
+    const __amdgpu_buffer_rsrc_t rc = uniform_rsrc(static_cast<char*>(p.out) + first * OB, bytes);
+    const __amdgpu_buffer_rsrc_t rh = uniform_rsrc(
+        KIND == kRowsSwiglu ? p.h + first : nullptr, KIND == kRowsSwiglu ? bytes : 0u);
+    const int col = t.n0 + wn * NJ * 32 + (lane % kLanes) * kCols;
+    const uint32_t side = col < p.N ? (uint32_t)col * OB : kOOB;  // past every row where out of range
 #pragma unroll
-                for (int v = 0; v < 8; ++v) o[v] = prev[v] + o[v];
-              }
-              __builtin_amdgcn_raw_buffer_store_b128(pack8(o), rc, at, 0, 0);
-            }
+    for (int i = 0; i < ni; ++i) {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          *place(lane & 31, j * 8 + 2 * g + (lane >> 5)) =
+              make_uint4(__float_as_uint(acc[j][i][4 * g]), __float_as_uint(acc[j][i][4 * g + 1]),
+                         __float_as_uint(acc[j][i][4 * g + 2]), __float_as_uint(acc[j][i][4 * g + 3]));
+      wave_lds_fence();
+#pragma unroll
+      for (int l = 0; l < 32; l += kLines) {
+        const int r = l + lane / kLanes;
+        float o[kCols];
+#pragma unroll
+        for (int c = 0; c < kCols; c += 4) {
+          const uint4 q = *place(r, ((lane % kLanes) * kCols + c) / 4);
+          o[c] = __uint_as_float(q.x);
+          o[c + 1] = __uint_as_float(q.y);
+          o[c + 2] = __uint_as_float(q.z);
+          o[c + 3] = __uint_as_float(q.w);
+        }
+        const uint32_t row = (uint32_t)((i * SH::WM + wm) * 32 + r);
+        const uint32_t at = side == kOOB ? kOOB : row * cols * OB + side;
+        if constexpr (KIND == kWeightsF32) {
+          if (p.accumulate) {
+            const int32x4_t prev = __builtin_amdgcn_raw_buffer_load_b128(rc, at, 0, 0);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) o[v] = __int_as_float(prev[v]) + o[v];
           }
+          __builtin_amdgcn_raw_buffer_store_b128(
+              int32x4_t{__float_as_int(o[0]), __float_as_int(o[1]), __float_as_int(o[2]),
+                        __float_as_int(o[3])},
+              rc, at, 0, 0);
+        } else if constexpr (KIND == kRowsSwiglu) {
+          const uint32_t up = side == kOOB ? kOOB : at + (uint32_t)p.N * 2u;
+          float gt[8], u[8];
+          unpack8(__builtin_amdgcn_raw_buffer_load_b128(rh, at, 0, 0), gt);
+          unpack8(__builtin_amdgcn_raw_buffer_load_b128(rh, up, 0, 0), u);
+#pragma unroll
+          for (int v = 0; v < 8; ++v) {
+            const float sg = 1.0f / (1.0f + __expf(-gt[v]));
+            const float silu = gt[v] * sg;
+            gt[v] = o[v] * u[v] * (sg + silu * (1.0f - sg));
+            u[v] = o[v] * silu;
+          }
+          __builtin_amdgcn_raw_buffer_store_b128(pack8(gt), rc, at, 0, 0);
+          __builtin_amdgcn_raw_buffer_store_b128(pack8(u), rc, up, 0, 0);
+        } else {
+          if (KIND == kWeights && p.accumulate) {
+            float prev[8];
+            unpack8(__builtin_amdgcn_raw_buffer_load_b128(rc, at, 0, 0), prev);
+#pragma unroll
+            for (int v = 0; v < 8; ++v) o[v] = prev[v] + o[v];
+          }
+          __builtin_amdgcn_raw_buffer_store_b128(pack8(o), rc, at, 0, 0);
         }
       }
+      wave_lds_fence();
     }
+  };
+
+  int item = first_item(blockIdx.x, gridDim.x);
+  if (item >= total) return;
+  setup(item);
+  fetch(stage0, 0);
+  fetch(stage1, 1);
+  bool more = true;
+  while (more) {
+    const int next = item + gridDim.x;
+    more = next < total;
+    auto go_on = [&]() {
+      if (more) {
+        setup(next);
+        fetch(stage0, 0);
+      }
+    };
+    // A wave with ni fragments of rows: the accumulators live here alone, so that
+    // the forms' registers do not add up.
+    auto work = [&](auto nic) {
+      constexpr int ni = decltype(nic)::value;
+      floatx16 acc[NJ][ni];
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int i = 0; i < ni; ++i) acc[j][i] = floatx16{};
+      contract([&](const uint4* stage) { multiply(stage, acc); });
+      const Item<SH> done = it;
+      go_on();
+      store(done, acc);
+    };
+    const int high = WEIGHTS ? min(p.M - it.m0, BM) : it.rows;
+    const int ni = max(0, (ceil_div(high, 32) - wm + SH::WM - 1) / SH::WM);
+    if (ni == 0 || it.n0 + wn * NJ * 32 >= p.N) {  // copies alone
+      contract([](const uint4*) {});
+      go_on();
+    } else if (ni == 1) {
+      work(std::integral_constant<int, 1>{});
+    } else if (ni == 2 || NI == 2) {
+      work(std::integral_constant<int, 2>{});
+    } else if constexpr (NI > 2) {
+      if (ni == 3) work(std::integral_constant<int, 3>{});
+      else work(std::integral_constant<int, 4>{});
+    }
+    if (more) fetch(stage1, 1);
+    item = next;
   }
 }
 
@@ -389,6 +462,13 @@ int grad_splits(int S, int max_rows, int M, int N, int tile) {
   return tiles >= kSplitBlocks || n < 2 ? 1 : n > kMaxSplits ? kMaxSplits : (int)n;
 }
 
+namespace {
+
+// Rows a slot up to which the rows' gradient takes small tiles.
+constexpr int kFewRows = 32;
+
+}  // namespace
+
 moe_status_t launch_gemm_backward_bf16(const void* dc, const int32_t* offsets, int S, int max_rows,
                                        const void* w, int Kd, int N, const void* h, void* out,
                                        hipStream_t stream) {
@@ -399,13 +479,20 @@ moe_status_t launch_gemm_backward_bf16(const void* dc, const int32_t* offsets, i
   p.S = S; p.max_rows = max_rows; p.N = N; p.Kd = Kd; p.splits = 1;
   p.h = static_cast<const uint16_t*>(h);
   p.out = out;
-  const int64_t items = (int64_t)(max_rows / kTile + 1 + (S < max_rows ? S : max_rows)) * ceil_div(N, kTile);
-  const int cus = device_cu_count();
-  const int G = items < cus ? (int)items : cus;
-  if (h != nullptr)
-    grouped_grad_kernel<kRowsSwiglu><<<G, kThreads, 0, stream>>>(p);
-  else
-    grouped_grad_kernel<kRows><<<G, kThreads, 0, stream>>>(p);
+  auto go = [&](auto kind, auto shape) {
+    typedef decltype(shape) SH;
+    const int64_t items = (int64_t)(max_rows / SH::kRowsM + 1 + (S < max_rows ? S : max_rows)) *
+                          ceil_div(N, SH::kColsN);
+    const int64_t blocks = (int64_t)device_cu_count() * (SH::kWaves == 8 ? 1 : 3);
+    grouped_grad_kernel<decltype(kind)::value, SH>
+        <<<(int)std::min(items, blocks), SH::kThreads, 0, stream>>>(p);
+  };
+  auto by_kind = [&](auto shape) {
+    if (h != nullptr) go(std::integral_constant<int, kRowsSwiglu>{}, shape);
+    else go(std::integral_constant<int, kRows>{}, shape);
+  };
+  if (max_rows <= (int64_t)S * kFewRows) by_kind(Small{});
+  else by_kind(Large{});
   return launch_status();
 }
 
@@ -417,16 +504,16 @@ moe_status_t launch_gemm_weight_grad_bf16(const void* dc, const void* a, const i
   p.n_side = static_cast<const uint16_t*>(a);
   p.offsets = offsets;
   p.S = S; p.max_rows = max_rows; p.M = M; p.N = N;
-  p.splits = grad_splits(S, max_rows, M, N, kTile);
+  p.splits = grad_splits(S, max_rows, M, N, kGradTileBf16);
   p.out = p.splits > 1 ? ws : dw;
   p.accumulate = p.splits > 1 ? 0 : accumulate;
-  const int64_t items = (int64_t)S * p.splits * ceil_div(M, kTile) * ceil_div(N, kTile);
+  const int64_t items = (int64_t)S * p.splits * ceil_div(M, kGradTileBf16) * ceil_div(N, kGradTileBf16);
   const int cus = device_cu_count();
   const int G = items < cus ? (int)items : cus;
   if (dw_f32 || p.splits > 1)
-    grouped_grad_kernel<kWeightsF32><<<G, kThreads, 0, stream>>>(p);
+    grouped_grad_kernel<kWeightsF32, Large><<<G, Large::kThreads, 0, stream>>>(p);
   else
-    grouped_grad_kernel<kWeights><<<G, kThreads, 0, stream>>>(p);
+    grouped_grad_kernel<kWeights, Large><<<G, Large::kThreads, 0, stream>>>(p);
   if (p.splits > 1)
     return launch_fold_splits(static_cast<const float*>(ws), p.splits, (size_t)S * M * N, dw, dw_f32,
                               accumulate, stream);
