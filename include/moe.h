@@ -536,7 +536,7 @@ moe_status_t moe_permute_backward(const void* dx_perm, moe_dtype_t dt, const int
  * rows behind the last slot's are neither read nor written. max_rows < 2^31 -
  * 1024. Products of bf16 values are exact, sums f32, one rounding at the end
  * (dt MOE_DTYPE_F32: f32 products and sums on the matrix cores). The orders of
- * the sums depend on shapes alone, not on the scheduling. Buffers 16-byte
+ * the sums depend on shapes and the device's number of compute units alone. Buffers 16-byte
  * aligned, H % 8 == 0, I % 8 == 0; no output may overlap an input.
  *
  * moe_swiglu -- act[r, j] = silu(h[r, j]) * h[r, I + j], one rounding.

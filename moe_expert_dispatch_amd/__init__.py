@@ -557,27 +557,27 @@ def norm_backward_workspace_size(T: int, H: int) -> int:
     return int(lib().moe_norm_backward_workspace_size(T, H))
 
 
-def _norm_backward(what, dy, x, gamma, eps, dresidual, dx, outs, ws):
+def _norm_backward(what, dy, x, gamma, eps, dresidual, dx, sums, ws):
+    """dx and the sums over the rows: f32 [H] each, given or None."""
     _dev(x, "x", (torch.float32, torch.bfloat16))
     if x.dim() != 2:
         raise ValueError("x must be [T, H]")
-    T, H = x.shape
-    _dev(dy, "dy", x.dtype, (T, H))
-    _dev(gamma, "gamma", x.dtype, (H,))
+    dt, shape = x.dtype, x.shape
+    T, H = shape
+    _dev(dy, "dy", dt, shape)
+    _dev(gamma, "gamma", dt, (H,))
     if dresidual is not None:
-        _dev(dresidual, "dresidual", x.dtype, (T, H))
-    dx = torch.empty_like(x) if dx is None else _dev(dx, "dx", x.dtype, (T, H))
+        _dev(dresidual, "dresidual", dt, shape)
+    dx = torch.empty_like(x) if dx is None else _dev(dx, "dx", dt, shape)
+    # like gamma and by one number: a third of the time that a new shape takes torch
+    sums = [torch.empty_like(gamma, dtype=torch.float32) if s is None
+            else _dev(s, "dgamma and dbeta", torch.float32, (H,)) for s in sums]
     if ws is None:
-        ws = _empty((norm_backward_workspace_size(T, H),), torch.uint8, x)
-    _launch(what, x, (dy, gamma, dresidual, dx, *outs, ws), dy.data_ptr(), x.data_ptr(),
-            gamma.data_ptr(), _ptr(dresidual), _DT[x.dtype], T, H, eps, dx.data_ptr(),
-            *(o.data_ptr() for o in outs), ws.data_ptr(), ws.numel() * ws.element_size())
-    return dx
-
-
-def _column_sums(x: torch.Tensor, t: Optional[torch.Tensor], name: str) -> torch.Tensor:
-    H = x.shape[-1]
-    return _empty((H,), torch.float32, x) if t is None else _dev(t, name, torch.float32, (H,))
+        ws = x.new_empty(norm_backward_workspace_size(T, H), dtype=torch.uint8)
+    _launch(what, x, (dy, gamma, dresidual, dx, *sums, ws), dy.data_ptr(), x.data_ptr(),
+            gamma.data_ptr(), _ptr(dresidual), _DT[dt], T, H, eps, dx.data_ptr(),
+            *[s.data_ptr() for s in sums], ws.data_ptr(), ws.numel() * ws.element_size())
+    return (dx, *sums)
 
 
 def rms_norm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-6,
@@ -589,10 +589,7 @@ def rms_norm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor, ep
     dy is the gradient of rms_norm's y; x its input, or its residual_out where it added a
     residual, whose gradient dresidual is then added (dx is the gradient of both addends). dx may
     be dy, x or dresidual itself."""
-    _dev(x, "x", (torch.float32, torch.bfloat16))
-    dgamma = _column_sums(x, dgamma, "dgamma")
-    dx = _norm_backward("moe_rms_norm_backward", dy, x, gamma, eps, dresidual, dx, (dgamma,), ws)
-    return dx, dgamma
+    return _norm_backward("moe_rms_norm_backward", dy, x, gamma, eps, dresidual, dx, (dgamma,), ws)
 
 
 def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-5,
@@ -602,12 +599,8 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor, 
                         ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """moe_layer_norm_backward -> (dx [T, H], dgamma [H] f32, dbeta [H] f32); arguments as
     rms_norm_backward."""
-    _dev(x, "x", (torch.float32, torch.bfloat16))
-    dgamma = _column_sums(x, dgamma, "dgamma")
-    dbeta = _column_sums(x, dbeta, "dbeta")
-    dx = _norm_backward("moe_layer_norm_backward", dy, x, gamma, eps, dresidual, dx,
-                        (dgamma, dbeta), ws)
-    return dx, dgamma, dbeta
+    return _norm_backward("moe_layer_norm_backward", dy, x, gamma, eps, dresidual, dx,
+                          (dgamma, dbeta), ws)
 
 
 # ---------------------------------------------------------------- the router's training step

@@ -44,7 +44,7 @@ struct Shape {
   static_assert(kVecM % kThreads == 0 && kVecN % kThreads == 0, "whole copies");
 };
 typedef Shape<2, 4, 4, 2> Large;  // 256 x 256: 64 KB a slice, one block a compute unit
-typedef Shape<1, 2, 4, 1> Small;  // 64 x 128: 24 KB a slice, three blocks a compute unit
+typedef Shape<1, 1, 4, 2> Small;  // 32 x 256: 36 KB a slice, two blocks a compute unit
 static_assert(Large::kRowsM == kGradTileBf16 && Large::kColsN == kGradTileBf16, "the host's tile");
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, uint32_t bytes) {
@@ -151,7 +151,7 @@ __device__ __forceinline__ void vm_wait() {
 // stores: no more outstanding operations than that second slice's then mean
 // that the first has arrived (loads arrive in order), whatever the stores do.
 template <int KIND, typename SH>
-__global__ __launch_bounds__(SH::kThreads, SH::kWaves == 8 ? 2 : 3) void grouped_grad_kernel(Args p) {
+__global__ __launch_bounds__(SH::kThreads, 2) void grouped_grad_kernel(Args p) {
   constexpr bool WEIGHTS = KIND >= kWeights;
   constexpr int BM = SH::kRowsM, BN = SH::kColsN, NI = SH::NI, NJ = SH::NJ;
   __shared__ uint4 stage0[SH::kVecM + SH::kVecN], stage1[SH::kVecM + SH::kVecN];
@@ -328,10 +328,10 @@ __global__ __launch_bounds__(SH::kThreads, SH::kWaves == 8 ? 2 : 3) void grouped
     constexpr int kCols = KIND == kWeightsF32 ? 4 : 8;
     constexpr int kLanes = NJ * 32 / kCols, kLines = kWave / kLanes;  // rows a step
     auto place = [&](int r, int ch) {
-      if constexpr (NJ == 2)
-        return stage1 + (r < 16 ? 0 : SH::kVecM) + wave * 256 + (r & 15) * 16 + (ch ^ (r & 15));
-      else
-        return stage1 + SH::kVecM + wave * 256 + r * 8 + (ch ^ ((r >> 1) & 7));
+      static_assert(NJ == 2 && SH::kCopiesN * kWave * (NI == 1 ? 1 : 2) == 512, "32 rows of 256 bytes");
+      const int half = NI == 1 || r >= 16 ? SH::kVecM : 0;  // which of the wave's parts
+      return stage1 + half + wave * SH::kCopiesN * kWave + (NI == 1 ? r : r & 15) * 16 +
+             (ch ^ (r & 15));
     };
     constexpr uint32_t OB = KIND == kWeightsF32 ? 4u : 2u;
     const uint32_t cols = KIND == kRowsSwiglu ? 2u * (uint32_t)p.N : (uint32_t)p.N;
@@ -439,12 +439,11 @@ __global__ __launch_bounds__(SH::kThreads, SH::kWaves == 8 ? 2 : 3) void grouped
     if (ni == 0 || it.n0 + wn * NJ * 32 >= p.N) {  // copies alone
       contract([](const uint4*) {});
       go_on();
-    } else if (ni == 1) {
+    } else if (ni == 1 || NI == 1) {
       work(std::integral_constant<int, 1>{});
-    } else if (ni == 2 || NI == 2) {
-      work(std::integral_constant<int, 2>{});
-    } else if constexpr (NI > 2) {
-      if (ni == 3) work(std::integral_constant<int, 3>{});
+    } else if constexpr (NI == 4) {
+      if (ni == 2) work(std::integral_constant<int, 2>{});
+      else if (ni == 3) work(std::integral_constant<int, 3>{});
       else work(std::integral_constant<int, 4>{});
     }
     if (more) fetch(stage1, 1);
@@ -464,8 +463,23 @@ int grad_splits(int S, int max_rows, int M, int N, int tile) {
 
 namespace {
 
-// Rows a slot up to which the rows' gradient takes small tiles.
-constexpr int kFewRows = 32;
+// Small tiles where the large ones would leave the chip half empty, or, with up to
+// 24 rows a slot (a tile each, bound by reading the weights), the last round of
+// them. Measured with large and small tiles: 16 slots of 1024 x 512 (32 and 64
+// large tiles) at 12 rows 21 and 18 us, at 192 rows 37 and 19; 60 slots of 2048 x
+// 1408 (360 and 480) at 4 rows 101 and 70, 137 and 124, at 24 rows 104 and 80, 135
+// and 128, at 32 rows 106 and 110, 136 and 165 (slots of two small tiles); 64
+// slots of 4096 x 1024 (256: a full round) at 12 rows 104 and 121.
+constexpr int kFewRows = 24;
+
+bool take_small(int S, int max_rows, int N, int cus) {
+  const bool few = max_rows <= (int64_t)S * kFewRows;
+  const int64_t slots = S < max_rows ? S : max_rows;
+  const int64_t tiles = (few ? slots : (int64_t)max_rows / Large::kRowsM + slots) *
+                        ceil_div(N, Large::kColsN);
+  const int64_t rounds = (tiles + cus - 1) / cus;
+  return 2 * tiles <= cus || (few && 20 * tiles < 19 * rounds * cus);
+}
 
 }  // namespace
 
@@ -483,7 +497,7 @@ moe_status_t launch_gemm_backward_bf16(const void* dc, const int32_t* offsets, i
     typedef decltype(shape) SH;
     const int64_t items = (int64_t)(max_rows / SH::kRowsM + 1 + (S < max_rows ? S : max_rows)) *
                           ceil_div(N, SH::kColsN);
-    const int64_t blocks = (int64_t)device_cu_count() * (SH::kWaves == 8 ? 1 : 3);
+    const int64_t blocks = (int64_t)device_cu_count() * (SH::kWaves == 8 ? 1 : 2);
     grouped_grad_kernel<decltype(kind)::value, SH>
         <<<(int)std::min(items, blocks), SH::kThreads, 0, stream>>>(p);
   };
@@ -491,7 +505,7 @@ moe_status_t launch_gemm_backward_bf16(const void* dc, const int32_t* offsets, i
     if (h != nullptr) go(std::integral_constant<int, kRowsSwiglu>{}, shape);
     else go(std::integral_constant<int, kRows>{}, shape);
   };
-  if (max_rows <= (int64_t)S * kFewRows) by_kind(Small{});
+  if (take_small(S, max_rows, N, device_cu_count())) by_kind(Small{});
   else by_kind(Large{});
   return launch_status();
 }

@@ -2,19 +2,40 @@
 // the bf16 kernels), on the f32 matrix instructions: v_mfma_f32_32x32x2_f32
 // multiplies and adds in f32, 256 operations a cycle and compute unit.
 //
-// Tiles of 64 x 64, four waves of 32 x 32, slices of 32 contracted values in
-// LDS with the contraction outermost, so that a lane's operand is one value
-// beside its neighbours' in both products.
+// Four waves in 2 x 2 on a tile of TILE x TILE, fragments of 16 x 16
+// (v_mfma_f32_16x16x4_f32), slices of SLICE contracted values through registers
+// into LDS. An operand that is contiguous along the contraction keeps its rows
+// there, the others have the contraction outermost; the pitches put the 16 x 4
+// values that a wave reads at once on 64 banks.
 #include "grouped_tiles.h"
 #include "vec8.h"
 
 namespace moe {
 namespace {
 
-typedef float floatx16 __attribute__((ext_vector_type(16)));
+typedef float floatx4 __attribute__((ext_vector_type(4)));
+typedef int int32x4_t __attribute__((ext_vector_type(4)));
 
-constexpr int kTile32 = kGradTileF32, kSlice32 = 32, kThreads32 = 256;
-constexpr int kPitch = kTile32 + 4;
+constexpr int kThreads32 = 256;
+constexpr uint32_t kOOB = 0x80000000u;  // past every resource here
+
+// Large tiles for throughput; small ones, with a long slice, where there are
+// few: a fragment's chain of products is what takes the time then.
+template <int TILE_, int SLICE_>
+struct Shape32 {
+  static constexpr int TILE = TILE_, SLICE = SLICE_;
+};
+typedef Shape32<kGradTileF32, 64> Large32;
+typedef Shape32<32, 128> Small32;
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, uint32_t bytes) {
+  const uint64_t a = reinterpret_cast<uint64_t>(base);
+  const uint32_t lo = (uint32_t)uniform_i32((int)(uint32_t)a);
+  const uint32_t hi = (uint32_t)uniform_i32((int)(uint32_t)(a >> 32));
+  return __builtin_amdgcn_make_buffer_rsrc(
+      reinterpret_cast<void*>(((uint64_t)hi << 32) | lo), (short)0,
+      uniform_i32((int)bytes), 0x00020000);
+}
 
 struct Args32 {
   const float* m_side;  // dc [rows, Kd], or dc [rows, M]
@@ -26,151 +47,179 @@ struct Args32 {
   int out_bf16, accumulate, splits;
 };
 
-template <bool WEIGHTS>
+template <bool WEIGHTS, typename SH>
 __global__ __launch_bounds__(kThreads32) void grouped_grad_f32_kernel(Args32 p) {
-  __shared__ float ms[kSlice32][kPitch], ns[kSlice32][kPitch];
+  constexpr int TILE = SH::TILE, SLICE = SH::SLICE, FR = TILE / 32;
+  constexpr int kVec = TILE * SLICE / 4 / kThreads32;  // vectors of 4 of an operand, a thread
+  constexpr int kPitchT = TILE + 16, kPitchK = SLICE + 4;
+  __shared__ float4 m_part[(WEIGHTS ? SLICE * kPitchT : TILE * kPitchK) / 4];
+  __shared__ float4 n_part[SLICE * kPitchT / 4];
   __shared__ int32_t tp[WEIGHTS ? 1 : MOE_MAX_SLOTS + 1];
   __shared__ int32_t scratch[WEIGHTS ? 1 : kThreads32];
-  const int tid = threadIdx.x, lane = lane_id(), wave = tid / kWave;
+  const float* ms = reinterpret_cast<const float*>(m_part);
+  const float* ns = reinterpret_cast<const float*>(n_part);
+  const int tid = threadIdx.x, lane = lane_id(), wave = uniform_i32(tid / kWave);
   const int wm = wave >> 1, wn = wave & 1;
-  const int NT = ceil_div(p.N, kTile32), MT = WEIGHTS ? ceil_div(p.M, kTile32) : 0;
+  const int NT = ceil_div(p.N, TILE), MT = WEIGHTS ? ceil_div(p.M, TILE) : 0;
   int RT = 0;
   if constexpr (!WEIGHTS) {
-    tile_prefix<kThreads32, kTile32>(p.offsets, p.S, p.max_rows, tp, scratch);
-    RT = tp[p.S];
+    tile_prefix<kThreads32, TILE>(p.offsets, p.S, p.max_rows, tp, scratch);
+    RT = uniform_i32(tp[p.S]);
   }
+  const uint32_t m_row = (uint32_t)(WEIGHTS ? p.M : p.Kd) * 4u, n_row = (uint32_t)p.N * 4u;
   const int total = WEIGHTS ? p.S * p.splits * MT * NT : RT * NT;
   for (int item = blockIdx.x; item < total; item += gridDim.x) {
-    int s, m0 = 0, n0, row0, rows, split = 0;
+    int s, m0 = 0, n0, row0, rows, split = 0, lo, hi;
     if constexpr (WEIGHTS) {
       const int z = item / (MT * NT), t = item - z * MT * NT;
       s = z / p.splits;
       split = z - s * p.splits;
-      m0 = t / NT * kTile32;
-      n0 = t % NT * kTile32;
-      int lo, hi;
+      m0 = t / NT * TILE;
+      n0 = t % NT * TILE;
       slot_rows(p.offsets, s, p.max_rows, &lo, &hi);
-      const int each = ceil_div(ceil_div(hi - lo, kSlice32), p.splits) * kSlice32;
+      const int each = ceil_div(ceil_div(hi - lo, SLICE), p.splits) * SLICE;
       row0 = min(lo + split * each, hi);
       rows = min(hi - row0, each);
     } else {
       const int rt = item / NT;
-      n0 = item % NT * kTile32;
-      s = tile_slot(tp, p.S, rt);
-      int lo, hi;
+      n0 = item % NT * TILE;
+      s = uniform_i32(tile_slot(tp, p.S, rt));
       slot_rows(p.offsets, s, p.max_rows, &lo, &hi);
-      row0 = lo + (rt - tp[s]) * kTile32;
-      rows = min(kTile32, hi - row0);
+      row0 = lo + (rt - tp[s]) * TILE;
+      rows = min(TILE, hi - row0);
     }
+    row0 = uniform_i32(row0);
+    rows = uniform_i32(rows);
     const int depth = WEIGHTS ? rows : p.Kd;
-    // two vectors of 4 of each operand a thread; zeros past the ends
-    float4 mv[2], nv[2];
-    auto load = [&](int k0) {
+    int32x4_t mv[kVec], nv[kVec];
+    auto load = [&](int k0) {  // zeros past the ends
+      const int left = min(depth - k0, SLICE);
+      const __amdgpu_buffer_rsrc_t rm =
+          WEIGHTS ? make_rsrc(p.m_side + ((size_t)row0 + k0) * p.M, (uint32_t)left * m_row)
+                  : make_rsrc(p.m_side + (size_t)row0 * p.Kd, (uint32_t)rows * m_row);
+      const __amdgpu_buffer_rsrc_t rn =
+          make_rsrc(WEIGHTS ? p.n_side + ((size_t)row0 + k0) * p.N
+                            : p.n_side + ((size_t)s * p.Kd + k0) * p.N,
+                    (uint32_t)left * n_row);
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
+      for (int u = 0; u < kVec; ++u) {
         const int q = tid + u * kThreads32;
-        const int k = k0 + q / 16, c = q % 16 * 4;
-        const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-        const float* n = WEIGHTS ? p.n_side + ((size_t)row0 + k) * p.N + n0 + c
-                                 : p.n_side + ((size_t)s * p.Kd + k) * p.N + n0 + c;
-        nv[u] = k < depth && n0 + c < p.N ? *reinterpret_cast<const float4*>(n) : zero;
+        const int k = q / (TILE / 4), c = q % (TILE / 4) * 4;
+        nv[u] = __builtin_amdgcn_raw_buffer_load_b128(
+            rn, n0 + c < p.N ? (uint32_t)k * n_row + (uint32_t)(n0 + c) * 4u : kOOB, 0, 0);
         if constexpr (WEIGHTS) {
-          mv[u] = k < depth && m0 + c < p.M ? *reinterpret_cast<const float4*>(
-                                                  p.m_side + ((size_t)row0 + k) * p.M + m0 + c)
-                                            : zero;
+          mv[u] = __builtin_amdgcn_raw_buffer_load_b128(
+              rm, m0 + c < p.M ? (uint32_t)k * m_row + (uint32_t)(m0 + c) * 4u : kOOB, 0, 0);
         } else {
-          const int r = q / 8, kk = k0 + q % 8 * 4;
-          mv[u] = r < rows && kk < p.Kd ? *reinterpret_cast<const float4*>(
-                                              p.m_side + ((size_t)row0 + r) * p.Kd + kk)
-                                        : zero;
+          const int r = q / (SLICE / 4), kk = k0 + q % (SLICE / 4) * 4;
+          mv[u] = __builtin_amdgcn_raw_buffer_load_b128(
+              rm, kk < p.Kd ? (uint32_t)r * m_row + (uint32_t)kk * 4u : kOOB, 0, 0);
         }
       }
     };
     auto store = [&]() {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
+      for (int u = 0; u < kVec; ++u) {
         const int q = tid + u * kThreads32;
-        *reinterpret_cast<float4*>(&ns[q / 16][q % 16 * 4]) = nv[u];
-        if constexpr (WEIGHTS) {
-          *reinterpret_cast<float4*>(&ms[q / 16][q % 16 * 4]) = mv[u];
-        } else {
-          const int r = q / 8, kk = q % 8 * 4;
-          ms[kk][r] = mv[u].x;
-          ms[kk + 1][r] = mv[u].y;
-          ms[kk + 2][r] = mv[u].z;
-          ms[kk + 3][r] = mv[u].w;
-        }
+        const int k = q / (TILE / 4), c = q % (TILE / 4);
+        n_part[k * (kPitchT / 4) + c] = __builtin_bit_cast(float4, nv[u]);
+        if constexpr (WEIGHTS)
+          m_part[k * (kPitchT / 4) + c] = __builtin_bit_cast(float4, mv[u]);
+        else
+          m_part[q / (SLICE / 4) * (kPitchK / 4) + q % (SLICE / 4)] =
+              __builtin_bit_cast(float4, mv[u]);
       }
     };
-    floatx16 acc = {};
+    // acc[j][i]: 16 columns j by 16 rows i of the wave
+    floatx4 acc[FR][FR] = {};
+    const int mr = wm * (TILE / 2) + (lane & 15), nc = wn * (TILE / 2) + (lane & 15), kl = lane >> 4;
     if (depth > 0) load(0);
-    for (int k0 = 0; k0 < depth; k0 += kSlice32) {
+    for (int k0 = 0; k0 < depth; k0 += SLICE) {
       __syncthreads();  // the slice before has been read
       store();
       __syncthreads();
-      if (k0 + kSlice32 < depth) load(k0 + kSlice32);
+      if (k0 + SLICE < depth) load(k0 + SLICE);
+      const int steps = min(SLICE, depth - k0);  // what lies behind is zeros
+#pragma unroll 8
+      for (int k = 0; k < steps; k += 4) {
+        float a[FR], b[FR];
 #pragma unroll
-      for (int k = 0; k < kSlice32; k += 2) {
-        const float a = ms[k + (lane >> 5)][wm * 32 + (lane & 31)];
-        const float b = ns[k + (lane >> 5)][wn * 32 + (lane & 31)];
-        acc = __builtin_amdgcn_mfma_f32_32x32x2f32(b, a, acc, 0, 0, 0);
+        for (int f = 0; f < FR; ++f) {
+          a[f] = WEIGHTS ? ms[(k + kl) * kPitchT + mr + f * 16] : ms[(mr + f * 16) * kPitchK + k + kl];
+          b[f] = ns[(k + kl) * kPitchT + nc + f * 16];
+        }
+#pragma unroll
+        for (int j = 0; j < FR; ++j)
+#pragma unroll
+          for (int i = 0; i < FR; ++i)
+            acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x4f32(b[j], a[i], acc[j][i], 0, 0, 0);
       }
     }
-    // register v: column 8 (v / 4) + 4 (lane / 32) + v % 4, row lane % 32
-    const int r = wm * 32 + (lane & 31);
-    if (WEIGHTS ? m0 + r >= p.M : r >= rows) continue;
+    // register v of acc[j][i]: column 4 (lane / 16) + v, row lane % 16
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const int col = n0 + wn * 32 + 8 * g + 4 * (lane >> 5);
-      if (col >= p.N) continue;
-      float4 o = make_float4(acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]);
-      if constexpr (WEIGHTS) {
-        const size_t at = ((((size_t)split * p.S + s) * p.M) + m0 + r) * p.N + col;
-        if (p.out_bf16) {
-          uint2* q = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at);
-          if (p.accumulate) {
-            const uint2 v = *q;
-            o.x = bf16_to_f32(v.x & 0xffffu) + o.x;
-            o.y = bf16_to_f32(v.x >> 16) + o.y;
-            o.z = bf16_to_f32(v.y & 0xffffu) + o.z;
-            o.w = bf16_to_f32(v.y >> 16) + o.w;
+    for (int i = 0; i < FR; ++i) {
+      const int r = mr + i * 16;
+      if (WEIGHTS ? m0 + r >= p.M : r >= rows) continue;
+#pragma unroll
+      for (int j = 0; j < FR; ++j) {
+        const int col = n0 + wn * (TILE / 2) + j * 16 + 4 * kl;
+        if (col >= p.N) continue;
+        float o[4] = {acc[j][i][0], acc[j][i][1], acc[j][i][2], acc[j][i][3]};
+        if constexpr (WEIGHTS) {
+          const size_t at = ((((size_t)split * p.S + s) * p.M) + m0 + r) * p.N + col;
+          if (p.out_bf16) {
+            uint2* q = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at);
+            if (p.accumulate) {
+              const uint2 v = *q;
+              o[0] = bf16_to_f32(v.x & 0xffffu) + o[0];
+              o[1] = bf16_to_f32(v.x >> 16) + o[1];
+              o[2] = bf16_to_f32(v.y & 0xffffu) + o[2];
+              o[3] = bf16_to_f32(v.y >> 16) + o[3];
+            }
+            *q = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+          } else {
+            float4* q = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
+            if (p.accumulate) {
+              const float4 v = *q;
+              o[0] = v.x + o[0];
+              o[1] = v.y + o[1];
+              o[2] = v.z + o[2];
+              o[3] = v.w + o[3];
+            }
+            *q = make_float4(o[0], o[1], o[2], o[3]);
           }
-          *q = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+        } else if (p.h != nullptr) {
+          const size_t at = ((size_t)row0 + r) * 2 * p.N + col;
+          const float4 g4 = *reinterpret_cast<const float4*>(p.h + at);
+          const float4 u4 = *reinterpret_cast<const float4*>(p.h + at + p.N);
+          float gt[4] = {g4.x, g4.y, g4.z, g4.w}, u[4] = {u4.x, u4.y, u4.z, u4.w};
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const float sg = 1.0f / (1.0f + expf(-gt[v]));
+            const float silu = gt[v] * sg;
+            gt[v] = o[v] * u[v] * (sg + silu * (1.0f - sg));
+            u[v] = o[v] * silu;
+          }
+          float* q = static_cast<float*>(p.out) + at;
+          *reinterpret_cast<float4*>(q) = make_float4(gt[0], gt[1], gt[2], gt[3]);
+          *reinterpret_cast<float4*>(q + p.N) = make_float4(u[0], u[1], u[2], u[3]);
         } else {
-          float4* q = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
-          if (p.accumulate) {
-            const float4 v = *q;
-            o.x = v.x + o.x; o.y = v.y + o.y; o.z = v.z + o.z; o.w = v.w + o.w;
-          }
-          *q = o;
+          *reinterpret_cast<float4*>(static_cast<float*>(p.out) + ((size_t)row0 + r) * p.N + col) =
+              make_float4(o[0], o[1], o[2], o[3]);
         }
-      } else if (p.h != nullptr) {
-        const size_t at = ((size_t)row0 + r) * 2 * p.N + col;
-        const float4 g4 = *reinterpret_cast<const float4*>(p.h + at);
-        const float4 u4 = *reinterpret_cast<const float4*>(p.h + at + p.N);
-        float d[4] = {o.x, o.y, o.z, o.w}, gt[4] = {g4.x, g4.y, g4.z, g4.w},
-              u[4] = {u4.x, u4.y, u4.z, u4.w};
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const float sg = 1.0f / (1.0f + expf(-gt[v]));
-          const float silu = gt[v] * sg;
-          gt[v] = d[v] * u[v] * (sg + silu * (1.0f - sg));
-          u[v] = d[v] * silu;
-        }
-        float* q = static_cast<float*>(p.out) + at;
-        *reinterpret_cast<float4*>(q) = make_float4(gt[0], gt[1], gt[2], gt[3]);
-        *reinterpret_cast<float4*>(q + p.N) = make_float4(u[0], u[1], u[2], u[3]);
-      } else {
-        *reinterpret_cast<float4*>(static_cast<float*>(p.out) + ((size_t)row0 + r) * p.N + col) = o;
       }
     }
   }
 }
 
+constexpr int kFewTiles = 3;  // large tiles a compute unit, below which small ones are taken
+
 int grid32(int64_t items) {
-  const int64_t most = 4 * (int64_t)device_cu_count();
+  const int64_t most = 3 * (int64_t)device_cu_count();  // as many as the LDS holds
   return items < most ? (int)items : (int)most;
 }
+
+bool few_tiles(int64_t large) { return large < kFewTiles * (int64_t)device_cu_count(); }
 
 // out[i] = (accumulate: out[i] +) the sum over the splits of part[split][i], 8 values a thread.
 template <typename OT>
@@ -220,9 +269,17 @@ moe_status_t launch_gemm_backward_f32(const void* dc, const int32_t* offsets, in
   p.S = S; p.max_rows = max_rows; p.N = N; p.Kd = Kd; p.splits = 1;
   p.h = static_cast<const float*>(h);
   p.out = out;
-  const int64_t items =
-      (int64_t)(max_rows / kTile32 + 1 + (S < max_rows ? S : max_rows)) * ceil_div(N, kTile32);
-  grouped_grad_f32_kernel<false><<<grid32(items), kThreads32, 0, stream>>>(p);
+  auto go = [&](auto shape) {
+    typedef decltype(shape) SH;
+    const int64_t items = (int64_t)(max_rows / SH::TILE + 1 + (S < max_rows ? S : max_rows)) *
+                          ceil_div(N, SH::TILE);
+    grouped_grad_f32_kernel<false, SH><<<grid32(items), kThreads32, 0, stream>>>(p);
+  };
+  if (few_tiles((int64_t)(max_rows / Large32::TILE + (S < max_rows ? S : max_rows)) *
+                ceil_div(N, Large32::TILE)))
+    go(Small32{});
+  else
+    go(Large32{});
   return launch_status();
 }
 
@@ -234,12 +291,19 @@ moe_status_t launch_gemm_weight_grad_f32(const void* dc, const void* a, const in
   p.n_side = static_cast<const float*>(a);
   p.offsets = offsets;
   p.S = S; p.max_rows = max_rows; p.M = M; p.N = N;
-  p.splits = grad_splits(S, max_rows, M, N, kTile32);
+  p.splits = grad_splits(S, max_rows, M, N, kGradTileF32);
   p.out = p.splits > 1 ? ws : dw;
   p.out_bf16 = p.splits > 1 ? 0 : !dw_f32;
   p.accumulate = p.splits > 1 ? 0 : accumulate;
-  const int64_t items = (int64_t)S * p.splits * ceil_div(M, kTile32) * ceil_div(N, kTile32);
-  grouped_grad_f32_kernel<true><<<grid32(items), kThreads32, 0, stream>>>(p);
+  auto go = [&](auto shape) {
+    typedef decltype(shape) SH;
+    const int64_t items = (int64_t)S * p.splits * ceil_div(M, SH::TILE) * ceil_div(N, SH::TILE);
+    grouped_grad_f32_kernel<true, SH><<<grid32(items), kThreads32, 0, stream>>>(p);
+  };
+  if (few_tiles((int64_t)S * p.splits * ceil_div(M, Large32::TILE) * ceil_div(N, Large32::TILE)))
+    go(Small32{});
+  else
+    go(Large32{});
   if (p.splits > 1)
     return launch_fold_splits(static_cast<const float*>(ws), p.splits, (size_t)S * M * N, dw, dw_f32,
                               accumulate, stream);

@@ -17,7 +17,8 @@ template <typename XT, int VPT, int L>
 __global__ __launch_bounds__(L == 0 ? 1024 : kNormGroupThreads) void layer_norm_kernel(
     const XT* x, const XT* residual, const XT* __restrict__ gamma, const XT* __restrict__ beta,
     int T, int H, float eps, XT* residual_out, XT* y, uint8_t* __restrict__ q, float inv) {
-  __shared__ float part[3][16];
+  __shared__ RowParts part;
+  constexpr bool kGuess = L == 0 && VPT == 1;
   constexpr int kRows = L == 0 ? 1 : kNormGroupThreads / (L == 0 ? 1 : L);
   const int64_t t = (int64_t)folded_block() * kRows + (L == 0 ? 0 : threadIdx.x / (L == 0 ? 1 : L));
   if (t >= T) return;
@@ -37,10 +38,26 @@ __global__ __launch_bounds__(L == 0 ? 1024 : kNormGroupThreads) void layer_norm_
 #pragma unroll
         for (int i = 0; i < 8; ++i) h[j][i] += r[i];
       }
-      if (residual_out != nullptr) store8(residual_out + row + v * 8, h[j]);
+      if (!kGuess && residual_out != nullptr) store8(residual_out + row + v * 8, h[j]);
     }
   }
-  normalize_row<true, VPT, L>(h, first, stride, nvec, H, eps, part);
+  float guess = 0.f, keep[8] = {};
+  if constexpr (kGuess) {
+    float v[8], r[8] = {};
+    load8(x + row, v);
+    if (residual != nullptr) load8(residual + row, r);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] += r[i];
+      keep[i] = h[0][i];
+    }
+    guess = mean8(v);
+  }
+  normalize_row<true, VPT, L>(h, first, stride, nvec, H, eps, part, guess);
+  // behind the first barrier: residual_out may be x or the residual, whose first
+  // values every thread reads
+  if constexpr (kGuess)
+    if (first < nvec && residual_out != nullptr) store8(residual_out + row + first * 8, keep);
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     const int v = first + j * stride;

@@ -21,26 +21,61 @@ template <typename XT, bool CENTRED, int VPT, int L>
 __global__ __launch_bounds__(L == 0 ? 1024 : kNormGroupThreads) void norm_backward_kernel(
     const XT* dy, const XT* x, const XT* __restrict__ gamma, const XT* dresidual, int T, int H,
     float eps, XT* dx, float* __restrict__ pg, float* __restrict__ pb, int part_stride) {
-  __shared__ float part[5][16];
+  __shared__ RowParts part;
   constexpr int kRows = L == 0 ? 1 : kNormGroupThreads / (L == 0 ? 1 : L);
   const int group = L == 0 ? 0 : threadIdx.x / (L == 0 ? 1 : L);
   const int first = L == 0 ? threadIdx.x : threadIdx.x % (L == 0 ? 1 : L);
   const int stride = L == 0 ? blockDim.x : L;
   const int nvec = H / 8;
   const float over = 1.0f / (float)H;
+  const int64_t step = (int64_t)gridDim.x * kRows;
   float ag[VPT][8] = {}, ab[VPT][8] = {};
-  for (int64_t t = (int64_t)blockIdx.x * kRows + group; t < T; t += (int64_t)gridDim.x * kRows) {
+  // A row's vectors are asked for while the row before is worked on (rows of one
+  // vector a thread: for wider ones the registers would not hold them).
+  constexpr bool kAhead = VPT == 1;
+  typedef decltype(raw8(x)) Raw;
+  Raw nx = {}, nd = {}, nr = {}, ng = {};
+  constexpr bool kGuess = CENTRED && L == 0 && VPT == 1;
+  const bool mine = first < nvec;
+  const bool add = dresidual != nullptr && dx != nullptr;
+  auto ask = [&](int64_t t) {
+    if (t < T && mine) {
+      const size_t at = (size_t)t * H + first * 8;
+      nx = raw8(x + at);
+      if constexpr (kGuess) ng = raw8(x + (size_t)t * H);
+      nd = raw8(dy + at);
+      if (add) nr = raw8(dresidual + at);
+    }
+  };
+  int64_t t = (int64_t)blockIdx.x * kRows + group;
+  if constexpr (kAhead) ask(t);
+  for (; t < T; t += step) {
     const size_t row = (size_t)t * H;
     float h[VPT][8] = {}, d[VPT][8] = {};
+    Raw res = nr;
+    float guess = 0.f;
+    if constexpr (kGuess) {
+      float v[8];
+      unpack8(ng, v);
+      guess = mean8(v);
+    }
+    if constexpr (kAhead) {
+      if (mine) {
+        unpack8(nx, h[0]);
+        unpack8(nd, d[0]);
+      }
+      ask(t + step);
+    } else {
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int v = first + j * stride;
-      if (v < nvec) {
-        load8(x + row + v * 8, h[j]);
-        load8(dy + row + v * 8, d[j]);
+      for (int j = 0; j < VPT; ++j) {
+        const int v = first + j * stride;
+        if (v < nvec) {
+          load8(x + row + v * 8, h[j]);
+          load8(dy + row + v * 8, d[j]);
+        }
       }
     }
-    const double r = normalize_row<CENTRED, VPT, L>(h, first, stride, nvec, H, eps, part);
+    const float r = normalize_row<CENTRED, VPT, L>(h, first, stride, nvec, H, eps, part, guess);
     float sg = 0.f, sn = 0.f;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
@@ -58,20 +93,23 @@ __global__ __launch_bounds__(L == 0 ? 1024 : kNormGroupThreads) void norm_backwa
         }
       }
     }
-    sn = lanes_sum<L>(sn, part[3]) * over;
-    if constexpr (CENTRED) sg = lanes_sum<L>(sg, part[4]) * over;
+    const float2 sums = lanes_sum2<L>(sn, sg, part.grad);
+    sn = sums.x * over;
+    sg = sums.y * over;
     if (dx != nullptr) {
-      const float rf = (float)r;
 #pragma unroll
       for (int j = 0; j < VPT; ++j) {
         const int v = first + j * stride;
         if (v < nvec) {
           float o[8] = {};
-          if (dresidual != nullptr) load8(dresidual + row + v * 8, o);
+          if (dresidual != nullptr) {
+            if constexpr (kAhead) unpack8(res, o);
+            else load8(dresidual + row + v * 8, o);
+          }
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const float c = CENTRED ? fmaf(-h[j][i], sn, d[j][i] - sg) : fmaf(-h[j][i], sn, d[j][i]);
-            o[i] = fmaf(c, rf, o[i]);
+            o[i] = fmaf(c, r, o[i]);
           }
           store8(dx + row + v * 8, o);
         }
@@ -142,13 +180,18 @@ __global__ __launch_bounds__(256) void fold_columns_kernel(const float* __restri
   *reinterpret_cast<float4*>(out + c) = s;
 }
 
-// Blocks that share the rows: about 4096 waves, 16 a compute unit, at most 1024.
+// Blocks that share the rows: whole rounds of 256 compute units with about 16
+// waves each (8192 rows of 5120, ten waves a row: 512 blocks 96 us, 409 117), and
+// 16 rows a block, or no more than 8 MB of partial sums, which are written and
+// read once more (2048 rows of 2048: 512 blocks 20 us, 1024 23).
 int norm_blocks(int T, int H) {
   if (T == 0) return 0;
   const int L = norm_lanes(H / 8);
   const int waves = L == 0 ? std::min(16, ceil_div(H / 8, kWave)) : kNormGroupThreads / kWave;
   const int64_t rows = L == 0 ? 1 : kNormGroupThreads / L;
-  return (int)std::min<int64_t>((T + rows - 1) / rows, std::min(1024, 4096 / waves));
+  const int64_t most = std::min(256 * std::clamp((16 + waves / 2) / waves, 1, 4),
+                                std::max({256, (1 << 20) / H, T / 16}));
+  return (int)std::min((T + rows - 1) / rows, most);
 }
 
 template <typename XT, bool CENTRED>

@@ -23,6 +23,33 @@ __device__ __forceinline__ void load8(const float* p, float* v) {
   v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
 
+// The same in two steps, for a load that is asked for early: the vector as it
+// lies in memory, and its values.
+struct Raw8B {
+  uint4 q;
+};
+struct Raw8F {
+  float4 a, b;
+};
+__device__ __forceinline__ Raw8B raw8(const uint16_t* p) {
+  return {*reinterpret_cast<const uint4*>(p)};
+}
+__device__ __forceinline__ Raw8F raw8(const float* p) {
+  return {*reinterpret_cast<const float4*>(p), *reinterpret_cast<const float4*>(p + 4)};
+}
+__device__ __forceinline__ void unpack8(const Raw8B& r, float* v) {
+  const uint32_t w[4] = {r.q.x, r.q.y, r.q.z, r.q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = bf16_to_f32(w[i] & 0xffffu);
+    v[2 * i + 1] = bf16_to_f32(w[i] >> 16);
+  }
+}
+__device__ __forceinline__ void unpack8(const Raw8F& r, float* v) {
+  v[0] = r.a.x; v[1] = r.a.y; v[2] = r.a.z; v[3] = r.a.w;
+  v[4] = r.b.x; v[5] = r.b.y; v[6] = r.b.z; v[7] = r.b.w;
+}
+
 __device__ __forceinline__ void store8(uint16_t* p, const float* v) {
   uint4 q;
   q.x = pack_bf16x2(v[0], v[1]);
