@@ -737,8 +737,12 @@ def combine_backward(dout: torch.Tensor, y: Optional[torch.Tensor], pair_row: to
             raise ValueError("w_masked must hold T*K entries")
         if y is None:
             raise ValueError("the weights' gradient needs y")
-        dw = (_empty((T, K), torch.float32, dout) if dw is None
-              else _dev(dw, "dw", torch.float32, (T, K)))
+        if dw is not None:
+            _dev(dw, "dw", torch.float32, (T, K))
+        elif w_masked.shape == (T, K):
+            dw = torch.empty_like(w_masked)
+        else:
+            dw = _empty((T, K), torch.float32, dout)
     elif dw is not None:
         raise ValueError("dw needs w_masked")
     if dy.shape[0] == 0:  # a share without pairs: an empty tensor has no address to pass

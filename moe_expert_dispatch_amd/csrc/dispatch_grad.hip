@@ -71,7 +71,7 @@ __device__ __forceinline__ void store8(__amdgpu_buffer_rsrc_t r, uint32_t off, c
   __builtin_amdgcn_raw_buffer_store_b128(b, r, (int)(off + 16u), 0, kNonTemporal);
 }
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 typedef float Parts[MOE_MAX_TOPK];  // a wave's parts of the token's dot products
 
 // Adds the wave's parts of the dot products of pairs k0 .. k0 + KMAX.
@@ -232,8 +232,9 @@ __global__ __launch_bounds__(kThreads) void permute_backward_kernel(
   store_dots(part, rows, K, dw + (size_t)t * K);
 }
 
-// As the combine: 32 bytes of each row a thread, whole waves, at most 256
-// threads; K <= 4 keeps half the rows in flight.
+// 32 bytes of each row a thread, whole waves, as many as hold the row up to 512
+// threads (2056 values of f32 are 257 vectors: 256 threads would go round twice);
+// K <= 4 keeps half the rows in flight.
 int row_threads(int H, int vec) {
   return std::min(kThreads, std::max(kWave, ceil_div(H / 8, vec * kWave) * kWave));
 }

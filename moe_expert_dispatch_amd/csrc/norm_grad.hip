@@ -149,33 +149,49 @@ __global__ __launch_bounds__(L == 0 ? 1024 : kNormGroupThreads) void norm_backwa
   }
 }
 
-// out[c] = the sum over n rows of part [n, H], or zero for none: 16 lines of
-// a block add every 16th row, then the lines are added in order.
+// out[c] = the sum over n rows of part [n, H], or zero for none: 32 lines of a
+// block add every 32nd row of 32 columns, 16 rows asked for at a time, then the
+// lines are added in order.
 __global__ __launch_bounds__(256) void fold_columns_kernel(const float* __restrict__ pg,
                                                            const float* __restrict__ pb, int n,
                                                            int H, float* __restrict__ dgamma,
                                                            float* __restrict__ dbeta) {
+  constexpr int kLines = 32, kAhead = 16;
   const float* part = blockIdx.y == 0 ? pg : pb;
   float* out = blockIdx.y == 0 ? dgamma : dbeta;
   if (out == nullptr) return;
-  __shared__ float4 lines[16][16];
-  const int line = threadIdx.x / 16, at = threadIdx.x % 16;
-  const int c = (blockIdx.x * 16 + at) * 4;
+  __shared__ float4 lines[kLines][8];
+  const int line = threadIdx.x / 8, at = threadIdx.x % 8;
+  const int c = (blockIdx.x * 8 + at) * 4;
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
   if (c < H) {
-#pragma unroll 4
-    for (int k = line; k < n; k += 16) {
-      const float4 v = *reinterpret_cast<const float4*>(part + (size_t)k * H + c);
-      s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+    for (int k0 = line; k0 < n; k0 += kLines * kAhead) {
+      float4 v[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int k = k0 + u * kLines;
+        v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k < n) v[u] = *reinterpret_cast<const float4*>(part + (size_t)k * H + c);
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        s.x += v[u].x;
+        s.y += v[u].y;
+        s.z += v[u].z;
+        s.w += v[u].w;
+      }
     }
   }
   lines[line][at] = s;
   __syncthreads();
   if (line != 0 || c >= H) return;
 #pragma unroll
-  for (int k = 1; k < 16; ++k) {
+  for (int k = 1; k < kLines; ++k) {
     const float4 v = lines[k][at];
-    s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+    s.x += v.x;
+    s.y += v.y;
+    s.z += v.z;
+    s.w += v.w;
   }
   *reinterpret_cast<float4*>(out + c) = s;
 }
@@ -252,7 +268,7 @@ moe_status_t launch_norm_backward(bool centred, const void* dy, const void* x, c
     else go(F32{}, std::false_type{});
   }
   if (sums && blocks != 1)
-    fold_columns_kernel<<<dim3(ceil_div(H, 64), dbeta != nullptr ? 2 : 1), 256, 0, stream>>>(
+    fold_columns_kernel<<<dim3(ceil_div(H, 32), dbeta != nullptr ? 2 : 1), 256, 0, stream>>>(
         pg, pb, blocks, H, dgamma, dbeta);
   return launch_status();
 }

@@ -3,14 +3,23 @@
 // the result):  act[r, j] = silu(h[r, j]) * h[r, I + j],  h [rows, 2I].
 //
 // Bound by the bytes, three values of the row's type for each result. A block
-// takes 1024 consecutive vectors of 8 results, whatever the rows' width.
+// takes 512 consecutive vectors of 8 results, whatever the rows' width.
 #include "common.h"
 #include "vec8.h"
 
 namespace moe {
 namespace {
 
-constexpr int kSwigluThreads = 256, kSwigluVec = 4;
+constexpr int kSwigluThreads = 256, kSwigluVec = 2;
+
+// silu(g) u. For bf16 results the quotient's and the exponential's fast forms,
+// as in the fused product: their few 2^-24 are far below the rounding.
+__device__ __forceinline__ float gate(float g, float u, const uint16_t*) {
+  return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
+}
+__device__ __forceinline__ float gate(float g, float u, const float*) {
+  return g / (1.0f + expf(-g)) * u;
+}
 
 template <typename XT>
 __global__ __launch_bounds__(kSwigluThreads) void swiglu_kernel(const XT* __restrict__ h,
@@ -18,11 +27,12 @@ __global__ __launch_bounds__(kSwigluThreads) void swiglu_kernel(const XT* __rest
                                                                 int S, int max_rows, int I,
                                                                 XT* __restrict__ act) {
   const uint32_t nvec = (uint32_t)I / 8u;
-  const int rows = max(0, min(offsets[S], max_rows));
+  const size_t rows = (size_t)max(0, min(offsets[S], max_rows));
   const uint64_t start = (uint64_t)folded_block() * (kSwigluThreads * kSwigluVec);
   const uint64_t row0 = start / nvec;
   const uint32_t rest = (uint32_t)(start - row0 * nvec);
-  float g[kSwigluVec][8], u[kSwigluVec][8];
+  typedef decltype(raw8(h)) Raw;
+  Raw g[kSwigluVec] = {}, u[kSwigluVec] = {};
   size_t row[kSwigluVec];
   uint32_t col[kSwigluVec];
 #pragma unroll
@@ -31,17 +41,20 @@ __global__ __launch_bounds__(kSwigluThreads) void swiglu_kernel(const XT* __rest
     const uint32_t down = q / nvec;
     row[k] = (size_t)row0 + down;
     col[k] = (q - down * nvec) * 8u;
-    if (row[k] < (size_t)rows) {
-      load8(h + row[k] * 2 * I + col[k], g[k]);
-      load8(h + row[k] * 2 * I + I + col[k], u[k]);
+    if (row[k] < rows) {
+      g[k] = raw8(h + row[k] * 2 * I + col[k]);
+      u[k] = raw8(h + row[k] * 2 * I + I + col[k]);
     }
   }
 #pragma unroll
   for (int k = 0; k < kSwigluVec; ++k) {
-    if (row[k] >= (size_t)rows) continue;
+    if (row[k] >= rows) continue;
+    float a[8], b[8];
+    unpack8(g[k], a);
+    unpack8(u[k], b);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) g[k][i] = g[k][i] / (1.0f + expf(-g[k][i])) * u[k][i];
-    store8(act + row[k] * I + col[k], g[k]);
+    for (int i = 0; i < 8; ++i) a[i] = gate(a[i], b[i], h);
+    store8(act + row[k] * I + col[k], a);
   }
 }
 
