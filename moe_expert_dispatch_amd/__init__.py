@@ -573,10 +573,12 @@ def _norm_backward(what, dy, x, gamma, eps, dresidual, dx, sums, ws):
     sums = [torch.empty_like(gamma, dtype=torch.float32) if s is None
             else _dev(s, "dgamma and dbeta", torch.float32, (H,)) for s in sums]
     if ws is None:
-        ws = x.new_empty(norm_backward_workspace_size(T, H), dtype=torch.uint8)
+        need = norm_backward_workspace_size(T, H)
+        ws = x.new_empty(need, dtype=torch.uint8) if need else None
     _launch(what, x, (dy, gamma, dresidual, dx, *sums, ws), dy.data_ptr(), x.data_ptr(),
             gamma.data_ptr(), _ptr(dresidual), _DT[dt], T, H, eps, dx.data_ptr(),
-            *[s.data_ptr() for s in sums], ws.data_ptr(), ws.numel() * ws.element_size())
+            *[s.data_ptr() for s in sums], _ptr(ws),
+            0 if ws is None else ws.numel() * ws.element_size())
     return (dx, *sums)
 
 

@@ -149,6 +149,178 @@ __global__ __launch_bounds__(L == 0 ? 1024 : kNormGroupThreads) void norm_backwa
   }
 }
 
+// The whole gradient of a few rows in one launch: blocks 0 .. T-1 give a row of
+// dx each, the others 64 columns of dgamma and dbeta each, for which they form
+// every row's mean and deviation once more, a wave to a row.
+constexpr int kFewRows = 64;
+constexpr int kColumns = 64;  // of a block
+
+// A wave's row: its mean and 1 / deviation, in f64 from f32 sums or, where those
+// will not do (normalize_row), from f64 ones.
+template <typename XT, bool CENTRED>
+__device__ __forceinline__ void wave_row(const XT* x, int nvec, int H, float eps, double* mean,
+                                         double* r) {
+  const float width = (float)H;
+  float m = 0.f, d = 0.f, ss = 0.f, var = 0.f;
+  auto spread = [&]() {
+    float sd = 0.f;
+    ss = 0.f;
+    for (int v0 = lane_id(); v0 < nvec; v0 += 4 * kWave) {  // four vectors in flight
+      decltype(raw8(x)) q[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (v0 + u * kWave < nvec) q[u] = raw8(x + (v0 + u * kWave) * 8);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (v0 + u * kWave >= nvec) continue;
+        float h[8];
+        unpack8(q[u], h);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float c = CENTRED ? h[i] - m : h[i];
+          ss = fmaf(c, c, ss);
+          sd += c;
+        }
+      }
+    }
+    ss = wave_sum(ss);
+    if constexpr (CENTRED) d = wave_sum(sd) / width;
+    var = (CENTRED ? fmaxf(ss / width - d * d, 0.f) : ss / width) + eps;
+  };
+  if constexpr (CENTRED) {
+    float h[8];
+    load8(x, h);
+    m = mean8(h);
+  }
+  spread();
+  if constexpr (CENTRED) {
+    if (!(var - eps >= d * d)) {
+      m += d;
+      spread();
+    }
+  }
+  if (var >= kLeastSquares && var >= d * d && ss < INFINITY) {
+    *mean = (double)m + (double)d;
+    *r = 1.0 / sqrt((double)var);
+    return;
+  }
+  double at = 0.0;
+  if constexpr (CENTRED) {
+    for (int v = lane_id(); v < nvec; v += kWave) {
+      float h[8];
+      load8(x + v * 8, h);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) at += (double)h[i];
+    }
+    at = lanes_sum_f64<64>(at, nullptr) / H;
+  }
+  double sq = 0.0;
+  for (int v = lane_id(); v < nvec; v += kWave) {
+    float h[8];
+    load8(x + v * 8, h);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const double c = (double)h[i] - at;
+      sq = fma(c, c, sq);
+    }
+  }
+  *mean = at;
+  *r = 1.0 / sqrt(lanes_sum_f64<64>(sq, nullptr) / H + (double)eps);
+}
+
+template <typename XT, bool CENTRED>
+__global__ __launch_bounds__(1024) void norm_backward_few_kernel(
+    const XT* dy, const XT* x, const XT* __restrict__ gamma, const XT* dresidual, int T, int H,
+    float eps, int row_blocks, XT* dx, float* __restrict__ dgamma, float* __restrict__ dbeta) {
+  const int nvec = H / 8;
+  if ((int)blockIdx.x < row_blocks) {
+    __shared__ RowParts part;
+    const size_t at = (size_t)blockIdx.x * H + threadIdx.x * 8;
+    const bool mine = (int)threadIdx.x < nvec;
+    float h[1][8] = {}, d[8] = {}, o[8] = {}, w[8] = {}, guess = 0.f;
+    if constexpr (CENTRED) {
+      float v[8];
+      load8(x + (size_t)blockIdx.x * H, v);
+      guess = mean8(v);
+    }
+    if (mine) {
+      load8(x + at, h[0]);
+      load8(dy + at, d);
+      if (dresidual != nullptr) load8(dresidual + at, o);
+      load8(gamma + threadIdx.x * 8, w);
+    }
+    const float r =
+        normalize_row<CENTRED, 1, 0>(h, threadIdx.x, blockDim.x, nvec, H, eps, part, guess);
+    float sg = 0.f, sn = 0.f;
+    if (mine) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        d[i] *= w[i];
+        sn = fmaf(d[i], h[0][i], sn);
+        sg += d[i];
+      }
+    }
+    const float2 sums = lanes_sum2<0>(sn, sg, part.grad);
+    sn = sums.x / (float)H;
+    sg = CENTRED ? sums.y / (float)H : 0.f;
+    if (mine) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = fmaf(fmaf(-h[0][i], sn, d[i] - sg), r, o[i]);
+      store8(dx + at, o);
+    }
+    return;
+  }
+  __shared__ double mean[kFewRows], dev[kFewRows];
+  __shared__ float sums[2][16][kColumns];
+  const int wave = threadIdx.x / kWave, waves = blockDim.x / kWave;
+  for (int t = wave; t < T; t += waves) {
+    double m, r;
+    wave_row<XT, CENTRED>(x + (size_t)t * H, nvec, H, eps, &m, &r);
+    if (lane_id() == 0) {
+      mean[t] = m;
+      dev[t] = r;
+    }
+  }
+  __syncthreads();
+  // 8 lanes to the 64 columns of a row, every 8th row of the wave's
+  const int v = (blockIdx.x - row_blocks) * (kColumns / 8) + (lane_id() & 7);
+  float ag[8] = {}, ab[8] = {};
+  if (v < nvec) {
+    for (int t = threadIdx.x / 8; t < T; t += blockDim.x / 8) {
+      float h[8], d[8];
+      load8(x + (size_t)t * H + v * 8, h);
+      load8(dy + (size_t)t * H + v * 8, d);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float n = (float)((CENTRED ? (double)h[i] - mean[t] : (double)h[i]) * dev[t]);
+        ag[i] = fmaf(d[i], n, ag[i]);
+        ab[i] += d[i];
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+#pragma unroll
+    for (int o = 8; o < kWave; o *= 2) {
+      ag[i] += __shfl_xor(ag[i], o, kWave);
+      if constexpr (CENTRED) ab[i] += __shfl_xor(ab[i], o, kWave);
+    }
+    if (lane_id() < 8) {
+      sums[0][wave][lane_id() * 8 + i] = ag[i];
+      sums[1][wave][lane_id() * 8 + i] = ab[i];
+    }
+  }
+  __syncthreads();
+  const int c = (blockIdx.x - row_blocks) * kColumns + (threadIdx.x & 63);
+  const int which = threadIdx.x / kColumns;
+  if (which > 1 || c >= H) return;
+  float* out = which == 0 ? dgamma : dbeta;
+  if (out == nullptr) return;
+  float s = 0.f;
+  for (int w = 0; w < waves; ++w) s += sums[which][w][threadIdx.x & 63];
+  out[c] = s;
+}
+
 // out[c] = the sum over n rows of part [n, H], or zero for none: 32 lines of a
 // block add every 32nd row of 32 columns, 16 rows asked for at a time, then the
 // lines are added in order.
@@ -210,6 +382,35 @@ int norm_blocks(int T, int H) {
   return (int)std::min((T + rows - 1) / rows, most);
 }
 
+// Up to there one launch takes less than two with the host's time for the second
+// one, 4 us a call: 2 rows of 2048 on the GPU 4.2 us (two launches 6.5), 16 6.2
+// (6.5), 64 11.6 (6.8); issued one after the other 11, 11 and 11.7 us a call (15.5).
+// 64 rows of 4096 20 and 15.6.
+bool take_few(int T, int H) {
+  return T > 1 && T <= kFewRows && H <= 8192 && (int64_t)T * H <= 1 << 17;
+}
+
+template <typename XT, bool CENTRED>
+void launch_few(const void* dy, const void* x, const void* gamma, const void* dresidual, int T,
+                int H, float eps, void* dx, float* dgamma, float* dbeta, hipStream_t stream) {
+  // enough waves that each has a few rows for the columns' blocks
+  const int threads = std::max({256, ceil_div(H / 8, kWave) * kWave, std::min(16, T) * kWave});
+  const int columns = dgamma != nullptr || dbeta != nullptr ? ceil_div(H, kColumns) : 0;
+  auto go = [&](int rows, int cols) {
+    if (rows + cols > 0)
+      norm_backward_few_kernel<XT, CENTRED><<<rows + cols, threads, 0, stream>>>(
+          static_cast<const XT*>(dy), static_cast<const XT*>(x), static_cast<const XT*>(gamma),
+          static_cast<const XT*>(dresidual), T, H, eps, rows, static_cast<XT*>(dx), dgamma, dbeta);
+  };
+  const int rows = dx != nullptr ? T : 0;
+  if (dx != x && dx != dy) {
+    go(rows, columns);
+  } else {  // the columns' blocks read what the rows' overwrite
+    go(0, columns);
+    go(rows, 0);
+  }
+}
+
 template <typename XT, bool CENTRED>
 void launch_typed(const void* dy, const void* x, const void* gamma, const void* dresidual, int T,
                   int H, float eps, void* dx, float* pg, float* pb, int part_stride, int blocks,
@@ -240,6 +441,7 @@ void launch_typed(const void* dy, const void* x, const void* gamma, const void* 
 }  // namespace
 
 size_t norm_backward_workspace_bytes(int T, int H) {
+  if (take_few(T, H)) return 0;
   const int blocks = norm_blocks(T, H);
   return blocks > 1 ? (size_t)blocks * H * 2 * sizeof(float) : 0;
 }
@@ -250,6 +452,7 @@ moe_status_t launch_norm_backward(bool centred, const void* dy, const void* x, c
                                   hipStream_t stream) {
   const bool sums = dgamma != nullptr || dbeta != nullptr;
   if (T == 0 && !sums) return MOE_OK;
+  const bool few = take_few(T, H);
   const int blocks = norm_blocks(T, H);
   float* pg = blocks == 1 ? dgamma : static_cast<float*>(ws);
   float* pb = blocks == 1 ? dbeta : static_cast<float*>(ws) + (size_t)blocks * H;  // of no rows: unread
@@ -257,8 +460,13 @@ moe_status_t launch_norm_backward(bool centred, const void* dy, const void* x, c
     float* kg = dgamma != nullptr ? pg : nullptr;
     float* kb = dbeta != nullptr ? pb : nullptr;
     auto go = [&](auto kind, auto c) {
-      launch_typed<typename decltype(kind)::type, decltype(c)::value>(
-          dy, x, gamma, dresidual, T, H, eps, dx, kg, kb, H, blocks, stream);
+      typedef typename decltype(kind)::type XT;
+      if (few)
+        launch_few<XT, decltype(c)::value>(dy, x, gamma, dresidual, T, H, eps, dx, dgamma, dbeta,
+                                           stream);
+      else
+        launch_typed<XT, decltype(c)::value>(dy, x, gamma, dresidual, T, H, eps, dx, kg, kb, H,
+                                             blocks, stream);
     };
     struct B16 { typedef uint16_t type; };
     struct F32 { typedef float type; };
@@ -267,7 +475,7 @@ moe_status_t launch_norm_backward(bool centred, const void* dy, const void* x, c
     else if (centred) go(F32{}, std::true_type{});
     else go(F32{}, std::false_type{});
   }
-  if (sums && blocks != 1)
+  if (sums && blocks != 1 && !few)
     fold_columns_kernel<<<dim3(ceil_div(H, 32), dbeta != nullptr ? 2 : 1), 256, 0, stream>>>(
         pg, pb, blocks, H, dgamma, dbeta);
   return launch_status();
