@@ -97,6 +97,17 @@ __device__ __forceinline__ bf16x8_t read_k(const uint4* part, int at) {
   return *reinterpret_cast<const bf16x8_t*>(reinterpret_cast<const char*>(part) + at);
 }
 
+// Two runs of 4 consecutive columns a lane (accumulator groups g and g + 1 of the
+// lane halves) packed to 8 consecutive columns: group g for lanes 0..31, g + 1 for
+// the others.
+__device__ __forceinline__ uint4 join_packed(const float* lo, const float* hi) {
+  const auto a = __builtin_amdgcn_permlane32_swap(pack_bf16x2(lo[0], lo[1]), pack_bf16x2(hi[0], hi[1]),
+                                                  false, false);
+  const auto b = __builtin_amdgcn_permlane32_swap(pack_bf16x2(lo[2], lo[3]), pack_bf16x2(hi[2], hi[3]),
+                                                  false, false);
+  return make_uint4(a[0], b[0], a[1], b[1]);
+}
+
 __device__ __forceinline__ int32x4_t pack8(const float* o) {
   return int32x4_t{(int)pack_bf16x2(o[0], o[1]), (int)pack_bf16x2(o[2], o[3]),
                    (int)pack_bf16x2(o[4], o[5]), (int)pack_bf16x2(o[6], o[7])};
@@ -139,24 +150,50 @@ struct Item {
 // Waits until at most N vector memory operations of the wave are outstanding.
 template <int N>
 __device__ __forceinline__ void vm_wait() {
-  static_assert(N < 16, "one field of the count");
-  __builtin_amdgcn_s_waitcnt(0x0f70 | N);
+  static_assert(N < 64, "six bits of the count, in two fields");
+  __builtin_amdgcn_s_waitcnt(0x0f70 | (N & 15) | ((N >> 4) << 14));
 }
+
+// LDS beside the stages: the rows' gradient finds a tile's slot in a prefix; the
+// weights' gradient has 4 KB a wave that its results pass through.
+template <bool WEIGHTS, typename SH>
+struct Beside {
+  int32_t tp[MOE_MAX_SLOTS + 1];
+  int32_t scratch[SH::kThreads];
+};
+template <typename SH>
+struct Beside<true, SH> {
+  uint4 out[SH::kWaves][256];
+};
 
 // A persistent block takes items (output tiles) in turn. LDS holds two slices
 // of both operands, each in an array of its own, so that the compiler sees
 // that the reads of one need not wait for the copies into the other. The copy
-// of slice d + 1 runs while slice d is multiplied. The next item's first slice
-// is asked for before an item's results are stored, its second one behind the
-// stores: no more outstanding operations than that second slice's then mean
-// that the first has arrived (loads arrive in order), whatever the stores do.
+// of slice d + 1 runs while slice d is multiplied.
+//
+// The next item's first slices are asked for before an item's results are
+// stored, and waited for by the number of younger operations outstanding (the
+// completion of a wave's vector memory operations, stores among them, is reported
+// in the order of their execution). The rows' gradient passes its results through its part of
+// stage 1 and asks for the first slice alone, and for the second behind the
+// stores; the weights' gradient has room for them elsewhere, asks for two slices
+// and multiplies them while the stores drain (bf16, 64 slots of 2048 x 4096 with
+// 512 rows each 754 -> 735 us).
+//
+// What bounds it, at 131072 rows of 2048 x 4096 in 64 slots, f32 results (2.2
+// TFLOP, 2.31 ms, 950 TFLOP/s): the products alone, without copies and stores, take
+// 1.70 ms, the copies alone 1.57 ms (11 TB/s into LDS), both 1.93, and the stores add
+// the rest: their 2.1 GB at the rate of plain writes are 0.5 ms. Measured and not
+// kept: slices of 32 values in four stages (3.2 ms), the last block's products over
+// the next slice's reads and copies (2.32 to 2.40), blocks out of step with each
+// other (2.36), non-temporal stores (2.43), tiles of several forms by columns too.
 template <int KIND, typename SH>
 __global__ __launch_bounds__(SH::kThreads, 2) void grouped_grad_kernel(Args p) {
   constexpr bool WEIGHTS = KIND >= kWeights;
   constexpr int BM = SH::kRowsM, BN = SH::kColsN, NI = SH::NI, NJ = SH::NJ;
   __shared__ uint4 stage0[SH::kVecM + SH::kVecN], stage1[SH::kVecM + SH::kVecN];
-  __shared__ int32_t tp[WEIGHTS ? 1 : MOE_MAX_SLOTS + 1];
-  __shared__ int32_t scratch[WEIGHTS ? 1 : SH::kThreads];
+  __shared__ Beside<WEIGHTS, SH> beside;
+  constexpr int kCopies = SH::kCopiesM + SH::kCopiesN;
   const int lane = lane_id();
   const int wave = uniform_i32(threadIdx.x / kWave);
   const int wm = wave / SH::WN, wn = wave % SH::WN;
@@ -165,8 +202,8 @@ __global__ __launch_bounds__(SH::kThreads, 2) void grouped_grad_kernel(Args p) {
   const int MT = WEIGHTS ? ceil_div(p.M, BM) : 0;
   int RT = 0;
   if constexpr (!WEIGHTS) {
-    tile_prefix<SH::kThreads, BM>(p.offsets, p.S, p.max_rows, tp, scratch);
-    RT = uniform_i32(tp[p.S]);
+    tile_prefix<SH::kThreads, BM>(p.offsets, p.S, p.max_rows, beside.tp, beside.scratch);
+    RT = uniform_i32(beside.tp[p.S]);
   }
   const int GN = NT < kGroupCols ? NT : kGroupCols;
   const int GM = kXcdItems / GN;
@@ -212,9 +249,9 @@ __global__ __launch_bounds__(SH::kThreads, 2) void grouped_grad_kernel(Args p) {
     } else {
       int rt, nt;
       item_tile(item, RT, NT, GM, GN, &rt, &nt);
-      it.s = uniform_i32(tile_slot(tp, p.S, rt));
+      it.s = uniform_i32(tile_slot(beside.tp, p.S, rt));
       slot_rows(p.offsets, it.s, p.max_rows, &lo, &hi);
-      it.row0 = uniform_i32(lo + (rt - tp[it.s]) * BM);
+      it.row0 = uniform_i32(lo + (rt - beside.tp[it.s]) * BM);
       it.rows = uniform_i32(min(BM, hi - it.row0));
       it.nd = ceil_div(p.Kd, kSlice);
       it.m0 = 0;
@@ -300,13 +337,18 @@ __global__ __launch_bounds__(SH::kThreads, 2) void grouped_grad_kernel(Args p) {
           acc[j][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fn[j], fm[i], acc[j][i], 0, 0, 0);
     }
   };
-  // All slices of the item; `use` multiplies the one in a stage.
+  // All slices of the item, the first of which has arrived for this wave; `use`
+  // multiplies the one in a stage. `behind`: stores issued since slice 1 was asked
+  // for (none or those of a full tile).
+  constexpr int kStores = (KIND == kWeightsF32 || KIND == kRowsSwiglu ? 8 : 4) * NI;  // of a full tile, a wave
+  int behind = 0;
   auto contract = [&](auto use) {
-    vm_wait<SH::kCopiesM + SH::kCopiesN>();
     __syncthreads();
     use(stage0);
     for (int d = 1; d < it.nd; d += 2) {
-      vm_wait<0>();
+      if (WEIGHTS && behind != 0) vm_wait<WEIGHTS ? kStores : 0>();
+      else vm_wait<0>();
+      behind = 0;
       __syncthreads();
       if (d + 1 < it.nd) fetch(stage0, d + 1);
       use(stage1);
@@ -318,90 +360,148 @@ __global__ __launch_bounds__(SH::kThreads, 2) void grouped_grad_kernel(Args p) {
     }
     __syncthreads();  // both stages have been read
   };
-  // Stores the wave's first ni fragments of rows of tile t, 32 rows at a time
-  // through the wave's own part of stage 1 (nobody else copies or reads there),
-  // so that whole lines are written. Register v of acc[j][i] is column 8 (v / 4) +
-  // 4 (lane / 32) + v % 4 of the 32 of j, row lane % 32 of the 32 of i; what is read
-  // back are 4 or 8 consecutive columns a lane, kLanes lanes to a row.
+
+  // Stores the wave's first ni fragments of rows of tile t through LDS, so that
+  // whole lines are written. Register v of acc[j][i] is column 8 (v / 4) +
+  // 4 (lane / 32) + v % 4 of the 32 of j, row lane % 32 of the 32 of i.
   auto store = [&](const Item<SH>& t, auto& acc) {
     constexpr int ni = sizeof(acc[0]) / sizeof(floatx16);
-    constexpr int kCols = KIND == kWeightsF32 ? 4 : 8;
-    constexpr int kLanes = NJ * 32 / kCols, kLines = kWave / kLanes;  // rows a step
-    auto place = [&](int r, int ch) {
-      static_assert(NJ == 2 && SH::kCopiesN * kWave * (NI == 1 ? 1 : 2) == 512, "32 rows of 256 bytes");
-      const int half = NI == 1 || r >= 16 ? SH::kVecM : 0;  // which of the wave's parts
-      return stage1 + half + wave * SH::kCopiesN * kWave + (NI == 1 ? r : r & 15) * 16 +
-             (ch ^ (r & 15));
-    };
     constexpr uint32_t OB = KIND == kWeightsF32 ? 4u : 2u;
     const uint32_t cols = KIND == kRowsSwiglu ? 2u * (uint32_t)p.N : (uint32_t)p.N;
     const size_t first = WEIGHTS ? (((size_t)t.split * p.S + t.s) * p.M + t.m0) * p.N
                                  : (size_t)t.row0 * cols;
     const uint32_t bytes = (uint32_t)(WEIGHTS ? min(p.M - t.m0, BM) : t.rows) * cols * OB;
     const __amdgpu_buffer_rsrc_t rc = uniform_rsrc(static_cast<char*>(p.out) + first * OB, bytes);
-    const __amdgpu_buffer_rsrc_t rh = uniform_rsrc(
-        KIND == kRowsSwiglu ? p.h + first : nullptr, KIND == kRowsSwiglu ? bytes : 0u);
-    const int col = t.n0 + wn * NJ * 32 + (lane % kLanes) * kCols;
-    const uint32_t side = col < p.N ? (uint32_t)col * OB : kOOB;  // past every row where out of range
+    if constexpr (WEIGHTS) {
+      // 32 rows of 128 bytes at a time: 32 columns of f32, or 64 of bf16 if they are
+      // not added to what is there (that sum is f32: 32 columns again).
+      uint4* out = beside.out[wave];
+      auto place = [&](int r, int ch) { return out + r * 8 + (ch ^ ((r >> 1) & 7)); };
+      const int r8 = lane >> 3, c8 = lane & 7;  // row and chunk of a line of 128 bytes, read back
 #pragma unroll
-    for (int i = 0; i < ni; ++i) {
+      for (int i = 0; i < ni; ++i) {
+        const uint32_t row = (uint32_t)((i * SH::WM + wm) * 32 + r8);
+        if (KIND == kWeights && !p.accumulate) {
 #pragma unroll
-      for (int j = 0; j < NJ; ++j)
+          for (int j = 0; j < NJ; ++j)
 #pragma unroll
-        for (int g = 0; g < 4; ++g)
-          *place(lane & 31, j * 8 + 2 * g + (lane >> 5)) =
-              make_uint4(__float_as_uint(acc[j][i][4 * g]), __float_as_uint(acc[j][i][4 * g + 1]),
-                         __float_as_uint(acc[j][i][4 * g + 2]), __float_as_uint(acc[j][i][4 * g + 3]));
-      wave_lds_fence();
+            for (int g = 0; g < 4; g += 2) {
+              float lo[4], hi[4];
 #pragma unroll
-      for (int l = 0; l < 32; l += kLines) {
-        const int r = l + lane / kLanes;
-        float o[kCols];
+              for (int v = 0; v < 4; ++v) {
+                lo[v] = acc[j][i][4 * g + v];
+                hi[v] = acc[j][i][4 * g + 4 + v];
+              }
+              *place(lane & 31, j * 4 + g + (lane >> 5)) = join_packed(lo, hi);
+            }
+          wave_lds_fence();
+          const int col = t.n0 + wn * NJ * 32 + c8 * 8;
 #pragma unroll
-        for (int c = 0; c < kCols; c += 4) {
-          const uint4 q = *place(r, ((lane % kLanes) * kCols + c) / 4);
-          o[c] = __uint_as_float(q.x);
-          o[c + 1] = __uint_as_float(q.y);
-          o[c + 2] = __uint_as_float(q.z);
-          o[c + 3] = __uint_as_float(q.w);
+          for (int l = 0; l < 32; l += 8) {
+            const uint32_t at = (row + l) * cols * 2u + (uint32_t)col * 2u;
+            __builtin_amdgcn_raw_buffer_store_b128(
+                __builtin_bit_cast(int32x4_t, *place(l + r8, c8)), rc, col < p.N ? at : kOOB, 0, 0);
+          }
+          wave_lds_fence();
+          continue;
         }
-        const uint32_t row = (uint32_t)((i * SH::WM + wm) * 32 + r);
-        const uint32_t at = side == kOOB ? kOOB : row * cols * OB + side;
-        if constexpr (KIND == kWeightsF32) {
-          if (p.accumulate) {
-            const int32x4_t prev = __builtin_amdgcn_raw_buffer_load_b128(rc, at, 0, 0);
 #pragma unroll
-            for (int v = 0; v < 4; ++v) o[v] = __int_as_float(prev[v]) + o[v];
-          }
-          __builtin_amdgcn_raw_buffer_store_b128(
-              int32x4_t{__float_as_int(o[0]), __float_as_int(o[1]), __float_as_int(o[2]),
-                        __float_as_int(o[3])},
-              rc, at, 0, 0);
-        } else if constexpr (KIND == kRowsSwiglu) {
-          const uint32_t up = side == kOOB ? kOOB : at + (uint32_t)p.N * 2u;
-          float gt[8], u[8];
-          unpack8(__builtin_amdgcn_raw_buffer_load_b128(rh, at, 0, 0), gt);
-          unpack8(__builtin_amdgcn_raw_buffer_load_b128(rh, up, 0, 0), u);
+        for (int j = 0; j < NJ; ++j) {
 #pragma unroll
-          for (int v = 0; v < 8; ++v) {
-            const float sg = 1.0f / (1.0f + __expf(-gt[v]));
-            const float silu = gt[v] * sg;
-            gt[v] = o[v] * u[v] * (sg + silu * (1.0f - sg));
-            u[v] = o[v] * silu;
-          }
-          __builtin_amdgcn_raw_buffer_store_b128(pack8(gt), rc, at, 0, 0);
-          __builtin_amdgcn_raw_buffer_store_b128(pack8(u), rc, up, 0, 0);
-        } else {
-          if (KIND == kWeights && p.accumulate) {
-            float prev[8];
-            unpack8(__builtin_amdgcn_raw_buffer_load_b128(rc, at, 0, 0), prev);
+          for (int g = 0; g < 4; ++g)
+            *place(lane & 31, 2 * g + (lane >> 5)) = make_uint4(
+                __float_as_uint(acc[j][i][4 * g]), __float_as_uint(acc[j][i][4 * g + 1]),
+                __float_as_uint(acc[j][i][4 * g + 2]), __float_as_uint(acc[j][i][4 * g + 3]));
+          wave_lds_fence();
+          const int col = t.n0 + (wn * NJ + j) * 32 + c8 * 4;
 #pragma unroll
-            for (int v = 0; v < 8; ++v) o[v] = prev[v] + o[v];
+          for (int l = 0; l < 32; l += 8) {
+            const uint4 q = *place(l + r8, c8);
+            float o[4] = {__uint_as_float(q.x), __uint_as_float(q.y), __uint_as_float(q.z),
+                          __uint_as_float(q.w)};
+            const uint32_t at = col < p.N ? ((row + l) * cols + (uint32_t)col) * OB : kOOB;
+            if constexpr (KIND == kWeightsF32) {
+              if (p.accumulate) {
+                const int32x4_t prev = __builtin_amdgcn_raw_buffer_load_b128(rc, at, 0, 0);
+#pragma unroll
+                for (int v = 0; v < 4; ++v) o[v] = __int_as_float(prev[v]) + o[v];
+              }
+              __builtin_amdgcn_raw_buffer_store_b128(
+                  int32x4_t{__float_as_int(o[0]), __float_as_int(o[1]), __float_as_int(o[2]),
+                            __float_as_int(o[3])},
+                  rc, at, 0, 0);
+            } else {
+              const int32x2_t prev = __builtin_amdgcn_raw_buffer_load_b64(rc, at, 0, 0);
+              o[0] = bf16_to_f32((uint32_t)prev[0] & 0xffffu) + o[0];
+              o[1] = bf16_to_f32((uint32_t)prev[0] >> 16) + o[1];
+              o[2] = bf16_to_f32((uint32_t)prev[1] & 0xffffu) + o[2];
+              o[3] = bf16_to_f32((uint32_t)prev[1] >> 16) + o[3];
+              __builtin_amdgcn_raw_buffer_store_b64(
+                  int32x2_t{(int)pack_bf16x2(o[0], o[1]), (int)pack_bf16x2(o[2], o[3])}, rc, at, 0,
+                  0);
+            }
           }
-          __builtin_amdgcn_raw_buffer_store_b128(pack8(o), rc, at, 0, 0);
+          wave_lds_fence();
         }
       }
-      wave_lds_fence();
+    } else {
+      // 32 rows of 64 columns of f32 at a time through the wave's own parts of stage 1:
+      // nobody else copies or reads there
+      constexpr int kLanes = 8, kLines = 8;  // 8 columns a lane, rows a step
+      auto place = [&](int r, int ch) {
+        static_assert(NJ == 2 && SH::kCopiesN * kWave * (NI == 1 ? 1 : 2) == 512,
+                      "32 rows of 256 bytes");
+        const int half = NI == 1 || r >= 16 ? SH::kVecM : 0;  // which of the wave's parts
+        return stage1 + half + wave * SH::kCopiesN * kWave + (NI == 1 ? r : r & 15) * 16 +
+               (ch ^ (r & 15));
+      };
+      const __amdgpu_buffer_rsrc_t rh = uniform_rsrc(
+          KIND == kRowsSwiglu ? p.h + first : nullptr, KIND == kRowsSwiglu ? bytes : 0u);
+      const int col = t.n0 + wn * NJ * 32 + (lane % kLanes) * 8;
+#pragma unroll
+      for (int i = 0; i < ni; ++i) {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+            *place(lane & 31, j * 8 + 2 * g + (lane >> 5)) = make_uint4(
+                __float_as_uint(acc[j][i][4 * g]), __float_as_uint(acc[j][i][4 * g + 1]),
+                __float_as_uint(acc[j][i][4 * g + 2]), __float_as_uint(acc[j][i][4 * g + 3]));
+        wave_lds_fence();
+#pragma unroll
+        for (int l = 0; l < 32; l += kLines) {
+          const int r = l + lane / kLanes;
+          float o[8];
+#pragma unroll
+          for (int c = 0; c < 8; c += 4) {
+            const uint4 q = *place(r, ((lane % kLanes) * 8 + c) / 4);
+            o[c] = __uint_as_float(q.x);
+            o[c + 1] = __uint_as_float(q.y);
+            o[c + 2] = __uint_as_float(q.z);
+            o[c + 3] = __uint_as_float(q.w);
+          }
+          const uint32_t row = (uint32_t)((i * SH::WM + wm) * 32 + r);
+          const uint32_t at = col < p.N ? (row * cols + (uint32_t)col) * 2u : kOOB;
+          if constexpr (KIND == kRowsSwiglu) {
+            const uint32_t up = col < p.N ? at + (uint32_t)p.N * 2u : kOOB;
+            float gt[8], u[8];
+            unpack8(__builtin_amdgcn_raw_buffer_load_b128(rh, at, 0, 0), gt);
+            unpack8(__builtin_amdgcn_raw_buffer_load_b128(rh, up, 0, 0), u);
+#pragma unroll
+            for (int v = 0; v < 8; ++v) {
+              const float sg = 1.0f / (1.0f + __expf(-gt[v]));
+              const float silu = gt[v] * sg;
+              gt[v] = o[v] * u[v] * (sg + silu * (1.0f - sg));
+              u[v] = o[v] * silu;
+            }
+            __builtin_amdgcn_raw_buffer_store_b128(pack8(gt), rc, at, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b128(pack8(u), rc, up, 0, 0);
+          } else {
+            __builtin_amdgcn_raw_buffer_store_b128(pack8(o), rc, at, 0, 0);
+          }
+        }
+        wave_lds_fence();
+      }
     }
   };
 
@@ -410,14 +510,19 @@ __global__ __launch_bounds__(SH::kThreads, 2) void grouped_grad_kernel(Args p) {
   setup(item);
   fetch(stage0, 0);
   fetch(stage1, 1);
+  vm_wait<kCopies>();
   bool more = true;
   while (more) {
     const int next = item + gridDim.x;
     more = next < total;
+    // Slice 1 of an item of one slice is nothing, but has to have been there before
+    // its place is used for results.
+    if (!WEIGHTS && it.nd < 2) vm_wait<0>();
     auto go_on = [&]() {
       if (more) {
         setup(next);
         fetch(stage0, 0);
+        if constexpr (WEIGHTS) fetch(stage1, 1);
       }
     };
     // A wave with ni fragments of rows: the accumulators live here alone, so that
@@ -432,13 +537,22 @@ __global__ __launch_bounds__(SH::kThreads, 2) void grouped_grad_kernel(Args p) {
       contract([&](const uint4* stage) { multiply(stage, acc); });
       const Item<SH> done = it;
       go_on();
+      __builtin_amdgcn_sched_barrier(0);  // the counts below go by this order
       store(done, acc);
+      __builtin_amdgcn_sched_barrier(0);
+      if (!WEIGHTS && more) fetch(stage1, 1);
+      // the next item's slice 0, with slice 1 and the stores behind it
+      vm_wait<kCopies + kStores / NI * ni>();
+      behind = WEIGHTS && ni == NI ? 1 : 0;
     };
     const int high = WEIGHTS ? min(p.M - it.m0, BM) : it.rows;
     const int ni = max(0, (ceil_div(high, 32) - wm + SH::WM - 1) / SH::WM);
     if (ni == 0 || it.n0 + wn * NJ * 32 >= p.N) {  // copies alone
       contract([](const uint4*) {});
       go_on();
+      if (!WEIGHTS && more) fetch(stage1, 1);
+      vm_wait<kCopies>();
+      behind = 0;
     } else if (ni == 1 || NI == 1) {
       work(std::integral_constant<int, 1>{});
     } else if constexpr (NI == 4) {
@@ -446,9 +560,9 @@ __global__ __launch_bounds__(SH::kThreads, 2) void grouped_grad_kernel(Args p) {
       else if (ni == 3) work(std::integral_constant<int, 3>{});
       else work(std::integral_constant<int, 4>{});
     }
-    if (more) fetch(stage1, 1);
     item = next;
   }
+  vm_wait<0>();  // no copy into LDS outlives the block
 }
 
 }  // namespace
