@@ -785,6 +785,8 @@ def permute_backward(dx_perm: torch.Tensor, pair_row: torch.Tensor, K: int,
     if dx is None:
         if accumulate:
             raise ValueError("accumulate needs dx")
+        if dx_dtype not in (None, torch.float32, torch.bfloat16):
+            raise TypeError(f"dx_dtype {dx_dtype}, expected torch.float32 or torch.bfloat16")
         dx = _empty((T, H), dx_dtype or dx_perm.dtype, dx_perm)
     else:
         _dev(dx, "dx", (torch.float32, torch.bfloat16), (T, H))

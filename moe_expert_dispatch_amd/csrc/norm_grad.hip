@@ -379,7 +379,9 @@ int norm_blocks(int T, int H) {
   const int64_t rows = L == 0 ? 1 : kNormGroupThreads / L;
   const int64_t most = std::min(256 * std::clamp((16 + waves / 2) / waves, 1, 4),
                                 std::max({256, (1 << 20) / H, T / 16}));
-  return (int)std::min((T + rows - 1) / rows, most);
+  // as many rows a block as it takes, evenly: no more partial sums than that
+  const int64_t sets = (T + rows - 1) / rows, each = (sets + most - 1) / most;
+  return (int)((sets + each - 1) / each);
 }
 
 // Up to there one launch takes less than two with the host's time for the second
