@@ -212,14 +212,19 @@ __global__ __launch_bounds__(kThreads32) void grouped_grad_f32_kernel(Args32 p) 
   }
 }
 
-constexpr int kFewTiles = 3;  // large tiles a compute unit, below which small ones are taken
+// Small tiles up to three large ones for every two compute units. Both sides, small
+// and large: rows' gradient of 51 large tiles (8 slots of 83 rows, 264 x 136) 7.9
+// and 13.6 us, 324 (16 of 256, 512 x 256) 26.5 and 29.5, 576 42 and 40, 2308 143
+// and 109 (79 TFLOP/s); weights' gradient of 120 tiles 4.6 and 5.5, 512 14 and 10,
+// 2048 129 and 82 (105 TFLOP/s).
+constexpr int kFewTiles = 3, kFewUnits = 2;
 
 int grid32(int64_t items) {
   const int64_t most = 3 * (int64_t)device_cu_count();  // as many as the LDS holds
   return items < most ? (int)items : (int)most;
 }
 
-bool few_tiles(int64_t large) { return large < kFewTiles * (int64_t)device_cu_count(); }
+bool few_tiles(int64_t large) { return kFewUnits * large < kFewTiles * (int64_t)device_cu_count(); }
 
 // out[i] = (accumulate: out[i] +) the sum over the splits of part[split][i], 8 values a thread.
 template <typename OT>

@@ -155,26 +155,39 @@ __global__ __launch_bounds__(L == 0 ? 1024 : kNormGroupThreads) void norm_backwa
 constexpr int kFewRows = 64;
 constexpr int kColumns = 64;  // of a block
 
+// The first vectors of a wave's row, and the row's first 8 values for all lanes.
+template <typename XT>
+struct WaveRow {
+  decltype(raw8((const XT*)nullptr)) q[4], f;
+  __device__ __forceinline__ void ask(const XT* x, int nvec) {
+    f = raw8(x);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (lane_id() + u * kWave < nvec) q[u] = raw8(x + (lane_id() + u * kWave) * 8);
+  }
+};
+
 // A wave's row: its mean and 1 / deviation, in f64 from f32 sums or, where those
 // will not do (normalize_row), from f64 ones.
 template <typename XT, bool CENTRED>
-__device__ __forceinline__ void wave_row(const XT* x, int nvec, int H, float eps, double* mean,
-                                         double* r) {
+__device__ __forceinline__ void wave_row(const XT* x, WaveRow<XT> w, int nvec, int H, float eps,
+                                         double* mean, double* r) {
   const float width = (float)H;
   float m = 0.f, d = 0.f, ss = 0.f, var = 0.f;
-  auto spread = [&]() {
+  auto spread = [&]() {  // w holds the first vectors
     float sd = 0.f;
     ss = 0.f;
     for (int v0 = lane_id(); v0 < nvec; v0 += 4 * kWave) {  // four vectors in flight
-      decltype(raw8(x)) q[4];
+      if (v0 >= 4 * kWave) {
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (v0 + u * kWave < nvec) q[u] = raw8(x + (v0 + u * kWave) * 8);
+        for (int u = 0; u < 4; ++u)
+          if (v0 + u * kWave < nvec) w.q[u] = raw8(x + (v0 + u * kWave) * 8);
+      }
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         if (v0 + u * kWave >= nvec) continue;
         float h[8];
-        unpack8(q[u], h);
+        unpack8(w.q[u], h);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float c = CENTRED ? h[i] - m : h[i];
@@ -189,19 +202,20 @@ __device__ __forceinline__ void wave_row(const XT* x, int nvec, int H, float eps
   };
   if constexpr (CENTRED) {
     float h[8];
-    load8(x, h);
+    unpack8(w.f, h);
     m = mean8(h);
   }
   spread();
   if constexpr (CENTRED) {
     if (!(var - eps >= d * d)) {
       m += d;
+      if (nvec > 4 * kWave) w.ask(x, nvec);
       spread();
     }
   }
   if (var >= kLeastSquares && var >= d * d && ss < INFINITY) {
     *mean = (double)m + (double)d;
-    *r = 1.0 / sqrt((double)var);
+    *r = (double)(1.0f / sqrtf(var));  // in f64 it took a wave 1 us a row
     return;
   }
   double at = 0.0;
@@ -273,9 +287,13 @@ __global__ __launch_bounds__(1024) void norm_backward_few_kernel(
   __shared__ double mean[kFewRows], dev[kFewRows];
   __shared__ float sums[2][16][kColumns];
   const int wave = threadIdx.x / kWave, waves = blockDim.x / kWave;
+  WaveRow<XT> next;
+  if (wave < T) next.ask(x + (size_t)wave * H, nvec);
   for (int t = wave; t < T; t += waves) {
+    const WaveRow<XT> row = next;
+    if (t + waves < T) next.ask(x + (size_t)(t + waves) * H, nvec);
     double m, r;
-    wave_row<XT, CENTRED>(x + (size_t)t * H, nvec, H, eps, &m, &r);
+    wave_row<XT, CENTRED>(x + (size_t)t * H, row, nvec, H, eps, &m, &r);
     if (lane_id() == 0) {
       mean[t] = m;
       dev[t] = r;

@@ -12,6 +12,13 @@ namespace moe {
 // range, are summed in f64.
 constexpr float kLeastSquares = 0x1p-80f;
 
+// The sum of a value a wave (up to 16), of which this lane has read that of wave
+// lane % 16: one LDS read and four steps, where a loop over the waves waits for
+// LDS as often as there are waves.
+__device__ __forceinline__ float over_waves(float v) {
+  return group_sum<16>((lane_id() & 15) < (int)(blockDim.x / kWave) ? v : 0.f);
+}
+
 // The lanes that hold one row: L = 16, 32 or 64 lanes of a wave (rows of one
 // block then need no barrier), or the whole block (L = 0). Every lane gets the
 // sum; its order does not depend on scheduling. `part` is one array for each
@@ -28,9 +35,7 @@ __device__ __forceinline__ float lanes_sum(float v, float* part) {
     v = wave_sum(v);
     if (lane_id() == 0) part[threadIdx.x / kWave] = v;
     __syncthreads();
-    float total = 0.f;
-    for (int w = 0; w < (int)(blockDim.x / kWave); ++w) total += part[w];
-    return total;
+    return over_waves(part[lane_id() & 15]);
   }
 }
 
@@ -46,12 +51,8 @@ __device__ __forceinline__ float2 lanes_sum2(float a, float b, float2* part) {
     b = wave_sum(b);
     if (lane_id() == 0) part[threadIdx.x / kWave] = make_float2(a, b);
     __syncthreads();
-    float2 total = make_float2(0.f, 0.f);
-    for (int w = 0; w < (int)(blockDim.x / kWave); ++w) {
-      total.x += part[w].x;
-      total.y += part[w].y;
-    }
-    return total;
+    const float2 v = part[lane_id() & 15];
+    return make_float2(over_waves(v.x), over_waves(v.y));
   }
 }
 
