@@ -236,3 +236,80 @@ def test_refusals():
             bad()
     with pytest.raises(RuntimeError):
         moe.swiglu(torch.zeros(8, 24, device=dev), off)   # 2I of a half that is no multiple of 8
+
+
+# every way that a tile of 256 (or 64) rows ends, in enough tiles that the large ones are taken
+ENDS = [0, 1, 31, 32, 33, 63, 64, 65, 95, 97, 127, 128, 129, 160, 191, 192, 193, 223, 224, 225, 255, 256, 257, 300, 384,
+        511, 512, 513]
+
+
+@pytest.mark.parametrize("dt", [B, F])
+@pytest.mark.parametrize("Kd", [8, 64, 72, 128, 200, 264])
+def test_large_tiles_of_rows(dt, Kd):
+    dev = device()
+    N = 1032
+    announce(f"large tiles rows {dt} Kd={Kd}")
+    off = _offsets(ENDS)
+    S, P = len(off) - 1, int(off[-1])
+    dc, w, h = _random(dt, Kd, (P + 9, Kd), (S, Kd, N), (P + 9, 2 * N))
+    dc[P:] = float("nan")
+    h[P:] = float("nan")
+    args = (moe.DOWN, dc.to(dev), off.to(dev), w.to(dev))
+    want = tr.grouped_rows_grad(dc[:P], off.numpy(), w)
+    size = tr.grouped_rows_grad(dc[:P].abs(), off.numpy(), w.abs())
+    for again in range(3):  # many tiles a block, one after the other: the same bits each time
+        out = torch.full((P + 9, N), -7.0, device=dev).to(dt)
+        got = moe.grouped_gemm_backward(*args, out=out)
+        assert (got[P:] == -7).all()
+        if again:
+            assert torch.equal(got, first)
+        first = got
+    _within(got[:P], want, size, Kd, dt, "rows")
+    dh = moe.grouped_gemm_backward(*args, h=h.to(dev), out=torch.full((P + 9, 2 * N), -7.0, device=dev).to(dt))
+    assert (dh[P:] == -7).all()
+    hd = np64(h[:P])
+    g, u = hd[:, :N], hd[:, N:]
+    s = tr.sigmoid(g)
+    want2 = tr.swiglu_backward(h[:P], want)
+    slope = np.concatenate([np.abs(u * s * (1 + g * (1 - s))), np.abs(g * s)], 1)
+    rest = np.concatenate([np.abs(u) * s * (1 + np.abs(g)), np.abs(g) * s], 1)
+    da, de, ga = (np.tile(a, (1, 2)) for a in (np.abs(want), (2 * Kd + 1) * U * size, np.abs(g)))
+    err = de * (slope + 8 * U * (ga + 6) * rest) + da * 8 * U * (ga + 6) * rest
+    assert_within(np64(dh[:P]), want2, err + ROUND[dt] * (np.abs(want2) + err) + TINY, "dh")
+
+
+@pytest.mark.parametrize("dt", [B, F])
+@pytest.mark.parametrize("N,Kd", [(264, 520), (520, 264), (1032, 72)])
+def test_many_tiles_of_weights(dt, N, Kd):
+    dev = device()
+    announce(f"many tiles weights {dt} N={N} Kd={Kd}")
+    off = _offsets(ENDS)
+    S, P = len(off) - 1, int(off[-1])
+    dc, a, before = _random(dt, N, (P + 9, N), (P + 9, Kd), (S, N, Kd))
+    dc[P:] = float("nan")
+    want = tr.grouped_weight_grad(dc[:P], a[:P], off.numpy())
+    size = tr.grouped_weight_grad(dc[:P].abs(), a[:P].abs(), off.numpy())
+    D, A, O = dc.to(dev), a.to(dev), off.to(dev)
+    for odt in (F, B):
+        first = moe.grouped_gemm_weight_grad(D, A, O, dw_dtype=odt)
+        _within(first, want, size, max(ENDS), odt, f"{odt}")
+        for _ in range(3):
+            assert torch.equal(moe.grouped_gemm_weight_grad(D, A, O, dw_dtype=odt), first)
+        dw = before.to(odt).to(dev)
+        moe.grouped_gemm_weight_grad(D, A, O, dw=dw, accumulate=True)
+        total = want + np64(before.to(odt))
+        _within(dw, total, size + np.abs(total), max(ENDS), odt, f"{odt} accumulated")
+
+
+@pytest.mark.parametrize("dt", [B, F])
+def test_the_most_slots(dt):
+    dev = device()
+    announce(f"1024 slots {dt}")
+    counts = [(5 * i) % 7 for i in range(1024)]
+    off = _offsets(counts)
+    S, P = 1024, int(off[-1])
+    dc, w, a = _random(dt, 3, (P, 40), (S, 40, 24), (P, 24))
+    got = moe.grouped_gemm_backward(moe.DOWN, dc.to(dev), off.to(dev), w.to(dev))
+    _within(got, tr.grouped_rows_grad(dc, off.numpy(), w), tr.grouped_rows_grad(dc.abs(), off.numpy(), w.abs()), 40, dt, "rows")
+    got = moe.grouped_gemm_weight_grad(dc.to(dev), a.to(dev), off.to(dev))
+    _within(got, tr.grouped_weight_grad(dc, a, off.numpy()), tr.grouped_weight_grad(dc.abs(), a.abs(), off.numpy()), 7, F, "weights")
