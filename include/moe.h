@@ -533,8 +533,8 @@ moe_status_t moe_permute_backward(const void* dx_perm, moe_dtype_t dt, const int
  *   dw_down  = moe_grouped_gemm_weight_grad(dy, act)
  *   dw_gate_up = moe_grouped_gemm_weight_grad(dh, x_perm)
  * Rows of slot s are offsets[s] .. offsets[s+1], as in moe_grouped_gemm;
- * rows behind the last slot's are neither read nor written. max_rows < 2^31 -
- * 1024. Products of bf16 values are exact, sums f32, one rounding at the end
+ * rows before the first slot's and behind the last one's are neither read nor
+ * written. max_rows < 2^31 - 1024. Products of bf16 values are exact, sums f32, one rounding at the end
  * (dt MOE_DTYPE_F32: f32 products and sums on the matrix cores). The orders of
  * the sums depend on shapes and the device's number of compute units alone. Buffers 16-byte
  * aligned, H % 8 == 0, I % 8 == 0; no output may overlap an input.

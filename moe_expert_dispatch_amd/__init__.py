@@ -575,6 +575,8 @@ def _norm_backward(what, dy, x, gamma, eps, dresidual, dx, sums, ws):
     if ws is None:
         need = norm_backward_workspace_size(T, H)
         ws = x.new_empty(need, dtype=torch.uint8) if need else None
+    else:
+        _dev(ws, "ws")
     _launch(what, x, (dy, gamma, dresidual, dx, *sums, ws), dy.data_ptr(), x.data_ptr(),
             gamma.data_ptr(), _ptr(dresidual), _DT[dt], T, H, eps, dx.data_ptr(),
             *[s.data_ptr() for s in sums], _ptr(ws),
@@ -807,8 +809,8 @@ def _slots(offsets) -> int:
 
 def swiglu(h: torch.Tensor, offsets: torch.Tensor, act: Optional[torch.Tensor] = None
            ) -> torch.Tensor:
-    """moe_swiglu: h [rows, 2I] (gate, up) -> act [rows, I]; rows behind offsets[S] are not
-    written. h is grouped_gemm(DOWN, x_perm, offsets, w_gate_up)."""
+    """moe_swiglu: h [rows, 2I] (gate, up) -> act [rows, I]; rows before offsets[0] and behind
+    offsets[S] are not written. h is grouped_gemm(DOWN, x_perm, offsets, w_gate_up)."""
     _dev(h, "h", (torch.float32, torch.bfloat16))
     S = _slots(offsets)
     if h.dim() != 2 or h.shape[1] % 2:
@@ -826,8 +828,8 @@ def grouped_gemm_backward(op: int, dc: torch.Tensor, offsets: torch.Tensor, w: t
                           ) -> torch.Tensor:
     """moe_grouped_gemm_backward, the rows' gradient. GATE_UP_SWIGLU: dc [rows, 2I] (gradient of
     h), w [S, 2I, H] -> [rows, H]. DOWN: dc [rows, H], w [S, H, I] -> [rows, I], or with h
-    [rows, 2I] (swiglu's input) -> its gradient [rows, 2I]. Rows behind offsets[S] are not
-    written."""
+    [rows, 2I] (swiglu's input) -> its gradient [rows, 2I]. Rows before offsets[0] and behind
+    offsets[S] are not written."""
     _dev(dc, "dc", (torch.float32, torch.bfloat16))
     _dev(w, "w", dc.dtype)
     S = _slots(offsets)
@@ -883,6 +885,8 @@ def grouped_gemm_weight_grad(dc: torch.Tensor, a: torch.Tensor, offsets: torch.T
     if ws is None:
         need = grouped_gemm_weight_grad_workspace_size(dc.dtype, S, rows, N, Kd)
         ws = _empty((need,), torch.uint8, dc) if need else None
+    else:
+        _dev(ws, "ws")
     _launch("moe_grouped_gemm_weight_grad", dc, (a, offsets, dw, ws), _DT[dc.dtype],
             dc.data_ptr(), a.data_ptr(), offsets.data_ptr(), S, rows, N, Kd, dw.data_ptr(),
             _DT[dw.dtype], 1 if accumulate else 0, _ptr(ws),

@@ -313,3 +313,38 @@ def test_the_most_slots(dt):
     _within(got, tr.grouped_rows_grad(dc, off.numpy(), w), tr.grouped_rows_grad(dc.abs(), off.numpy(), w.abs()), 40, dt, "rows")
     got = moe.grouped_gemm_weight_grad(dc.to(dev), a.to(dev), off.to(dev))
     _within(got, tr.grouped_weight_grad(dc, a, off.numpy()), tr.grouped_weight_grad(dc.abs(), a.abs(), off.numpy()), 7, F, "weights")
+
+
+@pytest.mark.parametrize("dt", [B, F])
+def test_rows_before_the_first_slot(dt):
+    """Slots that begin behind row 0: the rows before them are left as they were, whatever they hold."""
+    dev = device()
+    announce(f"rows before the first slot {dt}")
+    off = torch.tensor([37, 37, 90, 111], dtype=torch.int32)
+    dc, w, a, h = _random(dt, 7, (130, 72), (3, 72, 40), (130, 40), (130, 80))
+    for t in (dc, a, h):
+        t[:37] = float("nan")
+        t[111:] = float("nan")
+    D, W, A, H, O = (t.to(dev) for t in (dc, w, a, h, off))
+    inner = lambda t: t[37:111].contiguous()  # noqa: E731
+    O0 = O - 37
+    blank = lambda n: torch.full((130, n), -7.0, device=dev).to(dt)  # noqa: E731
+    for got, want in ((moe.swiglu(H, O, act=blank(40)), moe.swiglu(inner(H), O0)),
+                      (moe.grouped_gemm_backward(moe.DOWN, D, O, W, out=blank(40)),
+                       moe.grouped_gemm_backward(moe.DOWN, inner(D), O0, W)),
+                      (moe.grouped_gemm_backward(moe.DOWN, D, O, W, h=H, out=blank(80)),
+                       moe.grouped_gemm_backward(moe.DOWN, inner(D), O0, W, h=inner(H)))):
+        assert torch.equal(got[37:111], want) and torch.isfinite(want).all()
+        assert (got[:37] == -7).all() and (got[111:] == -7).all()
+    assert torch.equal(moe.grouped_gemm_weight_grad(D, A, O), moe.grouped_gemm_weight_grad(inner(D), inner(A), O0))
+
+
+def test_workspaces_are_contiguous():
+    """A workspace that holds one byte over and over has the bytes that are asked for, but not the memory."""
+    dev = device()
+    one = torch.zeros(1, dtype=torch.uint8, device=dev).expand(1 << 24)
+    x, off = torch.zeros(400, 64, device=dev), _offsets([400]).to(dev)
+    for bad in (lambda: moe.grouped_gemm_weight_grad(x, x, off, ws=one),
+                lambda: moe.layer_norm_backward(x, x, x[0], ws=one), lambda: moe.rms_norm_backward(x, x, x[0], ws=one)):
+        with pytest.raises(ValueError):
+            bad()
