@@ -23,19 +23,18 @@ typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef float floatx16 __attribute__((ext_vector_type(16)));
 typedef int int32x4_t __attribute__((ext_vector_type(4)));
-typedef int int32x2_t __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
-constexpr int kSlice = 64;              // of the contraction at a time
 constexpr uint32_t kOOB = 0x80000000u;  // past every resource here
 constexpr int kXcdItems = 32, kGroupCols = 4;
 
 // An output tile: WM x WN waves of NI x NJ fragments of 32 rows by 32 columns.
 // A wave's columns are consecutive. Its fragments of rows lie WM fragments
 // apart, so that the rows that a slot's last tile has are shared out among the
-// waves, 32 at a time.
-template <int WM_, int NI_, int WN_, int NJ_>
+// waves, 32 at a time. SLICE values of the contraction at a time.
+template <int WM_, int NI_, int WN_, int NJ_, int SLICE>
 struct Shape {
+  static constexpr int kSlice = SLICE;
   static constexpr int WM = WM_, NI = NI_, WN = WN_, NJ = NJ_;
   static constexpr int kRowsM = WM * NI * 32, kColsN = WN * NJ * 32;
   static constexpr int kWaves = WM * WN, kThreads = kWaves * kWave;
@@ -43,8 +42,9 @@ struct Shape {
   static constexpr int kCopiesM = kVecM / kThreads, kCopiesN = kVecN / kThreads;  // a wave, 1 KB each
   static_assert(kVecM % kThreads == 0 && kVecN % kThreads == 0, "whole copies");
 };
-typedef Shape<2, 4, 4, 2> Large;  // 256 x 256: 64 KB a slice, one block a compute unit
-typedef Shape<1, 1, 4, 2> Small;  // 32 x 256: 36 KB a slice, two blocks a compute unit
+typedef Shape<2, 4, 4, 2, 64> Large;  // 256 x 256: 64 KB a slice, one block a compute unit
+typedef Shape<1, 1, 4, 2, 64> Small;  // rows' gradient, 32 x 256: 36 KB a slice, two blocks a compute unit
+typedef Shape<1, 4, 4, 2, 32> Half;   // weights' gradient, 128 x 256: 24 KB a slice, two blocks a compute unit
 static_assert(Large::kRowsM == kGradTileBf16 && Large::kColsN == kGradTileBf16, "the host's tile");
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, uint32_t bytes) {
@@ -135,7 +135,7 @@ struct Args {
   int S, max_rows, M, N, Kd;  // Kd: rows' gradient; M: weights'
   const uint16_t* h;
   void* out;
-  int accumulate, splits;  // weights'; splits > 1: out is [splits, S, M, N]
+  int splits;  // weights'; splits > 1: out is [splits, S, M, N]
 };
 
 // A tile: its slot, output rows and columns, and what is contracted.
@@ -187,7 +187,7 @@ struct Beside<true, SH> {
 // kept: slices of 32 values in four stages (3.2 ms), the last block's products over
 // the next slice's reads and copies (2.32 to 2.40), blocks out of step with each
 // other (2.36), non-temporal stores (2.43), tiles of several forms by columns too.
-template <int KIND, typename SH>
+template <int KIND, typename SH, bool ADD = false>
 __global__ __launch_bounds__(SH::kThreads, 2) void grouped_grad_kernel(Args p) {
   constexpr bool WEIGHTS = KIND >= kWeights;
   constexpr int BM = SH::kRowsM, BN = SH::kColsN, NI = SH::NI, NJ = SH::NJ;
@@ -236,11 +236,11 @@ __global__ __launch_bounds__(SH::kThreads, 2) void grouped_grad_kernel(Args p) {
       it.s = z / p.splits;
       it.split = z - it.s * p.splits;
       slot_rows(p.offsets, it.s, p.max_rows, &lo, &hi);
-      const int whole = ceil_div(hi - lo, kSlice);
-      const int each = ceil_div(whole, p.splits) * kSlice;  // rows of a split
+      const int whole = ceil_div(hi - lo, SH::kSlice);
+      const int each = ceil_div(whole, p.splits) * SH::kSlice;  // rows of a split
       it.row0 = uniform_i32(min(lo + it.split * each, hi));
       it.rows = uniform_i32(min(hi - it.row0, each));
-      it.nd = ceil_div(it.rows, kSlice);
+      it.nd = ceil_div(it.rows, SH::kSlice);
       it.m0 = mt * BM;
       it.n0 = nt * BN;
       it.m_next = p.m_side + (size_t)it.row0 * p.M;
@@ -253,7 +253,7 @@ __global__ __launch_bounds__(SH::kThreads, 2) void grouped_grad_kernel(Args p) {
       slot_rows(p.offsets, it.s, p.max_rows, &lo, &hi);
       it.row0 = uniform_i32(lo + (rt - beside.tp[it.s]) * BM);
       it.rows = uniform_i32(min(BM, hi - it.row0));
-      it.nd = ceil_div(p.Kd, kSlice);
+      it.nd = ceil_div(p.Kd, SH::kSlice);
       it.m0 = 0;
       it.n0 = nt * BN;
     }
@@ -283,12 +283,12 @@ __global__ __launch_bounds__(SH::kThreads, 2) void grouped_grad_kernel(Args p) {
     uint4* to_m = stage + wave * SH::kCopiesM * kWave;
     uint4* to_n = stage + SH::kVecM + wave * SH::kCopiesN * kWave;
     if constexpr (WEIGHTS) {
-      const uint32_t have = (uint32_t)max(0, min(it.left, kSlice));
+      const uint32_t have = (uint32_t)max(0, min(it.left, SH::kSlice));
       const __amdgpu_buffer_rsrc_t rm = uniform_rsrc(it.m_next, have * m_row);
       const __amdgpu_buffer_rsrc_t rn = uniform_rsrc(it.n_next, have * n_row);
-      it.m_next += (size_t)kSlice * p.M;
-      it.n_next += (size_t)kSlice * p.N;
-      it.left -= kSlice;
+      it.m_next += (size_t)SH::kSlice * p.M;
+      it.n_next += (size_t)SH::kSlice * p.N;
+      it.left -= SH::kSlice;
 #pragma unroll
       for (int i = 0; i < SH::kCopiesM; ++i)
         copy16(rm, to_m + i * kWave, it.m_off[i]);
@@ -301,18 +301,18 @@ __global__ __launch_bounds__(SH::kThreads, 2) void grouped_grad_kernel(Args p) {
           uniform_rsrc(p.m_side + (size_t)it.row0 * p.Kd, live ? (uint32_t)it.rows * m_row : 0u);
       const __amdgpu_buffer_rsrc_t rn =
           uniform_rsrc(p.n_side + (size_t)it.s * p.Kd * p.N, live ? (uint32_t)p.Kd * n_row : 0u);
-      const bool tail = (d + 1) * kSlice > p.Kd;  // chunks past Kd belong to the next row
+      const bool tail = (d + 1) * SH::kSlice > p.Kd;  // chunks past Kd belong to the next row
 #pragma unroll
       for (int i = 0; i < SH::kCopiesM; ++i) {
         const int v = (wave * SH::kCopiesM + i) * kWave + lane;
         const int ch = (v % 8) ^ ((v / 8 >> 1) & 7);
         copy16(rm, to_m + i * kWave,
-               tail && d * kSlice + ch * 8 >= p.Kd ? kOOB : it.m_off[i] + (uint32_t)d * (kSlice * 2));
+               tail && d * SH::kSlice + ch * 8 >= p.Kd ? kOOB : it.m_off[i] + (uint32_t)d * (SH::kSlice * 2));
       }
 #pragma unroll
       for (int i = 0; i < SH::kCopiesN; ++i)
         copy16(rn, to_n + i * kWave,
-               it.n_off[i] == kOOB ? kOOB : it.n_off[i] + (uint32_t)d * kSlice * n_row);
+               it.n_off[i] == kOOB ? kOOB : it.n_off[i] + (uint32_t)d * SH::kSlice * n_row);
     }
   };
 
@@ -320,7 +320,7 @@ __global__ __launch_bounds__(SH::kThreads, 2) void grouped_grad_kernel(Args p) {
   auto multiply = [&](const uint4* stage, auto& acc) {
     constexpr int ni = sizeof(acc[0]) / sizeof(floatx16);
 #pragma unroll
-    for (int kb = 0; kb < kSlice / 16; ++kb) {
+    for (int kb = 0; kb < SH::kSlice / 16; ++kb) {
       bf16x8_t fm[ni], fn[NJ];
 #pragma unroll
       for (int i = 0; i < ni; ++i) {
@@ -373,15 +373,51 @@ __global__ __launch_bounds__(SH::kThreads, 2) void grouped_grad_kernel(Args p) {
     const uint32_t bytes = (uint32_t)(WEIGHTS ? min(p.M - t.m0, BM) : t.rows) * cols * OB;
     const __amdgpu_buffer_rsrc_t rc = uniform_rsrc(static_cast<char*>(p.out) + first * OB, bytes);
     if constexpr (WEIGHTS) {
-      // 32 rows of 128 bytes at a time: 32 columns of f32, or 64 of bf16 if they are
-      // not added to what is there (that sum is f32: 32 columns again).
+      // 32 rows of 128 bytes at a time: 32 columns of f32, or 64 of bf16. What they are
+      // added to is read in the same lines, two such steps ahead (bf16, 60 slots of 2816
+      // x 2048 with 32 rows each: 271 us, read where it is added 454).
       uint4* out = beside.out[wave];
       auto place = [&](int r, int ch) { return out + r * 8 + (ch ^ ((r >> 1) & 7)); };
-      const int r8 = lane >> 3, c8 = lane & 7;  // row and chunk of a line of 128 bytes, read back
+      const int r8 = lane >> 3, c8 = lane & 7;  // row and chunk of a line of 128 bytes
+      constexpr int kParts = KIND == kWeights ? 1 : NJ, kCols = 128 / (int)OB;
+      auto at = [&](int i, int part, int l) {
+        const int col = t.n0 + wn * NJ * 32 + part * 32 + c8 * (kCols / 8);
+        const uint32_t row = (uint32_t)((i * SH::WM + wm) * 32 + l + r8);
+        return col < p.N ? (row * cols + (uint32_t)col) * OB : kOOB;
+      };
+      constexpr int kSteps = ni * kParts, kAhead = ADD ? 2 : 1;
+      int32x4_t prev[kAhead][4];
+      auto ask = [&](int q) {
 #pragma unroll
-      for (int i = 0; i < ni; ++i) {
-        const uint32_t row = (uint32_t)((i * SH::WM + wm) * 32 + r8);
-        if (KIND == kWeights && !p.accumulate) {
+        for (int l = 0; l < 4; ++l)
+          prev[q % kAhead][l] =
+              __builtin_amdgcn_raw_buffer_load_b128(rc, at(q / kParts, q % kParts, l * 8), 0, 0);
+      };
+      if constexpr (ADD) {
+#pragma unroll
+        for (int q = 0; q < kAhead && q < kSteps; ++q) ask(q);
+      }
+#pragma unroll
+      for (int q = 0; q < kSteps; ++q) {
+        const int i = q / kParts, part = q % kParts;
+        if constexpr (KIND == kWeights) {
+          if constexpr (ADD) {  // to the accumulators' lanes
+#pragma unroll
+            for (int l = 0; l < 4; ++l)
+              *place(l * 8 + r8, c8) = __builtin_bit_cast(uint4, prev[q % kAhead][l]);
+            wave_lds_fence();
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+#pragma unroll
+              for (int g = 0; g < 4; ++g) {
+                const uint2 v = reinterpret_cast<const uint2*>(place(lane & 31, j * 4 + g))[lane >> 5];
+                acc[j][i][4 * g] = bf16_to_f32(v.x & 0xffffu) + acc[j][i][4 * g];
+                acc[j][i][4 * g + 1] = bf16_to_f32(v.x >> 16) + acc[j][i][4 * g + 1];
+                acc[j][i][4 * g + 2] = bf16_to_f32(v.y & 0xffffu) + acc[j][i][4 * g + 2];
+                acc[j][i][4 * g + 3] = bf16_to_f32(v.y >> 16) + acc[j][i][4 * g + 3];
+              }
+            wave_lds_fence();
+          }
 #pragma unroll
           for (int j = 0; j < NJ; ++j)
 #pragma unroll
@@ -394,54 +430,27 @@ __global__ __launch_bounds__(SH::kThreads, 2) void grouped_grad_kernel(Args p) {
               }
               *place(lane & 31, j * 4 + g + (lane >> 5)) = join_packed(lo, hi);
             }
-          wave_lds_fence();
-          const int col = t.n0 + wn * NJ * 32 + c8 * 8;
-#pragma unroll
-          for (int l = 0; l < 32; l += 8) {
-            const uint32_t at = (row + l) * cols * 2u + (uint32_t)col * 2u;
-            __builtin_amdgcn_raw_buffer_store_b128(
-                __builtin_bit_cast(int32x4_t, *place(l + r8, c8)), rc, col < p.N ? at : kOOB, 0, 0);
-          }
-          wave_lds_fence();
-          continue;
-        }
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
+        } else {
 #pragma unroll
           for (int g = 0; g < 4; ++g)
             *place(lane & 31, 2 * g + (lane >> 5)) = make_uint4(
-                __float_as_uint(acc[j][i][4 * g]), __float_as_uint(acc[j][i][4 * g + 1]),
-                __float_as_uint(acc[j][i][4 * g + 2]), __float_as_uint(acc[j][i][4 * g + 3]));
-          wave_lds_fence();
-          const int col = t.n0 + (wn * NJ + j) * 32 + c8 * 4;
+                __float_as_uint(acc[part][i][4 * g]), __float_as_uint(acc[part][i][4 * g + 1]),
+                __float_as_uint(acc[part][i][4 * g + 2]), __float_as_uint(acc[part][i][4 * g + 3]));
+        }
+        wave_lds_fence();
 #pragma unroll
-          for (int l = 0; l < 32; l += 8) {
-            const uint4 q = *place(l + r8, c8);
-            float o[4] = {__uint_as_float(q.x), __uint_as_float(q.y), __uint_as_float(q.z),
-                          __uint_as_float(q.w)};
-            const uint32_t at = col < p.N ? ((row + l) * cols + (uint32_t)col) * OB : kOOB;
-            if constexpr (KIND == kWeightsF32) {
-              if (p.accumulate) {
-                const int32x4_t prev = __builtin_amdgcn_raw_buffer_load_b128(rc, at, 0, 0);
+        for (int l = 0; l < 4; ++l) {
+          int32x4_t o = __builtin_bit_cast(int32x4_t, *place(l * 8 + r8, c8));
+          if constexpr (ADD && KIND == kWeightsF32) {
 #pragma unroll
-                for (int v = 0; v < 4; ++v) o[v] = __int_as_float(prev[v]) + o[v];
-              }
-              __builtin_amdgcn_raw_buffer_store_b128(
-                  int32x4_t{__float_as_int(o[0]), __float_as_int(o[1]), __float_as_int(o[2]),
-                            __float_as_int(o[3])},
-                  rc, at, 0, 0);
-            } else {
-              const int32x2_t prev = __builtin_amdgcn_raw_buffer_load_b64(rc, at, 0, 0);
-              o[0] = bf16_to_f32((uint32_t)prev[0] & 0xffffu) + o[0];
-              o[1] = bf16_to_f32((uint32_t)prev[0] >> 16) + o[1];
-              o[2] = bf16_to_f32((uint32_t)prev[1] & 0xffffu) + o[2];
-              o[3] = bf16_to_f32((uint32_t)prev[1] >> 16) + o[3];
-              __builtin_amdgcn_raw_buffer_store_b64(
-                  int32x2_t{(int)pack_bf16x2(o[0], o[1]), (int)pack_bf16x2(o[2], o[3])}, rc, at, 0,
-                  0);
-            }
+            for (int v = 0; v < 4; ++v)
+              o[v] = __float_as_int(__int_as_float(prev[q % kAhead][l][v]) + __int_as_float(o[v]));
           }
-          wave_lds_fence();
+          __builtin_amdgcn_raw_buffer_store_b128(o, rc, at(i, part, l * 8), 0, 0);
+        }
+        wave_lds_fence();
+        if constexpr (ADD) {
+          if (q + kAhead < kSteps) ask(q + kAhead);
         }
       }
     } else {
@@ -595,6 +604,24 @@ bool take_small(int S, int max_rows, int N, int cus) {
   return 2 * tiles <= cus || (few && 20 * tiles < 19 * rounds * cus);
 }
 
+// Half tiles of the weights' gradient, whose two blocks a compute unit copy, multiply
+// and store independently of each other: where large tiles would leave the chip half
+// empty, or would be at most one round of short contractions, and for bf16 results of
+// few rows a slot, whose stores are what takes the time. Measured with large and half
+// tiles: 1 slot of 2048 x 1408 (48 large tiles), 1000 rows 25.2 and 19.2 us; 16 of
+// 1024 x 512 (128) at 32 rows 9.6 and 8.9, 1000 27.0 and 23.6; 20 of 1408 x 512 (240)
+// at 96 rows 11.8 and 10.4, f32 15.8 and 13.9, at 510 19.5 and 19.8, 1000 30.2 and
+// 32.4; 60 of 2816 x 2048 at 32 rows 145 and 135, 96 213 and 189, 192 262 and 257, f32
+// results at 32 rows 263 and 274, added to bf16 271 and 279; 64 of 2048 x 4096 at 32
+// rows 220 and 218, 96 326 and 317, 128 357 and 362, 510 669 and 722.
+constexpr int kHalfRows = 96, kHalfRoundRows = 256;
+
+bool take_half(int S, int splits, int max_rows, int M, int N, bool f32, bool add, int cus) {
+  const int64_t tiles = (int64_t)S * splits * ceil_div(M, Large::kRowsM) * ceil_div(N, Large::kColsN);
+  return 2 * tiles <= cus || (tiles <= cus && max_rows <= (int64_t)S * kHalfRoundRows) ||
+         (!f32 && !add && max_rows <= (int64_t)S * kHalfRows);
+}
+
 }  // namespace
 
 moe_status_t launch_gemm_backward_bf16(const void* dc, const int32_t* offsets, int S, int max_rows,
@@ -634,14 +661,24 @@ moe_status_t launch_gemm_weight_grad_bf16(const void* dc, const void* a, const i
   p.S = S; p.max_rows = max_rows; p.M = M; p.N = N;
   p.splits = grad_splits(S, max_rows, M, N, kGradTileBf16);
   p.out = p.splits > 1 ? ws : dw;
-  p.accumulate = p.splits > 1 ? 0 : accumulate;
-  const int64_t items = (int64_t)S * p.splits * ceil_div(M, kGradTileBf16) * ceil_div(N, kGradTileBf16);
-  const int cus = device_cu_count();
-  const int G = items < cus ? (int)items : cus;
-  if (dw_f32 || p.splits > 1)
-    grouped_grad_kernel<kWeightsF32, Large><<<G, Large::kThreads, 0, stream>>>(p);
-  else
-    grouped_grad_kernel<kWeights, Large><<<G, Large::kThreads, 0, stream>>>(p);
+  const bool f32 = dw_f32 || p.splits > 1, add = accumulate && p.splits == 1;
+  auto go = [&](auto kind, auto shape, auto adds) {
+    typedef decltype(shape) SH;
+    const int64_t items = (int64_t)S * p.splits * ceil_div(M, SH::kRowsM) * ceil_div(N, SH::kColsN);
+    const int64_t blocks = (int64_t)device_cu_count() * (SH::kWaves == 8 ? 1 : 2);
+    grouped_grad_kernel<decltype(kind)::value, SH, decltype(adds)::value>
+        <<<(int)std::min(items, blocks), SH::kThreads, 0, stream>>>(p);
+  };
+  auto by_add = [&](auto kind, auto shape) {
+    if (add) go(kind, shape, std::true_type{});
+    else go(kind, shape, std::false_type{});
+  };
+  auto by_kind = [&](auto shape) {
+    if (f32) by_add(std::integral_constant<int, kWeightsF32>{}, shape);
+    else by_add(std::integral_constant<int, kWeights>{}, shape);
+  };
+  if (take_half(S, p.splits, max_rows, M, N, f32, add, device_cu_count())) by_kind(Half{});
+  else by_kind(Large{});
   if (p.splits > 1)
     return launch_fold_splits(static_cast<const float*>(ws), p.splits, (size_t)S * M * N, dw, dw_f32,
                               accumulate, stream);

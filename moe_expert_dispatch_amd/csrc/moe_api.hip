@@ -861,7 +861,8 @@ moe_status_t moe_grouped_gemm_weight_grad(moe_dtype_t dt, const void* dc, const 
   if (st != MOE_OK) return st;
   if (!dtype_ok(dw_dt)) return MOE_ERR_UNSUPPORTED;
   const int tile = grad_tile(dt);
-  if (!tiles_fit((int64_t)S * grad_splits(S, max_rows, N, Kd, tile), N, Kd, tile))
+  // twice: tiles of half the rows
+  if (!tiles_fit((int64_t)S * grad_splits(S, max_rows, N, Kd, tile) * 2, N, Kd, tile))
     return MOE_ERR_UNSUPPORTED;
   if (!dw || !aligned16(dw)) return MOE_ERR_INVALID_ARG;
   if (max_rows > 0 && (!dc || !a || dw == dc || dw == a || !aligned16(dc) || !aligned16(a)))

@@ -279,7 +279,7 @@ def test_large_tiles_of_rows(dt, Kd):
 
 
 @pytest.mark.parametrize("dt", [B, F])
-@pytest.mark.parametrize("N,Kd", [(264, 520), (520, 264), (1032, 72)])
+@pytest.mark.parametrize("N,Kd", [(264, 520), (520, 264), (1032, 72), (1032, 520), (520, 1288)])
 def test_many_tiles_of_weights(dt, N, Kd):
     dev = device()
     announce(f"many tiles weights {dt} N={N} Kd={Kd}")
