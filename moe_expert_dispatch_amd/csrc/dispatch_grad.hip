@@ -11,7 +11,7 @@
 // wave, then over the waves in order. Each output is written by one thread.
 //
 // Bound by the bytes, 2 P + T rows and P + 2 T: 16384 tokens of 4096 bf16, top-8,
-// 432 us at 5.3 TB/s and 216 at 6.2; 4096 of 2048 58 us (4.9) and 30 (5.6); 64
+// 415 to 437 us at 5.2 to 5.5 TB/s and 202 at 6.6; 4096 of 2048 58 us (4.9) and 30 (5.6); 64
 // tokens of 2048, top-4, 4.4 us.
 #include <algorithm>
 
