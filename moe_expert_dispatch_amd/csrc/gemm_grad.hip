@@ -236,10 +236,9 @@ __global__ __launch_bounds__(SH::kThreads, 2) void grouped_grad_kernel(Args p) {
       it.s = z / p.splits;
       it.split = z - it.s * p.splits;
       slot_rows(p.offsets, it.s, p.max_rows, &lo, &hi);
-      const int whole = ceil_div(hi - lo, SH::kSlice);
-      const int each = ceil_div(whole, p.splits) * SH::kSlice;  // rows of a split
-      it.row0 = uniform_i32(min(lo + it.split * each, hi));
-      it.rows = uniform_i32(min(hi - it.row0, each));
+      split_rows(lo, hi, SH::kSlice, p.splits, it.split, &it.row0, &it.rows);
+      it.row0 = uniform_i32(it.row0);
+      it.rows = uniform_i32(it.rows);
       it.nd = ceil_div(it.rows, SH::kSlice);
       it.m0 = mt * BM;
       it.n0 = nt * BN;

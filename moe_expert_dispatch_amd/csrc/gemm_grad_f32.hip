@@ -77,9 +77,7 @@ __global__ __launch_bounds__(kThreads32) void grouped_grad_f32_kernel(Args32 p) 
       m0 = t / NT * TILE;
       n0 = t % NT * TILE;
       slot_rows(p.offsets, s, p.max_rows, &lo, &hi);
-      const int each = ceil_div(ceil_div(hi - lo, SLICE), p.splits) * SLICE;
-      row0 = min(lo + split * each, hi);
-      rows = min(hi - row0, each);
+      split_rows(lo, hi, SLICE, p.splits, split, &row0, &rows);
     } else {
       const int rt = item / NT;
       n0 = item % NT * TILE;

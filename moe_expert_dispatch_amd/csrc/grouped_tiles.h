@@ -5,6 +5,7 @@
 
 #include "common.h"
 #include "item_order.h"
+#include "split_rows.h"
 
 namespace moe {
 
