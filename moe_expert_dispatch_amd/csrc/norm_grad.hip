@@ -157,8 +157,9 @@ __global__ __launch_bounds__(L == 0 ? 1024 : kNormGroupThreads) void norm_backwa
 
 // The whole gradient of a few rows in one launch: blocks 0 .. T-1 give a row of
 // dx each, the others 64 columns of dgamma and dbeta each, for which they form
-// every row's mean and deviation once more, a wave to a row.
-constexpr int kFewRows = 64;
+// every row's mean and deviation once more, a wave to a row: time that grows with
+// the rows and their width (take_few).
+constexpr int kFewRows = 16;
 constexpr int kColumns = 64;  // of a block
 
 // The first vectors of a wave's row, and the row's first 8 values for all lanes.
@@ -293,16 +294,15 @@ __global__ __launch_bounds__(1024) void norm_backward_few_kernel(
   __shared__ double mean[kFewRows], dev[kFewRows];
   __shared__ float sums[2][16][kColumns];
   const int wave = threadIdx.x / kWave, waves = blockDim.x / kWave;
-  WaveRow<XT> next;
-  if (wave < T) next.ask(x + (size_t)wave * H, nvec);
-  for (int t = wave; t < T; t += waves) {
-    const WaveRow<XT> row = next;
-    if (t + waves < T) next.ask(x + (size_t)(t + waves) * H, nvec);
+  if (wave < T) {  // the block has a wave for each row
+    const XT* row = x + (size_t)wave * H;
+    WaveRow<XT> w;
+    w.ask(row, nvec);
     double m, r;
-    wave_row<XT, CENTRED>(x + (size_t)t * H, row, nvec, H, eps, &m, &r);
+    wave_row<XT, CENTRED>(row, w, nvec, H, eps, &m, &r);
     if (lane_id() == 0) {
-      mean[t] = m;
-      dev[t] = r;
+      mean[wave] = m;
+      dev[wave] = r;
     }
   }
   __syncthreads();
@@ -408,19 +408,24 @@ int norm_blocks(int T, int H) {
   return (int)((sets + each - 1) / each);
 }
 
-// Up to there one launch takes less than two with the host's time for the second
-// one, 4 us a call: 2 rows of 2048 on the GPU 4.2 us (two launches 6.5), 16 6.2
-// (6.5), 64 11.6 (6.8); issued one after the other 11, 11 and 11.7 us a call (15.5).
-// 64 rows of 4096 20 and 15.6.
+// Up to there one launch takes the GPU no longer than two, whose second one also
+// costs the host 4 us a call (11 and 15 us issued one after the other, 10 and 14 RMS).
+// One launch and two, us on the GPU, layer norm bf16: 12 rows of 512 to 2048 4.7 to
+// 5.2 and 6.0 to 6.2, of 8192 7.8 and 8.3; 16 rows of 512 5.4 and 6.1, of 2048 6.1 and
+// 6.2, of 4096 6.8 and 6.7, of 8192 8.4 and 8.5 (f32 9.7 and 9.1); above, with several
+// rows a wave, 24 of 512 6.3 and 5.9, of 2048 7.0 and 6.2, of 8192 10.1 and 8.8, 64 of
+// 2048 11.7 and 6.5. RMS 16 rows of 512 to 8192 4.1 to 6.1 and 5.6 to 6.8, 24 of 2048
+// 5.1 and 5.6, 64 8.1 and 5.7. Rows that one block of the other form holds need no
+// second launch there: 16 of 128 2.8 us (here 5.7), 4 of 512 3.1 (3.9).
 bool take_few(int T, int H) {
-  return T > 1 && T <= kFewRows && H <= 8192 && (int64_t)T * H <= 1 << 17;
+  return T <= kFewRows && H <= 8192 && norm_blocks(T, H) > 1;
 }
 
 template <typename XT, bool CENTRED>
 void launch_few(const void* dy, const void* x, const void* gamma, const void* dresidual, int T,
                 int H, float eps, void* dx, float* dgamma, float* dbeta, hipStream_t stream) {
-  // enough waves that each has a few rows for the columns' blocks
-  const int threads = std::max({256, ceil_div(H / 8, kWave) * kWave, std::min(16, T) * kWave});
+  // vectors of a row for its block, and a wave a row for the columns' blocks
+  const int threads = std::max({256, ceil_div(H / 8, kWave) * kWave, T * kWave});
   const int columns = dgamma != nullptr || dbeta != nullptr ? ceil_div(H, kColumns) : 0;
   auto go = [&](int rows, int cols) {
     if (rows + cols > 0)
