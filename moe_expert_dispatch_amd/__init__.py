@@ -189,13 +189,31 @@ def _dev(t: torch.Tensor, name: str, dtype=None, shape=None) -> torch.Tensor:
     return t
 
 
+_WIDE = 1 << 31
+
+
+def _fits(what: str, *sizes: int) -> None:
+    """Sizes that an int of the C ABI holds: ctypes keeps the low 32 bits of a larger one."""
+    if max(sizes) >= _WIDE:
+        raise ValueError(f"{what}: a size of {max(sizes)} does not fit 32 bits")
+
+
+def _size(what: str, *sizes: int) -> int:
+    """A workspace size."""
+    _fits(what, *sizes)
+    return int(getattr(_lib or lib(), what)(*sizes))
+
+
 def _empty(shape, dtype, like: torch.Tensor) -> torch.Tensor:
     return like.new_empty(shape, dtype=dtype)
 
 
 def _launch(what: str, like: torch.Tensor, others: Sequence[Optional[torch.Tensor]], *args) -> None:
     """Calls entry point `what` with args and the current stream of like's device, which is made
-    the current device for the call; the other tensors have to be on it too."""
+    the current device for the call; the other tensors have to be on it too. Rows that 32 bits do
+    not hold are like's (sizes that are not the callers look at)."""
+    if like.numel() >= _WIDE:
+        _fits(what, *(a for a, kind in zip(args, _SIGS[what][1]) if kind is _i))
     dev = like.get_device()
     for o in others:
         if o is not None and o.get_device() != dev:
@@ -258,7 +276,7 @@ def slot_map(ids: torch.Tensor, w: torch.Tensor, E_global: int, ep_size: int = 1
 
 
 def permute_workspace_size(T: int, K: int, S: int) -> int:
-    return int(lib().moe_permute_workspace_size(T, K, S))
+    return _size("moe_permute_workspace_size", T, K, S)
 
 
 def permute(x: torch.Tensor, slot: torch.Tensor, mask: torch.Tensor, S: int,
@@ -554,7 +572,7 @@ def layer_norm(x: torch.Tensor, gamma: torch.Tensor, beta: Optional[torch.Tensor
 
 
 def norm_backward_workspace_size(T: int, H: int) -> int:
-    return int(lib().moe_norm_backward_workspace_size(T, H))
+    return _size("moe_norm_backward_workspace_size", T, H)
 
 
 def _norm_backward(what, dy, x, gamma, eps, dresidual, dx, sums, ws):
@@ -620,7 +638,7 @@ def _router_inputs(logits, ids, token_mask) -> Tuple[int, int, int]:
 
 
 def balance_loss_workspace_size(T: int, E: int, K: int) -> int:
-    return int(lib().moe_balance_loss_workspace_size(T, E, K))
+    return _size("moe_balance_loss_workspace_size", T, E, K)
 
 
 def balance_loss(logits: torch.Tensor, ids: torch.Tensor, coef: float,
@@ -709,6 +727,7 @@ def _pair_rows(pair_row, K: int) -> int:
     _dev(pair_row, "pair_row", torch.int32)
     if K < 1 or pair_row.numel() % K != 0:
         raise ValueError("pair_row must hold T*K entries")
+    _fits("pair_row", pair_row.numel())
     return pair_row.numel() // K
 
 
@@ -804,6 +823,7 @@ def _slots(offsets) -> int:
     _dev(offsets, "offsets", torch.int32)
     if offsets.dim() != 1 or offsets.numel() < 2:
         raise ValueError("offsets must have S + 1 entries")
+    _fits("offsets", offsets.numel())
     return offsets.numel() - 1
 
 
@@ -859,7 +879,7 @@ def grouped_gemm_backward(op: int, dc: torch.Tensor, offsets: torch.Tensor, w: t
 
 def grouped_gemm_weight_grad_workspace_size(dtype: torch.dtype, S: int, rows: int, N: int, K: int
                                             ) -> int:
-    return int(lib().moe_grouped_gemm_weight_grad_workspace_size(_DT[dtype], S, rows, N, K))
+    return _size("moe_grouped_gemm_weight_grad_workspace_size", _DT[dtype], S, rows, N, K)
 
 
 def grouped_gemm_weight_grad(dc: torch.Tensor, a: torch.Tensor, offsets: torch.Tensor,
@@ -874,6 +894,7 @@ def grouped_gemm_weight_grad(dc: torch.Tensor, a: torch.Tensor, offsets: torch.T
     if dc.dim() != 2 or a.dim() != 2 or a.shape[0] != dc.shape[0]:
         raise ValueError("dc must be [rows, N] and a [rows, K]")
     rows, N, Kd = dc.shape[0], dc.shape[1], a.shape[1]
+    _fits("a", Kd)
     if dw is None:
         if accumulate:
             raise ValueError("accumulate needs dw")
@@ -917,6 +938,7 @@ class ForwardConfig:
         self.x_codes = bool(x_codes)  # FP8: x holds E4M3 codes at a1_scale (rms_norm's q)
 
     def c_struct(self) -> _Config:
+        _fits("ForwardConfig", self.T_max, self.T, self.H, self.I, self.E_global, self.K, self.S)
         return _Config(self.T_max, self.T, self.H, self.I, self.E_global, self.K,
                        int(self.renormalize), self.ep_size, self.ep_rank, self.S,
                        _DT[self.dtype], _DT[self.out_dtype], int(self.accumulate),
@@ -1007,7 +1029,7 @@ def forward(cfg: ForwardConfig, x: torch.Tensor, w_gate_up: torch.Tensor, w_down
 
 # ---------------------------------------------------------------- all-to-all
 def a2a_dispatch_workspace_size(T: int, ep_size: int, cap: int) -> int:
-    return int(lib().moe_a2a_dispatch_workspace_size(T, ep_size, cap))
+    return _size("moe_a2a_dispatch_workspace_size", T, ep_size, cap)
 
 
 def a2a_dispatch(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor, E_global: int,
