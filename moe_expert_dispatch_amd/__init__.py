@@ -158,10 +158,6 @@ def _check(code: int, what: str) -> None:
         raise RuntimeError(f"{what}: {status_str(code)}")
 
 
-def _stream() -> int:
-    return torch.cuda.current_stream().cuda_stream
-
-
 # The current stream's handle by device index: torch.cuda.current_stream() builds an object for
 # it, which took longer than a small kernel runs (about 2 us of a 12 us call).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
@@ -241,12 +237,11 @@ def route(logits: torch.Tensor, K: int, renormalize: bool,
     ids = _empty((T, K), torch.int32, logits) if ids is None else _dev(ids, "ids", torch.int32, (T, K))
     w = _empty((T, K), torch.float32, logits) if w is None else _dev(w, "w", torch.float32, (T, K))
     if num_groups:
-        _check(lib().moe_route_grouped(_ptr(logits), T, E, K, int(bool(renormalize)), num_groups,
-                                       topk_groups, _ptr(ids), _ptr(w), _stream()),
-               "moe_route_grouped")
+        _launch("moe_route_grouped", logits, (ids, w), _ptr(logits), T, E, K,
+                int(bool(renormalize)), num_groups, topk_groups, _ptr(ids), _ptr(w))
     else:
-        _check(lib().moe_route(_ptr(logits), T, E, K, int(bool(renormalize)), _ptr(ids),
-                               _ptr(w), _stream()), "moe_route")
+        _launch("moe_route", logits, (ids, w), _ptr(logits), T, E, K, int(bool(renormalize)),
+                _ptr(ids), _ptr(w))
     return ids, w
 
 
@@ -269,9 +264,8 @@ def slot_map(ids: torch.Tensor, w: torch.Tensor, E_global: int, ep_size: int = 1
     slot = _empty((T, K), torch.int32, ids)
     wm = _empty((T, K), torch.float32, ids)
     mask = _empty((T, K), torch.uint8, ids)
-    _check(lib().moe_slot_map(_ptr(ids), _ptr(w), T, K, E_global, ep_size, ep_rank,
-                              _ptr(rep_off), _ptr(rep_slots), S, _ptr(slot), _ptr(wm),
-                              _ptr(mask), _stream()), "moe_slot_map")
+    _launch("moe_slot_map", ids, (w, rep_off, rep_slots), _ptr(ids), _ptr(w), T, K, E_global,
+            ep_size, ep_rank, _ptr(rep_off), _ptr(rep_slots), S, _ptr(slot), _ptr(wm), _ptr(mask))
     return slot, wm, mask
 
 
@@ -304,16 +298,13 @@ def permute(x: torch.Tensor, slot: torch.Tensor, mask: torch.Tensor, S: int,
         _dev(pair_w, "pair_w", torch.float32, (T, K))
         if x_perm is None:
             raise ValueError("pair_w needs the row gather")
-        _check(lib().moe_permute_scaled(_ptr(x), _DT[x.dtype], T, H, K, _ptr(slot), _ptr(mask),
-                                        S, _ptr(pair_w), _ptr(offsets), _ptr(sorted_pairs),
-                                        _ptr(pair_row), _ptr(x_perm), _ptr(ws),
-                                        ws.numel() * ws.element_size(), _stream()),
-               "moe_permute_scaled")
+        _launch("moe_permute_scaled", x, (slot, mask, pair_w, ws), _ptr(x), _DT[x.dtype], T, H, K,
+                _ptr(slot), _ptr(mask), S, _ptr(pair_w), _ptr(offsets), _ptr(sorted_pairs),
+                _ptr(pair_row), _ptr(x_perm), _ptr(ws), ws.numel() * ws.element_size())
     else:
-        _check(lib().moe_permute(_ptr(x), _DT[x.dtype], T, H, K, _ptr(slot), _ptr(mask), S,
-                                 _ptr(offsets), _ptr(sorted_pairs), _ptr(pair_row),
-                                 _ptr(x_perm), _ptr(ws), ws.numel() * ws.element_size(),
-                                 _stream()), "moe_permute")
+        _launch("moe_permute", x, (slot, mask, ws), _ptr(x), _DT[x.dtype], T, H, K, _ptr(slot),
+                _ptr(mask), S, _ptr(offsets), _ptr(sorted_pairs), _ptr(pair_row), _ptr(x_perm),
+                _ptr(ws), ws.numel() * ws.element_size())
     return offsets, sorted_pairs, pair_row, x_perm
 
 
@@ -339,9 +330,9 @@ def permute_noalloc(x: torch.Tensor, slot: torch.Tensor, mask: torch.Tensor, S: 
     _dev(pair_row, "pair_row", torch.int32, (T * K,))
     if x_perm is not None:
         _dev(x_perm, "x_perm", x.dtype, (T * K, H))
-    _check(lib().moe_permute_noalloc(_ptr(x), _DT[x.dtype], T, H, K, _ptr(slot), _ptr(mask), S,
-                                     _ptr(offsets), _ptr(sorted_pairs), _ptr(pair_row),
-                                     _ptr(x_perm), _stream()), "moe_permute_noalloc")
+    _launch("moe_permute_noalloc", x, (slot, mask, offsets, sorted_pairs, pair_row, x_perm),
+            _ptr(x), _DT[x.dtype], T, H, K, _ptr(slot), _ptr(mask), S, _ptr(offsets),
+            _ptr(sorted_pairs), _ptr(pair_row), _ptr(x_perm))
     return offsets, sorted_pairs, pair_row, x_perm
 
 
@@ -373,8 +364,8 @@ def grouped_gemm(op: int, a: torch.Tensor, offsets: torch.Tensor, w: torch.Tenso
     else:
         raise ValueError("op must be GATE_UP_SWIGLU or DOWN")
     c = _empty((rows, N), a.dtype, a) if c is None else _dev(c, "c", a.dtype, (rows, N))
-    _check(lib().moe_grouped_gemm(op, _DT[a.dtype], _ptr(a), _ptr(offsets), S, rows, _ptr(w),
-                                  H, I, _ptr(c), _stream()), "moe_grouped_gemm")
+    _launch("moe_grouped_gemm", a, (offsets, w, c), op, _DT[a.dtype], _ptr(a), _ptr(offsets), S,
+            rows, _ptr(w), H, I, _ptr(c))
     return c
 
 
@@ -382,8 +373,7 @@ def quantize_fp8(x: torch.Tensor, scale: float, q: Optional[torch.Tensor] = None
     """moe_quantize_fp8: E4M3 codes (uint8, shape of x) of x (bf16 or f32) / scale."""
     _dev(x, "x", (torch.float32, torch.bfloat16))
     q = _empty(tuple(x.shape), torch.uint8, x) if q is None else _dev(q, "q", _CODES, x.shape)
-    _check(lib().moe_quantize_fp8(_ptr(x), _DT[x.dtype], x.numel(), float(scale), _ptr(q),
-                                  _stream()), "moe_quantize_fp8")
+    _launch("moe_quantize_fp8", x, (q,), _ptr(x), _DT[x.dtype], x.numel(), float(scale), _ptr(q))
     return q
 
 
@@ -419,9 +409,8 @@ def grouped_gemm_fp8(op: int, a: torch.Tensor, a_scale: float, offsets: torch.Te
         c = _empty(shape, torch.uint8 if op == GATE_UP_SWIGLU else torch.bfloat16, a)
     else:
         _dev(c, "c", cdt, shape)
-    _check(lib().moe_grouped_gemm_fp8(op, _ptr(a), float(a_scale), _ptr(offsets), S, rows,
-                                      _ptr(w), _ptr(w_scale), H, I, _ptr(c), float(c_scale),
-                                      _stream()), "moe_grouped_gemm_fp8")
+    _launch("moe_grouped_gemm_fp8", a, (offsets, w, w_scale, c), op, _ptr(a), float(a_scale),
+            _ptr(offsets), S, rows, _ptr(w), _ptr(w_scale), H, I, _ptr(c), float(c_scale))
     return c
 
 
@@ -699,6 +688,7 @@ def combine(y: torch.Tensor, pair_row: torch.Tensor, w_masked: Optional[torch.Te
             raise ValueError("pair_row / w_masked must hold T*K entries")
     if P % K != 0:
         raise ValueError("pair_row must hold T*K entries")
+    _fits("pair_row", P)
     T = P // K
     H = y.shape[1]
     if out is None:
@@ -712,13 +702,12 @@ def combine(y: torch.Tensor, pair_row: torch.Tensor, w_masked: Optional[torch.Te
         if shared is not None:
             _dev(shared, "shared", (torch.float32, torch.bfloat16), (T, H))
             sdt = _DT[shared.dtype]
-        _check(lib().moe_combine_shared(_ptr(y), _DT[y.dtype], _ptr(pair_row), _ptr(w_masked), T,
-                                        K, H, _ptr(shared), sdt, _ptr(out), _DT[out.dtype],
-                                        int(bool(accumulate)), _stream()), "moe_combine_shared")
+        _launch("moe_combine_shared", y, (pair_row, w_masked, shared, out), _ptr(y), _DT[y.dtype],
+                _ptr(pair_row), _ptr(w_masked), T, K, H, _ptr(shared), sdt, _ptr(out),
+                _DT[out.dtype], int(bool(accumulate)))
     else:
-        _check(lib().moe_combine(_ptr(y), _DT[y.dtype], _ptr(pair_row), _ptr(w_masked), T, K,
-                                 H, _ptr(out), _DT[out.dtype], int(bool(accumulate)),
-                                 _stream()), "moe_combine")
+        _launch("moe_combine", y, (pair_row, w_masked, out), _ptr(y), _DT[y.dtype], _ptr(pair_row),
+                _ptr(w_masked), T, K, H, _ptr(out), _DT[out.dtype], int(bool(accumulate)))
     return out
 
 
@@ -1046,6 +1035,7 @@ def a2a_dispatch(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor, 
         raise ValueError("x must be [T, H] with T matching topk_ids")
     H = x.shape[1]
     cap = T if cap is None else cap
+    _fits("cap", cap)
     offsets = _empty((ep_size + 1,), torch.int32, x)
     token_pos = _empty((T, ep_size), torch.int32, x)
     send_token = _empty((ep_size * cap,), torch.int32, x)
@@ -1055,11 +1045,10 @@ def a2a_dispatch(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor, 
     need = a2a_dispatch_workspace_size(T, ep_size, cap)
     if ws is None:
         ws = _empty((max(need, 1),), torch.uint8, x)
-    _check(lib().moe_a2a_dispatch(_ptr(x), _DT[x.dtype], T, H, K, _ptr(topk_ids), _ptr(topk_w),
-                                  E_global, ep_size, cap, _ptr(offsets), _ptr(token_pos),
-                                  _ptr(send_token), _ptr(send_x), _ptr(send_ids), _ptr(send_w),
-                                  _ptr(ws), ws.numel() * ws.element_size(), _stream()),
-           "moe_a2a_dispatch")
+    _launch("moe_a2a_dispatch", x, (topk_ids, topk_w, ws), _ptr(x), _DT[x.dtype], T, H, K,
+            _ptr(topk_ids), _ptr(topk_w), E_global, ep_size, cap, _ptr(offsets), _ptr(token_pos),
+            _ptr(send_token), _ptr(send_x), _ptr(send_ids), _ptr(send_w), _ptr(ws),
+            ws.numel() * ws.element_size())
     return offsets, token_pos, send_token, send_x, send_ids, send_w
 
 
@@ -1072,6 +1061,7 @@ def a2a_combine(partial: torch.Tensor, token_pos: torch.Tensor,
     T, ep_size = token_pos.shape
     H = partial.shape[1]
     out = _empty((T, H), out_dtype or partial.dtype, partial)
-    _check(lib().moe_a2a_combine(_ptr(partial), _DT[partial.dtype], _ptr(token_pos), T, ep_size,
-                                 H, _ptr(out), _DT[out.dtype], _stream()), "moe_a2a_combine")
+    _fits("token_pos", T)
+    _launch("moe_a2a_combine", partial, (token_pos,), _ptr(partial), _DT[partial.dtype],
+            _ptr(token_pos), T, ep_size, H, _ptr(out), _DT[out.dtype])
     return out
