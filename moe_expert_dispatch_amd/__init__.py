@@ -292,8 +292,7 @@ def permute(x: torch.Tensor, slot: torch.Tensor, mask: torch.Tensor, S: int,
     pair_row = _empty((T * K,), torch.int32, x)
     x_perm = _empty((T * K, H), x.dtype, x) if gather else None
     need = permute_workspace_size(T, K, S)
-    if ws is None:
-        ws = _empty((max(need, 1),), torch.uint8, x)
+    ws = _empty((max(need, 1),), torch.uint8, x) if ws is None else _dev(ws, "ws")
     if pair_w is not None:
         _dev(pair_w, "pair_w", torch.float32, (T, K))
         if x_perm is None:
@@ -642,6 +641,8 @@ def balance_loss(logits: torch.Tensor, ids: torch.Tensor, coef: float,
     loss = _empty((), torch.float32, logits)
     if ws is None:
         ws = _empty((max(balance_loss_workspace_size(T, E, K), 1),), torch.uint8, logits)
+    else:
+        _dev(ws, "ws")
     _launch("moe_balance_loss", logits, (ids, token_mask, ws), logits.data_ptr(),
             ids.data_ptr(), _ptr(token_mask), T, E, K, coef, counts.data_ptr(), prob.data_ptr(),
             loss.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
@@ -995,8 +996,7 @@ def forward(cfg: ForwardConfig, x: torch.Tensor, w_gate_up: torch.Tensor, w_down
         _dev(out, "out", cfg.out_dtype, (T, H))
     c = cfg.c_struct()
     need = _workspace_size(c)
-    if ws is None:
-        ws = _empty((need,), torch.uint8, x)
+    ws = _empty((need,), torch.uint8, x) if ws is None else _dev(ws, "ws")
     ev = _NO_EVENTS
     if events is not None:
         ev = (_p * NUM_EVENTS)()
@@ -1043,8 +1043,7 @@ def a2a_dispatch(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor, 
     send_ids = _empty((ep_size * cap, K), torch.int32, x)
     send_w = _empty((ep_size * cap, K), torch.float32, x)
     need = a2a_dispatch_workspace_size(T, ep_size, cap)
-    if ws is None:
-        ws = _empty((max(need, 1),), torch.uint8, x)
+    ws = _empty((max(need, 1),), torch.uint8, x) if ws is None else _dev(ws, "ws")
     _launch("moe_a2a_dispatch", x, (topk_ids, topk_w, ws), _ptr(x), _DT[x.dtype], T, H, K,
             _ptr(topk_ids), _ptr(topk_w), E_global, ep_size, cap, _ptr(offsets), _ptr(token_pos),
             _ptr(send_token), _ptr(send_x), _ptr(send_ids), _ptr(send_w), _ptr(ws),
