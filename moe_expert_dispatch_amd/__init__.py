@@ -190,8 +190,9 @@ _WIDE = 1 << 31
 
 def _fits(what: str, *sizes: int) -> None:
     """Sizes that an int of the C ABI holds: ctypes keeps the low 32 bits of a larger one."""
-    if max(sizes) >= _WIDE:
-        raise ValueError(f"{what}: a size of {max(sizes)} does not fit 32 bits")
+    most = max(sizes, default=0)
+    if most >= _WIDE:
+        raise ValueError(f"{what}: a size of {most} does not fit 32 bits")
 
 
 def _size(what: str, *sizes: int) -> int:

@@ -54,3 +54,16 @@ def test_workspace_sizes_and_the_layer():
         with pytest.raises(ValueError, match="32 bits"):
             call()
     assert moe.norm_backward_workspace_size(2 ** 31 - 1, 64) > 0
+
+
+def test_many_values_in_sizes_that_fit(unread):
+    """Tensors of 2^31 values and more, no size of which is: the entry point is called, also one without a size
+    among its own arguments."""
+    t = unread
+    rows = 2 ** 31 // 8 + 1
+    x, off = t(rows, 8), t(3, dt=torch.int32)
+    cfg = moe.ForwardConfig(rows, 8, 8, 4, 2, True, 4, torch.bfloat16)
+    for call in (lambda: moe.forward(cfg, x, t(4, 16, 8), t(4, 8, 8), t(rows, 4, dt=torch.float32)),
+                 lambda: moe.layer_norm(x, t(8)), lambda: moe.grouped_gemm_weight_grad(x, x, off)):
+        with pytest.raises(AssertionError, match="was called"):
+            call()
