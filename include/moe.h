@@ -539,7 +539,8 @@ moe_status_t moe_permute_backward(const void* dx_perm, moe_dtype_t dt, const int
  * the sums depend on shapes and the device's number of compute units alone. Buffers 16-byte
  * aligned, H % 8 == 0, I % 8 == 0; no output may overlap an input.
  *
- * moe_swiglu -- act[r, j] = silu(h[r, j]) * h[r, I + j], one rounding.
+ * moe_swiglu -- act[r, j] = silu(h[r, j]) * h[r, I + j], one rounding. Here and
+ * in the gradient a sigmoid under 2^-126 (a gate under -87.3) may count as 0.
  *
  * moe_grouped_gemm_backward -- the rows' gradient of a grouped product.
  * op == MOE_GEMM_GATE_UP_SWIGLU: dc [rows, 2I] (gradient of h, before the
