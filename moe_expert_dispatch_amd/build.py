@@ -50,12 +50,13 @@ COMPILE_FLAGS = [
 ]
 
 
-# The direct-to-LDS GEMM counts its own outstanding vector-memory operations
+# The direct-to-LDS GEMMs count their own outstanding vector-memory operations
 # (s_waitcnt vmcnt with fixed counts), so no compiler-generated memory access
-# may appear in it: register spills to scratch would shift every count. The
+# may appear in them: register spills to scratch would shift every count. The
 # build asks for the resource-usage remarks and rejects such a kernel (file ->
 # kernel-name fragment) if it uses scratch.
-NO_SCRATCH = {"gemm_mfma.hip": "grouped_gemm_dma_kernel"}
+NO_SCRATCH = {"gemm_mfma.hip": "grouped_gemm_dma_kernel",
+              "gemm_grad.hip": "grouped_grad_kernel"}
 _REMARK = "kernel-resource-usage"
 
 
