@@ -197,8 +197,9 @@ def _fits(what: str, *sizes: int) -> None:
 
 def _size(what: str, *sizes: int) -> int:
     """A workspace size."""
-    _fits(what, *sizes)
-    return int(getattr(_lib or lib(), what)(*sizes))
+    if max(sizes) >= _WIDE:
+        _fits(what, *sizes)
+    return getattr(_lib or lib(), what)(*sizes)
 
 
 def _empty(shape, dtype, like: torch.Tensor) -> torch.Tensor:
@@ -716,10 +717,12 @@ def combine(y: torch.Tensor, pair_row: torch.Tensor, w_masked: Optional[torch.Te
 # ---------------------------------------------------------------- the layer's training step
 def _pair_rows(pair_row, K: int) -> int:
     _dev(pair_row, "pair_row", torch.int32)
-    if K < 1 or pair_row.numel() % K != 0:
+    P = pair_row.numel()
+    if K < 1 or P % K != 0:
         raise ValueError("pair_row must hold T*K entries")
-    _fits("pair_row", pair_row.numel())
-    return pair_row.numel() // K
+    if P >= _WIDE:
+        _fits("pair_row", P)
+    return P // K
 
 
 def combine_backward(dout: torch.Tensor, y: Optional[torch.Tensor], pair_row: torch.Tensor,
@@ -812,10 +815,12 @@ def permute_backward(dx_perm: torch.Tensor, pair_row: torch.Tensor, K: int,
 
 def _slots(offsets) -> int:
     _dev(offsets, "offsets", torch.int32)
-    if offsets.dim() != 1 or offsets.numel() < 2:
+    n = offsets.numel()
+    if offsets.dim() != 1 or n < 2:
         raise ValueError("offsets must have S + 1 entries")
-    _fits("offsets", offsets.numel())
-    return offsets.numel() - 1
+    if n >= _WIDE:
+        _fits("offsets", n)
+    return n - 1
 
 
 def swiglu(h: torch.Tensor, offsets: torch.Tensor, act: Optional[torch.Tensor] = None
@@ -885,7 +890,8 @@ def grouped_gemm_weight_grad(dc: torch.Tensor, a: torch.Tensor, offsets: torch.T
     if dc.dim() != 2 or a.dim() != 2 or a.shape[0] != dc.shape[0]:
         raise ValueError("dc must be [rows, N] and a [rows, K]")
     rows, N, Kd = dc.shape[0], dc.shape[1], a.shape[1]
-    _fits("a", Kd)
+    if Kd >= _WIDE:
+        _fits("a", Kd)
     if dw is None:
         if accumulate:
             raise ValueError("accumulate needs dw")
