@@ -532,12 +532,15 @@ moe_status_t moe_permute_backward(const void* dx_perm, moe_dtype_t dt, const int
  *   dx_perm  = moe_grouped_gemm_backward(MOE_GEMM_GATE_UP_SWIGLU, dh, w_gate_up)
  *   dw_down  = moe_grouped_gemm_weight_grad(dy, act)
  *   dw_gate_up = moe_grouped_gemm_weight_grad(dh, x_perm)
- * Rows of slot s are offsets[s] .. offsets[s+1], as in moe_grouped_gemm;
- * rows before the first slot's and behind the last one's are neither read nor
- * written. max_rows < 2^31 - 1024. Products of bf16 values are exact, sums f32, one rounding at the end
+ * Rows of slot s are offsets[s] .. offsets[s+1], as in moe_grouped_gemm; rows
+ * before the first slot's and behind the last one's are neither read nor
+ * written. max_rows < 2^31 - 1024; tiles and splits are chosen by it, so a caller
+ * who knows how many rows are in use (offsets[S], a share of T*K) passes that
+ * number. Products of bf16 values are exact, sums f32, one rounding at the end
  * (dt MOE_DTYPE_F32: f32 products and sums on the matrix cores). The orders of
- * the sums depend on shapes and the device's number of compute units alone. Buffers 16-byte
- * aligned, H % 8 == 0, I % 8 == 0; no output may overlap an input.
+ * the sums depend on shapes, max_rows and the device's number of compute units
+ * alone. Buffers 16-byte aligned, H % 8 == 0, I % 8 == 0; no output may overlap an
+ * input.
  *
  * moe_swiglu -- act[r, j] = silu(h[r, j]) * h[r, I + j], one rounding. Here and
  * in the gradient a sigmoid under 2^-126 (a gate under -87.3) may count as 0.
@@ -556,7 +559,7 @@ moe_status_t moe_permute_backward(const void* dx_perm, moe_dtype_t dt, const int
  * dc [rows, N], a [rows, Kd] of dt; dw of dw_dt (f32 or bf16). Slots without
  * rows get zeros. accumulate != 0: dw += in f32, then the rounding. N and Kd
  * are multiples of 8 under 2^20. With few tiles and many rows a slot's rows are
- * split, the parts' f32 sums held in ws: 16-byte aligned, at least
+ * split (by max_rows), the parts' f32 sums held in ws: 16-byte aligned, at least
  * moe_grouped_gemm_weight_grad_workspace_size(..) bytes (often 0; then ws may
  * be NULL), contents ignored.
  */

@@ -883,7 +883,9 @@ def grouped_gemm_weight_grad(dc: torch.Tensor, a: torch.Tensor, offsets: torch.T
                              dw_dtype: torch.dtype = torch.float32, accumulate: bool = False,
                              ws: Optional[torch.Tensor] = None) -> torch.Tensor:
     """moe_grouped_gemm_weight_grad: dw [S, N, K] (f32 or bf16) of dc [rows, N] and a [rows, K],
-    zeros for slots without rows. accumulate adds to dw, which must be given."""
+    zeros for slots without rows. accumulate adds to dw, which must be given. Tiles and splits are
+    chosen by the buffers' rows: where the rows in use are known on the host, dc[:used] and
+    a[:used] take the forms that suit them."""
     _dev(dc, "dc", (torch.float32, torch.bfloat16))
     _dev(a, "a", dc.dtype)
     S = _slots(offsets)

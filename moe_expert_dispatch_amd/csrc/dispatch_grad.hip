@@ -237,8 +237,7 @@ __global__ __launch_bounds__(kThreads) void permute_backward_kernel(
 }
 
 // 32 bytes of each row a thread, whole waves, as many as hold the row up to 512
-// threads (2056 values of f32 are 257 vectors: 256 threads would go round twice);
-// K <= 4 keeps half the rows in flight.
+// threads (2056 values of f32 are 257 vectors: 256 threads would go round twice).
 int row_threads(int H, int vec) {
   return std::min(kThreads, std::max(kWave, ceil_div(H / 8, vec * kWave) * kWave));
 }

@@ -7,8 +7,8 @@
 //
 // Both contract an operand along the dimension in which it is not contiguous:
 // the rows' gradient the weights, the weights' gradient both. The tiles of
-// such operands lie in LDS as they do in memory, 64 rows of the contraction by
-// 256 columns, and reach the matrix cores through transposing LDS reads
+// such operands lie in LDS as they do in memory, 64 or 32 rows of the contraction
+// by the tile's 256, 128 or 32 columns, and reach the matrix cores through transposing LDS reads
 // (ds_read_b64_tr_b16: 16 lanes read 4 rows of 16 columns, each lane gets the
 // 4 rows of its column).
 #include <algorithm>
@@ -176,14 +176,20 @@ struct Beside<true, SH> {
 // completion of a wave's vector memory operations, stores among them, is reported
 // in the order of their execution). The rows' gradient passes its results through its part of
 // stage 1 and asks for the first slice alone, and for the second behind the
-// stores; the weights' gradient has room for them elsewhere, asks for two slices
-// and multiplies them while the stores drain (bf16, 64 slots of 2048 x 4096 with
-// 512 rows each 754 -> 735 us).
+// stores; as compiled that first slice is waited for before the first result is
+// written to LDS, so it does not overlap the stores, and through the SwiGLU each 8
+// rows' gates and ups are read, waited for and stored in turn. The weights' gradient
+// has room for its results elsewhere and asks for two slices: the first is multiplied
+// while the stores drain (bf16, 64 slots of 2048 x 4096 with 512 rows each 754 -> 735
+// us), before the second the compiler waits for half of them (a wait of its own, for
+// tiles of fewer rows, whose paths meet there).
 //
 // What bounds it, at 131072 rows of 2048 x 4096 in 64 slots, f32 results (2.2
-// TFLOP, 2.31 ms, 950 TFLOP/s): the products alone, without copies and stores, take
-// 1.70 ms, the copies alone 1.57 ms (11 TB/s into LDS), both 1.93, and the stores add
-// the rest: their 2.1 GB at the rate of plain writes are 0.5 ms. Measured and not
+// TFLOP, 2.21 to 2.29 ms, 960 to 995 TFLOP/s): the products alone, without copies and
+// stores, take 1.70 ms, the copies alone 1.57 ms (11 TB/s into LDS), both 1.93, and the
+// stores add the rest: their 2.1 GB at the rate of plain writes are 0.5 ms. Rows'
+// gradient of 32768 rows in 64 slots: gate/up (2048 x 4096) 575 us (956 TFLOP/s), down
+// through the SwiGLU (4096 x 1024) 391 (703). Measured and not
 // kept: slices of 32 values in four stages (3.2 ms), the last block's products over
 // the next slice's reads and copies (2.32 to 2.40), blocks out of step with each
 // other (2.36), non-temporal stores (2.43), tiles of several forms by columns too.

@@ -1,12 +1,15 @@
 // Gradients of the grouped products in f32 (gemm_grad.hip has the formulas and
-// the bf16 kernels), on the f32 matrix instructions: v_mfma_f32_32x32x2_f32
+// the bf16 kernels), on the f32 matrix instructions: v_mfma_f32_16x16x4_f32
 // multiplies and adds in f32, 256 operations a cycle and compute unit.
 //
-// Four waves in 2 x 2 on a tile of TILE x TILE, fragments of 16 x 16
-// (v_mfma_f32_16x16x4_f32), slices of SLICE contracted values through registers
-// into LDS. An operand that is contiguous along the contraction keeps its rows
+// Four waves in 2 x 2 on a tile of TILE x TILE, fragments of 16 x 16, slices of
+// SLICE contracted values through registers into LDS. An operand that is contiguous along the contraction keeps its rows
 // there, the others have the contraction outermost; the pitches put the 16 x 4
 // values that a wave reads at once on 64 banks.
+//
+// 114 to 120 TFLOP/s in either direction (16384 rows, 8 slots of 1024 x 1024 or 16 of
+// 2048 x 1024) of the 154 of a large library product: an LDS read of 4 bytes a lane
+// for each matrix instruction, and one stage with two barriers a slice.
 #include "grouped_tiles.h"
 #include "vec8.h"
 

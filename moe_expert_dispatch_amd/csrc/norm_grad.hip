@@ -12,10 +12,10 @@
 // Every sum's order depends on T and H alone.
 //
 // Bound by the bytes, two or three rows read and one written: 16384 rows of 4096
-// bf16 with dresidual 117 to 123 us (4.4 to 4.6 TB/s; the sums of the row before
-// and the loads of the next one overlap only as far as the registers of one block a
-// compute unit reach), 8192 rows of 5120 RMS, dresidual too, 65 (5.2), 777 rows of 2056
-// f32 without it 11.7; the second kernel 4 to 5 us.
+// bf16 with dresidual 124 to 128 us (4.2 to 4.3 TB/s; the sums of the row before
+// and the loads of the next one overlap only as far as the registers of two blocks
+// of eight waves a compute unit reach), 8192 rows of 5120 RMS, dresidual too, 67 (5.0),
+// 777 rows of 2056 f32 without it 11.2; the second kernel 4 to 5 us.
 #include <algorithm>
 
 #include "norm_row.h"
