@@ -935,9 +935,9 @@ class ForwardConfig:
         self.routing_on_input = bool(routing_on_input)
         self.gemm_blocks = int(gemm_blocks)  # 0: one persistent GEMM block per compute unit
         self.x_codes = bool(x_codes)  # FP8: x holds E4M3 codes at a1_scale (rms_norm's q)
+        _fits("ForwardConfig", self.T_max, T, H, I, E_global, K, S)
 
     def c_struct(self) -> _Config:
-        _fits("ForwardConfig", self.T_max, self.T, self.H, self.I, self.E_global, self.K, self.S)
         return _Config(self.T_max, self.T, self.H, self.I, self.E_global, self.K,
                        int(self.renormalize), self.ep_size, self.ep_rank, self.S,
                        _DT[self.dtype], _DT[self.out_dtype], int(self.accumulate),
@@ -976,6 +976,8 @@ def forward(cfg: ForwardConfig, x: torch.Tensor, w_gate_up: torch.Tensor, w_down
     cfg.dtype MXFP4: x is bf16, the weights are codes [S, 2I, H/2], [S, H, I/2]
     and scales [S, 2I, H/32], [S, H, I/32], all uint8 (quantize_mxfp4)."""
     T, H, I, S = cfg.T, cfg.H, cfg.I, cfg.S
+    if T >= _WIDE:  # set behind the constructor's look at it
+        _fits("forward", T)
     fp8, mx = cfg.dtype == FP8, cfg.dtype == MXFP4
     xdt = torch.bfloat16 if fp8 or mx else cfg.dtype
     wdt = _CODES if fp8 else torch.uint8 if mx else cfg.dtype

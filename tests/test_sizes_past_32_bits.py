@@ -50,9 +50,14 @@ def test_workspace_sizes_and_the_layer():
     for call in (lambda: moe.norm_backward_workspace_size(ROWS, 64), lambda: moe.permute_workspace_size(ROWS, 2, 4),
                  lambda: moe.balance_loss_workspace_size(ROWS, 8, 2), lambda: moe.a2a_dispatch_workspace_size(8, 2, ROWS),
                  lambda: moe.grouped_gemm_weight_grad_workspace_size(torch.bfloat16, 2, ROWS, 64, 64),
-                 lambda: moe.ForwardConfig(ROWS, 64, 64, 4, 2, True, 4, torch.bfloat16).c_struct()):
+                 lambda: moe.ForwardConfig(ROWS, 64, 64, 4, 2, True, 4, torch.bfloat16),
+                 lambda: moe.ForwardConfig(4, 64, 64, 4, 2, True, 4, torch.bfloat16, T_max=ROWS)):
         with pytest.raises(ValueError, match="32 bits"):
             call()
+    cfg = moe.ForwardConfig(4, 64, 64, 4, 2, True, 4, torch.bfloat16)
+    cfg.T = ROWS
+    with pytest.raises(ValueError, match="32 bits"):
+        moe.forward(cfg, None, None, None)
     assert moe.norm_backward_workspace_size(2 ** 31 - 1, 64) > 0
 
 
